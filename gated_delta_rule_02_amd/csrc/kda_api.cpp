@@ -435,6 +435,65 @@ int kda_output_norm_gate_fp8(const void* o, kda_dtype o_dtype, const void* gate,
     return hip_status(launch_norm_gate_fp8(a, static_cast<hipStream_t>(hip_stream)), "kda_output_norm_gate_fp8");
 }
 
+// ---------------------------------------------------------------- residual + RMSNorm
+static int add_rmsnorm_impl(const char* fn, const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual,
+                            int64_t residual_ld, void* residual_out, int64_t residual_out_ld,
+                            kda_dtype residual_dtype, const float* norm_weight, int64_t M, int64_t K, float eps,
+                            void* y, int64_t y_ld, kda_dtype y_dtype, float* scales, int64_t scale_ld, bool fp8,
+                            void* hip_stream)
+{
+    REQUIRE(M >= 0 && M <= 0x7fffffff && K >= 8, KDA_ERR_INVALID_ARG, "%s: M in [0, 2^31) and K >= 8 required", fn);
+    REQUIRE(valid_dtype(x_dtype) && valid_dtype(y_dtype) && (!residual || valid_dtype(residual_dtype)),
+            KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    REQUIRE(K % (fp8 ? 128 : 8) == 0, KDA_ERR_UNSUPPORTED, "%s: K must be a multiple of %d (got %lld)", fn,
+            fp8 ? 128 : 8, (long long)K);
+    REQUIRE(eps >= 0.0f, KDA_ERR_INVALID_ARG, "%s: eps must be >= 0 (got %g)", fn, (double)eps);
+    REQUIRE(residual || !residual_out, KDA_ERR_INVALID_ARG, "%s: residual_out needs a residual", fn);
+    if (M == 0) return ok();
+    REQUIRE(x && norm_weight && y && (!fp8 || scales), KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    for (int64_t ld : {x_ld, residual ? residual_ld : K, residual_out ? residual_out_ld : K, y_ld})
+        REQUIRE(ld >= K && ld % 8 == 0, KDA_ERR_INVALID_ARG, "%s: row strides must be >= K and multiples of 8", fn);
+    REQUIRE(!fp8 || scale_ld >= K / 128, KDA_ERR_INVALID_ARG, "%s: the scales' row stride must be >= K/128", fn);
+    for (const void* p : {x, residual, (const void*)residual_out, (const void*)norm_weight, fp8 ? nullptr : (const void*)y})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    REQUIRE(!fp8 || ((uintptr_t)y % 8 == 0 && (uintptr_t)scales % 4 == 0), KDA_ERR_INVALID_ARG,
+            "%s: codes must be 8-byte aligned", fn);
+    const size_t r = (size_t)(M - 1), er = esize(residual_dtype);
+    const Range rx = rng(x, (r * x_ld + K) * esize(x_dtype)), rw = rng(norm_weight, (size_t)K * 4);
+    const Range rr = rng(residual, residual ? (r * residual_ld + K) * er : 0);
+    const Range ro = rng(residual_out, residual_out ? (r * residual_out_ld + K) * er : 0);
+    const Range ry = rng(y, (r * y_ld + K) * (fp8 ? 1 : esize(y_dtype)));
+    const Range rs = rng(scales, fp8 ? (r * scale_ld + K / 128) * 4 : 0);
+    for (Range out : {ro, ry, rs})
+        REQUIRE(!overlap(out, rx) && !overlap(out, rw), KDA_ERR_INVALID_ARG, "%s: an output overlaps x or the weight", fn);
+    REQUIRE(!overlap(ry, rr) && !overlap(rs, rr) && !overlap(ry, ro) && !overlap(rs, ro) && !overlap(ry, rs),
+            KDA_ERR_INVALID_ARG, "%s: outputs overlap each other or the residual", fn);
+    REQUIRE(!overlap(ro, rr) || (residual == residual_out && residual_ld == residual_out_ld), KDA_ERR_INVALID_ARG,
+            "%s: residual and residual_out overlap without being the same rows", fn);
+    AddNormArgs a{x, x_ld, (DType)x_dtype, residual, residual_ld, residual_out, residual_out_ld,
+                  (DType)residual_dtype, norm_weight, M, K, eps, y, y_ld, (DType)y_dtype, fp8 ? scales : nullptr,
+                  scale_ld};
+    return hip_status(launch_add_norm(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_add_rmsnorm(const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual, int64_t residual_ld,
+                    void* residual_out, int64_t residual_out_ld, kda_dtype residual_dtype, const float* norm_weight,
+                    int64_t M, int64_t K, float eps, void* y, int64_t y_ld, kda_dtype y_dtype, void* hip_stream)
+{
+    return add_rmsnorm_impl("kda_add_rmsnorm", x, x_ld, x_dtype, residual, residual_ld, residual_out, residual_out_ld,
+                            residual_dtype, norm_weight, M, K, eps, y, y_ld, y_dtype, nullptr, 0, false, hip_stream);
+}
+
+int kda_add_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual, int64_t residual_ld,
+                        void* residual_out, int64_t residual_out_ld, kda_dtype residual_dtype,
+                        const float* norm_weight, int64_t M, int64_t K, float eps, uint8_t* codes, int64_t ldc,
+                        float* scales, int64_t ld_scale, void* hip_stream)
+{
+    return add_rmsnorm_impl("kda_add_rmsnorm_fp8", x, x_ld, x_dtype, residual, residual_ld, residual_out,
+                            residual_out_ld, residual_dtype, norm_weight, M, K, eps, codes, ldc, KDA_F32, scales,
+                            ld_scale, true, hip_stream);
+}
+
 // ---------------------------------------------------------------- prefill
 namespace {
 constexpr int64_t kChunk = 64;          // chunk of the bfloat16 forms
@@ -733,6 +792,42 @@ int kda_gemm(const void* A, int64_t lda, const void* B, int64_t ldb, void* C, in
             KDA_ERR_INVALID_ARG, "kda_gemm: C overlaps A or B");
     GemmArgs a{A, B, C, lda, ldb, ldc, M, N, K, (DType)c_dtype};
     return hip_status(launch_gemm(a, static_cast<hipStream_t>(hip_stream)), "kda_gemm");
+}
+
+int kda_gemm_epilogue(const void* A, int64_t lda, const void* B, int64_t ldb, const float* bias,
+                      kda_activation activation, const void* residual, int64_t residual_ld,
+                      kda_dtype residual_dtype, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                      kda_dtype ab_dtype, kda_dtype c_dtype, void* hip_stream)
+{
+    const char* fn = "kda_gemm_epilogue";
+    REQUIRE(valid_dtype(ab_dtype) && valid_dtype(c_dtype) && (!residual || valid_dtype(residual_dtype)),
+            KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    REQUIRE(ab_dtype == KDA_BF16, KDA_ERR_UNSUPPORTED, "%s: only bfloat16 A and B are supported", fn);
+    REQUIRE((int)activation >= KDA_ACT_NONE && (int)activation <= KDA_ACT_SIGMOID, KDA_ERR_INVALID_ARG,
+            "%s: unknown activation %d", fn, (int)activation);
+    REQUIRE(M >= 0 && N >= 1 && K >= 8 && M <= 0x7fffffff && N <= 0x7fffffff && K <= 0x7fffffff, KDA_ERR_INVALID_ARG,
+            "%s: bad sizes", fn);
+    REQUIRE(K % 8 == 0, KDA_ERR_UNSUPPORTED, "%s: K must be a multiple of 8", fn);
+    if (M == 0) return ok();
+    REQUIRE(A && B && C, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(lda >= K && ldb >= K && ldc >= N && lda % 8 == 0 && ldb % 8 == 0 && ldc % 4 == 0, KDA_ERR_INVALID_ARG,
+            "%s: lda, ldb >= K (multiples of 8), ldc >= N (multiple of 4)", fn);
+    REQUIRE(!residual || (residual_ld >= N && residual_ld % 4 == 0), KDA_ERR_INVALID_ARG,
+            "%s: residual_ld >= N (multiple of 4)", fn);
+    for (const void* p : {A, B, (const void*)C, residual, (const void*)bias})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const Range rc = rng(C, ((size_t)(M - 1) * ldc + N) * esize(c_dtype));
+    REQUIRE(!overlap(rc, rng(A, ((size_t)(M - 1) * lda + K) * 2)) &&
+                !overlap(rc, rng(B, ((size_t)(N - 1) * ldb + K) * 2)) && !overlap(rc, rng(bias, bias ? (size_t)N * 4 : 0)),
+            KDA_ERR_INVALID_ARG, "%s: C overlaps A, B or the bias", fn);
+    // the kernels address a tile's rows through 32-bit offsets
+    REQUIRE(256 * 2 * (std::max(lda, ldb) + K) < ((int64_t)1 << 31), KDA_ERR_UNSUPPORTED, "%s: row strides too large", fn);
+    const Range rr = rng(residual, residual ? ((size_t)(M - 1) * residual_ld + N) * esize(residual_dtype) : 0);
+    REQUIRE(!overlap(rc, rr) || (residual == C && residual_ld == ldc && residual_dtype == c_dtype), KDA_ERR_INVALID_ARG,
+            "%s: C and the residual overlap without being the same matrix", fn);
+    GemmArgs a{A, B, C, lda, ldb, ldc, M, N, K, (DType)c_dtype, bias, residual, residual_ld, (DType)residual_dtype,
+               (int)activation};
+    return hip_status(launch_gemm_epilogue(a, static_cast<hipStream_t>(hip_stream)), fn);
 }
 
 }  // extern "C"

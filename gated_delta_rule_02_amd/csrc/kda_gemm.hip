@@ -30,6 +30,125 @@
 namespace kda {
 namespace {
 
+// ------------------------------------------------------------ epilogue
+// act(v + bias) + residual in float32. The activation and the residual's type
+// are uniform over the launch: branches, not instantiations (a few scalar
+// instructions per output against the K products before them).
+__device__ __forceinline__ float activate(int act, float y)
+{
+    switch (act) {
+        case 1: return y < 0.0f ? 0.0f : y;  // keeps NaN
+        case 2: return siluf_(y);
+        case 3: return 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
+        case 4: return sigmoidf_(y);
+        default: return y;
+    }
+}
+__device__ __forceinline__ float epilogue1(const GemmArgs& a, int64_t row, int64_t col, float v)
+{
+    if (a.bias) v += a.bias[col];
+    v = activate(a.act, v);
+    if (a.res) {
+        const int64_t i = row * a.ldr + col;
+        v += a.r_dtype == F32 ? static_cast<const float*>(a.res)[i] : bf16_to_f32(static_cast<const bf16_t*>(a.res)[i]);
+    }
+    return v;
+}
+// columns col .. col + 3 (col a multiple of 4, all of them inside N)
+__device__ __forceinline__ f32x4 epilogue4(const GemmArgs& a, int64_t row, int64_t col, f32x4 v)
+{
+    if (a.bias) v += *reinterpret_cast<const f32x4*>(a.bias + col);
+    if (a.act) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]);
+    }
+    if (a.res) {
+        const int64_t i = row * a.ldr + col;
+        v += a.r_dtype == F32 ? ld4(static_cast<const float*>(a.res) + i) : ld4(static_cast<const bf16_t*>(a.res) + i);
+    }
+    return v;
+}
+
+// Columns col .. col + 3 of a row's residual (0 past N).
+__device__ __forceinline__ f32x4 residual4(const GemmArgs& a, int64_t row, int64_t col)
+{
+    f32x4 r = {0.f, 0.f, 0.f, 0.f};
+    if (row >= a.M) return r;
+    const int64_t i = row * a.ldr + col;
+    const float* pf = static_cast<const float*>(a.res) + i;
+    const bf16_t* pb = static_cast<const bf16_t*>(a.res) + i;
+    if (col + 3 < a.N) return a.r_dtype == F32 ? ld4(pf) : ld4(pb);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (col + e < a.N) r[e] = a.r_dtype == F32 ? pf[e] : bf16_to_f32(pb[e]);
+    return r;
+}
+
+// The epilogue of a wavefront's NI x NJ MFMA tiles (16 x 16, transposed: lane
+// (m16, q4) element e of acc[i][j] is C[16i + m16][16j + 4q4 + e]), 16 rows at a
+// time through LDS that the wavefront has to itself: a lane then holds four
+// consecutive columns of a row that 4 NJ neighbouring lanes cover, so residual
+// and C move in whole row segments, and the activation is a rolled loop (inlined
+// into the unrolled tiles it spilled the 256 x 256 kernel's accumulators: 1,040
+// registers, 15 times the time). The residual of the next 16 rows is
+// loaded before this one's are finished.
+template <int NJ> constexpr int kEpiFloats = 16 * (16 * NJ + 4);  // rows padded by 16 bytes
+template <typename TC, int NI, int NJ>
+__device__ __forceinline__ void tile_epilogue(const GemmArgs& a, const f32x4 (&acc)[NI][NJ], float* lds, int64_t row0,
+                                              int64_t col0)
+{
+    constexpr int kLd = 16 * NJ + 4, kLanes = 4 * NJ, kRows = 64 / kLanes;  // kRows rows a step, NJ steps
+    const int lane = threadIdx.x & 63, m16 = lane & 15, q4 = lane >> 4;
+    const int r0 = lane / kLanes, c0 = 4 * (lane % kLanes);
+    const int64_t col = col0 + c0;
+    f32x4 bias = {0.f, 0.f, 0.f, 0.f};
+    if (a.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < a.N) bias[e] = a.bias[col + e];
+    }
+    const bool whole = col + 3 < a.N;
+    TC* Cp = static_cast<TC*>(a.C);
+    f32x4 res[2][NJ];
+    auto load_res = [&](int i, f32x4* r) {
+#pragma unroll
+        for (int t = 0; t < NJ; ++t) r[t] = residual4(a, row0 + 16 * i + r0 + kRows * t, col);
+    };
+    if (a.res) load_res(0, res[0]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) *reinterpret_cast<f32x4*>(lds + m16 * kLd + 16 * j + 4 * q4) = acc[i][j];
+        if (a.res && i + 1 < NI) load_res(i + 1, res[(i + 1) & 1]);
+        if (a.act) {
+#pragma unroll 1
+            for (int t = 0; t < NJ; ++t) {
+                f32x4* p = reinterpret_cast<f32x4*>(lds + (r0 + kRows * t) * kLd + c0);
+                f32x4 v = *p + bias;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]);
+                *p = v;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NJ; ++t) {
+            const int64_t row = row0 + 16 * i + r0 + kRows * t;
+            f32x4 v = *reinterpret_cast<const f32x4*>(lds + (r0 + kRows * t) * kLd + c0);
+            if (!a.act) v += bias;
+            if (a.res) v += res[i & 1][t];
+            if (row >= a.M) continue;
+            TC* p = Cp + row * a.ldc + col;
+            if (whole) {
+                st4(p, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (col + e < a.N) st(p + e, v[e]);
+            }
+        }
+    }
+}
+
 constexpr int BM = 128, BN = 128, BK = 32;
 constexpr int LDS_LD = BK + 8;  // padded row (bf16 elements)
 constexpr int kThreads = 256;
@@ -132,7 +251,7 @@ __device__ __forceinline__ int swz(int r, int c) { return r * 128 + ((c ^ ((r >>
 // NJ: 16-column MFMA tiles per wavefront in N (8: the 256 x 256 tile; 2 or 4:
 // a 256 x 64 or 256 x 128 tile for the last N mod 256 columns, so that they
 // cost a fraction of a full tile instead of a whole one)
-template <typename TC, int NJ>
+template <typename TC, int NJ, bool EPI>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm256_kernel(GemmArgs a)
 {
     constexpr int TNW = 32 * NJ;         // columns of C per workgroup
@@ -235,6 +354,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
     // acc[i][j] holds C^T of tile (i, j): lane (m16, q4) element e is
     // C[row 16i + m16][column 16j + 4q4 + e]
+    if constexpr (EPI) {
+        tile_epilogue<TC, 8, NJ>(a, acc, reinterpret_cast<float*>(&smem[0][0][0]) + wave * kEpiFloats<NJ>, m0 + wm,
+                                 n0 + wn);
+        return;
+    }
     TC* Cp = static_cast<TC*>(a.C);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -356,6 +480,178 @@ __global__ __launch_bounds__(256) void gemm_narrow_kernel(GemmArgs a)
     }
 }
 
+// ------------------------------------------------------------ general tiles
+// The epilogue entry's kernel for every shape the 256 x 256 tiles do not suit:
+// TMx x TNx tiles of C by WM x WN wavefronts, K steps of 64 in STAGES LDS stages
+// filled by buffer-to-LDS copies STAGES - 1 steps ahead (the last of them may
+// still be in flight while a step computes: the wait counts copies). Rows past
+// M or N and, in the last step, chunks past K lie outside the descriptors and
+// read as zero.
+template <typename TC, int TMx, int TNx, int WM, int WN, int STAGES>
+__global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a)
+{
+    constexpr int kW = WM * WN, NI = TMx / WM / 16, NJ = TNx / WN / 16;
+    constexpr int kStage = (TMx + TNx) * 128;             // bytes of a stage: A rows, then B rows, 128 bytes each
+    constexpr int kCopies = (TMx + TNx) / 8 / kW;         // 1 KiB copies per wavefront and stage
+    static_assert((TMx + TNx) % (8 * kW) == 0 && TMx % 8 == 0, "whole copies");
+    static_assert(kW * kEpiFloats<NJ> * 4 <= STAGES * kStage, "the epilogue fits the stages");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[STAGES * kStage];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m16 = lane & 15, q4 = lane >> 4;
+    const int wm = (wave / WN) * (TMx / WM), wn = (wave % WN) * (TNx / WN);
+    const int tiles_m = (int)((a.M + TMx - 1) / TMx);
+    const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * TMx, n0 = (int64_t)(blockIdx.x / tiles_m) * TNx;
+    const int64_t rows_a = min<int64_t>(TMx, a.M - m0), rows_b = min<int64_t>(TNx, a.N - n0);
+    const rsrc_t ra = make_rsrc(static_cast<const bf16_t*>(a.A) + m0 * a.lda, ((rows_a - 1) * a.lda + a.K) * 2);
+    const rsrc_t rb = make_rsrc(static_cast<const bf16_t*>(a.B) + n0 * a.ldb, ((rows_b - 1) * a.ldb + a.K) * 2);
+
+    // copy i (of this wavefront's kCopies): rows 8i .. 8i + 7 of the stage, lane
+    // l its row l / 8, LDS chunk l % 8 (K chunk swizzled as the main kernel's)
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)&smem[0];
+    const int lrow = lane >> 3, lslot = lane & 7;
+    const int nk = (int)((a.K + 63) / 64);
+    auto copy = [&](int kt) {
+        const int st = kt % STAGES;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+            const int row = 8 * (wave * kCopies + c);  // of A rows then B rows; a copy lies in one of them
+            const bool isa = row < TMx;
+            const int r = (isa ? row : row - TMx) + lrow;
+            const int k = kt * 64 + (lslot ^ ((r >> 1) & 7)) * 8;
+            const int64_t ld = isa ? a.lda : a.ldb;
+            const int64_t rows = isa ? rows_a : rows_b;
+            const int off = k < a.K && r < rows ? (int)((r * ld + k) * 2) : (int)0x80000000;  // outside either descriptor
+            lds_void* dst = (lds_void*)(uintptr_t)(lds0 + st * kStage + row * 128);
+            if (isa) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, off, 0, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, off, 0, 0, 0);
+        }
+    };
+    f32x4 acc[NI][NJ];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int p = 0; p < STAGES - 1; ++p)
+        if (p < nk) copy(p);
+    for (int kt = 0; kt < nk; ++kt) {
+        // stage kt is there once at most the copies of the later steps under way are left
+        constexpr int kAhead = (STAGES - 2) * kCopies;
+        if (kt + STAGES - 1 <= nk) __builtin_amdgcn_s_waitcnt(0x0f70 | (kAhead & 15) | ((kAhead >> 4) << 14));
+        else __builtin_amdgcn_s_waitcnt(0x0f70);  // the last steps: everything
+        lds_barrier();  // everyone's copies of stage kt; every read of the stage refilled now is done
+        if (kt + STAGES - 1 < nk) copy(kt + STAGES - 1);
+        const uint8_t* sa = smem + (kt % STAGES) * kStage;
+        const uint8_t* sb = sa + TMx * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            u32x4_t fa[NI], fb[NJ];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) fa[i] = *reinterpret_cast<const u32x4_t*>(sa + swz(wm + 16 * i + m16, 4 * h + q4));
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) fb[j] = *reinterpret_cast<const u32x4_t*>(sb + swz(wn + 16 * j + m16, 4 * h + q4));
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[j]),
+                                                                        __builtin_bit_cast(bf16x8, fa[i]), acc[i][j], 0,
+                                                                        0, 0);
+        }
+    }
+    lds_barrier();  // every wavefront has read its last stage
+    tile_epilogue<TC, NI, NJ>(a, acc, reinterpret_cast<float*>(smem) + wave * kEpiFloats<NJ>, m0 + wm, n0 + wn);
+}
+
+// ------------------------------------------------------------ few rows
+// C for up to 16 MT rows of A (decode): bound by reading B once. A workgroup
+// takes 16 rows of B (columns of C) and its KS wavefronts a KS-th of K each;
+// fragments go straight from memory into registers, kFewDepth K steps of 64 (a
+// row's 128-byte line) in flight at a time, and the partial tiles are summed
+// in LDS. Rows past M and N repeat the last one (their results are dropped), so
+// every address is inside its matrix; the last, partial K step masks its lanes.
+constexpr int kFewDepth = 4;
+
+template <typename TC, int MT, int KS>
+__global__ __launch_bounds__(KS * 64) void gemm_few_kernel(GemmArgs a)
+{
+    __shared__ f32x4 part[KS - 1][MT][64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int m16 = lane & 15, q4 = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    // this wavefront's K range, in whole steps of 64
+    const int64_t steps = (a.K + 63) / 64;
+    const int64_t s0 = steps * wave / KS, s1 = steps * (wave + 1) / KS;
+    const bf16_t* pb = static_cast<const bf16_t*>(a.B) + min<int64_t>(n0 + m16, a.N - 1) * a.ldb + 8 * q4;
+    const bf16_t* pa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+        pa[i] = static_cast<const bf16_t*>(a.A) + min<int64_t>(16 * i + m16, a.M - 1) * a.lda + 8 * q4;
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto product = [&](const u32x4_t& fb, const u32x4_t& fa, f32x4& c) {
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, fa), c, 0,
+                                                    0, 0);
+    };
+    int64_t s = s0;
+    for (; s + kFewDepth <= s1 && (s + kFewDepth) * 64 <= a.K; s += kFewDepth) {
+        u32x4_t fb[kFewDepth][2], fa[kFewDepth][2][MT];
+#pragma unroll
+        for (int d = 0; d < kFewDepth; ++d)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t k = (s + d) * 64 + 32 * h;
+                fb[d][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(pb + k));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) fa[d][h][i] = ld16(pa[i] + k);
+            }
+#pragma unroll
+        for (int d = 0; d < kFewDepth; ++d)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) product(fb[d][h], fa[d][h][i], acc[i]);
+    }
+    for (; s < s1; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = s * 64 + 32 * h;
+            const bool in = k + 8 * q4 < a.K;  // K is a multiple of 8: a lane's 8 elements are in or out together
+            const u32x4_t zero = {0u, 0u, 0u, 0u};
+            const u32x4_t fb = in ? ld16(pb + k) : zero;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) product(fb, in ? ld16(pa[i] + k) : zero, acc[i]);
+        }
+    // acc[i] holds C^T: lane (m16, q4) element e is C[row 16i + m16][column n0 + 4 q4 + e]
+    if (wave > 0) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) part[wave - 1][i][lane] = acc[i];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+#pragma unroll
+    for (int w = 0; w < KS - 1; ++w)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] += part[w][i][lane];
+    TC* Cp = static_cast<TC*>(a.C);
+    const int64_t col = n0 + 4 * q4;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int64_t row = 16 * i + m16;
+        if (row >= a.M) continue;
+        if (col + 3 < a.N) {
+            st4(Cp + row * a.ldc + col, epilogue4(a, row, col, acc[i]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < a.N) st(Cp + row * a.ldc + col + e, epilogue1(a, row, col + e, acc[i][e]));
+        }
+    }
+}
+
 }  // namespace
 
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t s)
@@ -372,8 +668,8 @@ hipError_t launch_gemm(const GemmArgs& a, hipStream_t s)
         m.N = a.N / TN * TN;
         if (m.N > 0) {
             dim3 grid((unsigned)(tiles_m * (m.N / TN))), block(256);
-            if (a.c_dtype == F32) hipLaunchKernelGGL((gemm256_kernel<float, 8>), grid, block, 0, s, m);
-            else hipLaunchKernelGGL((gemm256_kernel<bf16_t, 8>), grid, block, 0, s, m);
+            if (a.c_dtype == F32) hipLaunchKernelGGL((gemm256_kernel<float, 8, false>), grid, block, 0, s, m);
+            else hipLaunchKernelGGL((gemm256_kernel<bf16_t, 8, false>), grid, block, 0, s, m);
         }
         GemmArgs r = a;
         r.N = a.N - m.N;
@@ -390,8 +686,8 @@ hipError_t launch_gemm(const GemmArgs& a, hipStream_t s)
             const int nj = r.N <= 64 ? 2 : (r.N <= 128 ? 4 : 8);
             dim3 grid((unsigned)(tiles_m * ((r.N + 32 * nj - 1) / (32 * nj)))), block(256);
 #define KDA_GEMM_REM(NJ)                                                                            \
-    if (a.c_dtype == F32) hipLaunchKernelGGL((gemm256_kernel<float, NJ>), grid, block, 0, s, r);     \
-    else hipLaunchKernelGGL((gemm256_kernel<bf16_t, NJ>), grid, block, 0, s, r);
+    if (a.c_dtype == F32) hipLaunchKernelGGL((gemm256_kernel<float, NJ, false>), grid, block, 0, s, r);     \
+    else hipLaunchKernelGGL((gemm256_kernel<bf16_t, NJ, false>), grid, block, 0, s, r);
             if (nj == 2) { KDA_GEMM_REM(2) }
             else if (nj == 4) { KDA_GEMM_REM(4) }
             else { KDA_GEMM_REM(8) }
@@ -405,6 +701,53 @@ hipError_t launch_gemm(const GemmArgs& a, hipStream_t s)
     else
         hipLaunchKernelGGL(gemm_kernel<bf16_t>, grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+namespace {
+
+template <typename TC>
+hipError_t launch_few(const GemmArgs& a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.N + 15) / 16)), block(256);
+    switch ((a.M + 15) / 16) {
+        case 1: hipLaunchKernelGGL((gemm_few_kernel<TC, 1, 4>), grid, block, 0, s, a); break;
+        case 2: hipLaunchKernelGGL((gemm_few_kernel<TC, 2, 4>), grid, block, 0, s, a); break;
+        case 3: hipLaunchKernelGGL((gemm_few_kernel<TC, 3, 4>), grid, block, 0, s, a); break;
+        default: hipLaunchKernelGGL((gemm_few_kernel<TC, 4, 4>), grid, block, 0, s, a); break;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+namespace {
+
+template <typename TC, int TMx, int TNx, int WM, int WN, int STAGES>
+hipError_t launch_tile(const GemmArgs& a, hipStream_t s)
+{
+    const int64_t tiles = ((a.M + TMx - 1) / TMx) * ((a.N + TNx - 1) / TNx);
+    hipLaunchKernelGGL((gemm_tile_kernel<TC, TMx, TNx, WM, WN, STAGES>), dim3((unsigned)tiles), dim3(WM * WN * 64), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename TC>
+hipError_t launch_epilogue(const GemmArgs& a, hipStream_t s)
+{
+    if (a.M <= 64) return launch_few<TC>(a, s);
+    auto tiles = [&](int64_t tm, int64_t tn) { return ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn); };
+    if (a.K % 64 == 0 && tiles(256, 256) >= 256) {
+        hipLaunchKernelGGL((gemm256_kernel<TC, 8, true>), dim3((unsigned)tiles(256, 256)), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    if (tiles(128, 128) >= 256) return launch_tile<TC, 128, 128, 2, 2, 3>(a, s);
+    return launch_tile<TC, 64, 64, 2, 2, 4>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_epilogue(const GemmArgs& a, hipStream_t s)
+{
+    return a.c_dtype == F32 ? launch_epilogue<float>(a, s) : launch_epilogue<bf16_t>(a, s);
 }
 
 }  // namespace kda

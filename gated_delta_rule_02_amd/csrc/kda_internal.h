@@ -165,12 +165,41 @@ struct NormGateFp8Args {
 };
 hipError_t launch_norm_gate_fp8(const NormGateFp8Args& a, hipStream_t s);
 
+// h = x + res (res may be null); res_out = h (null: not stored); y = RMSNorm(h) w,
+// stored in y_dtype, or, with scales set, as E4M3 codes with one scale per 128 columns
+struct AddNormArgs {
+    const void* x;
+    int64_t x_ld;
+    DType x_dtype;
+    const void* res;
+    int64_t res_ld;
+    void* res_out;
+    int64_t res_out_ld;
+    DType res_dtype;
+    const float* w;
+    int64_t M, K;
+    float eps;
+    void* y;
+    int64_t y_ld;
+    DType y_dtype;
+    float* scales;
+    int64_t scale_ld;
+};
+hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t s);
+
 struct GemmArgs {
     const void *A, *B;
     void* C;
     int64_t lda, ldb, ldc, M, N, K;
     DType c_dtype;
+    // the epilogue of launch_gemm_epilogue: C = act(A B^T + bias) + res
+    const float* bias = nullptr;  // [N] or null
+    const void* res = nullptr;    // [M, N], row stride ldr, or null; may be C itself
+    int64_t ldr = 0;
+    DType r_dtype = F32;
+    int act = 0;                  // a kda_activation
 };
 hipError_t launch_gemm(const GemmArgs& a, hipStream_t s);
+hipError_t launch_gemm_epilogue(const GemmArgs& a, hipStream_t s);
 
 }  // namespace kda

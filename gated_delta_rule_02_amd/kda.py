@@ -17,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
 
 KDA_F32, KDA_BF16 = 0, 1
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_WORKSPACE, KDA_ERR_HIP = 0, -1, -2, -3, -4
 
 _P = ctypes.c_void_p
@@ -49,6 +50,9 @@ _SIGS = {
     "kda_gate_prologue": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _F, _I, _P, _P, _I, _P]),
     "kda_output_norm_gate": (_I, [_P, _I, _P, _I64, _P, _I64, _I, _I, _F, _P, _I, _P]),
     "kda_gemm": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
+    "kda_add_rmsnorm": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _I64, _I, _P]),
+    "kda_add_rmsnorm_fp8": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _I64, _P, _I64, _P]),
+    "kda_gemm_epilogue": (_I, [_P, _I64, _P, _I64, _P, _I, _P, _I64, _I, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
     "kda_state_bytes": (_SZ, [_I, _I, _I, _I]),
     "kda_conv_state_bytes": (_SZ, [_I, _I, _I, _I]),
     "kda_last_error": (ctypes.c_char_p, []),
@@ -453,6 +457,94 @@ def kda_output_norm_gate_fp8(o, gate, norm_weight, y_codes, y_scales, eps=1e-6, 
     _call("kda_output_norm_gate_fp8", _ptr(o), _dt(o), _ptr(gate), gate.stride(0), _dt(gate), _ptr(norm_weight),
           T, H, dv, eps, _ptr(y_codes), _ptr(y_scales), _stream(stream))
     return y_codes, y_scales
+
+
+def _rows(name, t, shape, dtype=None):
+    """Checks a row-strided 2-D tensor: shape, contiguous rows, dtype (if given)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError("%s rows must be contiguous" % name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    return t
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor (a single row's stride means nothing: its width, rounded up)."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+
+
+def _call_on(name, tensors, stream, *args):
+    """_call with the tensors' device current and, without a stream, that
+    device's current stream; tensors on several devices are refused."""
+    device = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("%s: tensors on several devices (%s, %s)" % (name, device, t.device))
+    if device.index == torch.cuda.current_device():
+        return _call(name, *args, _stream(stream))
+    with torch.cuda.device(device):
+        return _call(name, *args, _stream(stream))
+
+
+def _add_rmsnorm_args(x, norm_weight, residual, residual_out):
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    _rows("x", x, x.shape)
+    _rows("residual", residual, x.shape)
+    _rows("residual_out", residual_out, x.shape, None if residual is None else residual.dtype)
+    if norm_weight.dtype != torch.float32 or tuple(norm_weight.shape) != (x.shape[1],):
+        raise TypeError("norm_weight must be float32 [K]")
+    r, ro = residual, residual_out
+    return (_ptr(x), _ld(x), _dt(x), _ptr(r), 0 if r is None else _ld(r), _ptr(ro), 0 if ro is None else _ld(ro),
+            KDA_F32 if r is None else _dt(r), _ptr(_dense(norm_weight, "norm_weight")), x.shape[0], x.shape[1])
+
+
+def kda_add_rmsnorm(x, norm_weight, y, residual=None, residual_out=None, eps=1e-6, stream=None):
+    """y = RMSNorm(x + residual) * norm_weight, residual_out = x + residual. x, residual,
+    y [M, K] (row strides allowed; float32 or bfloat16 each), norm_weight float32
+    [K]; residual_out (the residual's dtype) may be residual itself."""
+    args = _add_rmsnorm_args(x, norm_weight, residual, residual_out)
+    _rows("y", y, x.shape)
+    _call_on("kda_add_rmsnorm", (x, norm_weight, y, residual, residual_out), stream, *args, eps, _ptr(y), _ld(y), _dt(y))
+    return y
+
+
+def kda_add_rmsnorm_fp8(x, norm_weight, codes, scales, residual=None, residual_out=None, eps=1e-6, stream=None):
+    """kda_add_rmsnorm with y quantized as kda_quantize_fp8 does: codes uint8
+    [M, K] (E4M3), scales float32 [M, K/128]; K a multiple of 128."""
+    args = _add_rmsnorm_args(x, norm_weight, residual, residual_out)
+    _rows("codes", codes, x.shape, torch.uint8)
+    _rows("scales", scales, (x.shape[0], x.shape[1] // 128), torch.float32)
+    _call_on("kda_add_rmsnorm_fp8", (x, norm_weight, codes, scales, residual, residual_out), stream, *args, eps,
+             _ptr(codes), _ld(codes), _ptr(scales), _ld(scales))
+    return codes, scales
+
+
+def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stream=None):
+    """C[M,N] = act(A[M,K] B[N,K]^T + bias) + residual (bfloat16 A and B; C and the
+    residual float32 or bfloat16; rows may be strided). bias float32 [N];
+    activation one of ACTIVATIONS; residual may be C itself."""
+    if A.dim() != 2 or B.dim() != 2:
+        raise ValueError("A must be [M, K] and B [N, K]")
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s (got %r)" % (sorted(ACTIVATIONS), activation))
+    M, K = A.shape
+    N = B.shape[0]
+    _rows("A", A, (M, K))
+    _rows("B", B, (N, K), A.dtype)
+    _rows("C", C, (M, N))
+    _rows("residual", residual, (M, N))
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)):
+        raise TypeError("bias must be float32 [N]")
+    r = residual
+    _call_on("kda_gemm_epilogue", (A, B, C, bias, residual), stream, _ptr(A), _ld(A), _ptr(B), _ld(B),
+             _ptr(_dense(bias, "bias")), ACTIVATIONS[activation], _ptr(r), 0 if r is None else _ld(r),
+             KDA_F32 if r is None else _dt(r), _ptr(C), _ld(C), M, N, K, _dt(A), _dt(C))
+    return C
 
 
 def kda_state_bytes(H, dk=128, dv=128, dtype=KDA_F32):

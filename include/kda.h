@@ -530,6 +530,70 @@ int kda_gemm(const void* A, int64_t lda, const void* B, int64_t ldb, void* C, in
              void* hip_stream);
 
 /* ------------------------------------------------------------------------
+ * kda_add_rmsnorm -- residual addition and RMSNorm in front of a block.
+ *
+ *   h = x + residual,  residual_out = h,  y = h / sqrt(mean(h^2) + eps) * norm_weight
+ * per row of K columns. y is formed from the float32 h and every output is
+ * rounded once, when stored. A pre-norm block takes y into its projections and
+ * carries residual_out on.
+ *
+ * x             [M, K] x_dtype, row stride x_ld: the previous block's output.
+ * residual      [M, K] residual_dtype, row stride residual_ld, or NULL (h = x).
+ * residual_out  [M, K] residual_dtype, row stride residual_out_ld, or NULL (not
+ *               stored); needs a residual. It may be residual itself (same
+ *               pointer and stride: updated in place).
+ * norm_weight   float32 [K].
+ * y             [M, K] y_dtype, row stride y_ld.
+ * K and the row strides are multiples of 8; M = 0 does nothing; eps >= 0. No
+ * output may overlap another tensor, but for the in-place residual.
+ * ---------------------------------------------------------------------- */
+int kda_add_rmsnorm(const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual, int64_t residual_ld,
+                    void* residual_out, int64_t residual_out_ld, kda_dtype residual_dtype, const float* norm_weight,
+                    int64_t M, int64_t K, float eps, void* y, int64_t y_ld, kda_dtype y_dtype, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_add_rmsnorm_fp8 -- kda_add_rmsnorm with y quantized to block FP8.
+ *
+ * The input of the W8A8 projections in one pass: y as above (float32, not
+ * rounded in between), then per row and group of 128 columns scale =
+ * max|y| / 448 (1 where that is zero), code = E4M3 of y / scale, nearest, ties to
+ * even: the format of kda_quantize_fp8, taken by kda_gemm_fp8. A NaN gives NaN
+ * codes (its group's scale is 1).
+ *
+ * codes   uint8 [M, K], row stride ldc (a multiple of 8), 8-byte aligned.
+ * scales  float32 [M, K/128], row stride ld_scale.
+ * Everything else as kda_add_rmsnorm; K must be a multiple of 128.
+ * ---------------------------------------------------------------------- */
+int kda_add_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual, int64_t residual_ld,
+                        void* residual_out, int64_t residual_out_ld, kda_dtype residual_dtype,
+                        const float* norm_weight, int64_t M, int64_t K, float eps, uint8_t* codes, int64_t ldc,
+                        float* scales, int64_t ld_scale, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_gemm_epilogue -- kda_gemm with bias, activation and residual.
+ *
+ *   C[M, N] = act(A[M, K] * B[N, K]^T + bias) + residual
+ * The product, the bias, the activation and the residual are taken in float32;
+ * C is rounded once, when stored. Every M takes one launch that reads B once
+ * for few rows (decode), or tiles of the matrix cores.
+ *
+ * A, B, C    as kda_gemm (ab_dtype = KDA_BF16; C in c_dtype).
+ * bias       float32 [N] or NULL.
+ * activation a kda_activation: SiLU y sigmoid(y), GELU y Phi(y) (Phi the normal
+ *            distribution function, not its tanh approximation).
+ * residual   [M, N] residual_dtype, row stride residual_ld (a multiple of 4),
+ *            16-byte aligned, or NULL. It may be C itself (same pointer, stride
+ *            and dtype: accumulated in place); any other overlap is rejected.
+ * M = 0 does nothing. Sizes, strides and alignment as kda_gemm.
+ * ---------------------------------------------------------------------- */
+typedef enum { KDA_ACT_NONE = 0, KDA_ACT_RELU = 1, KDA_ACT_SILU = 2, KDA_ACT_GELU = 3, KDA_ACT_SIGMOID = 4 } kda_activation;
+
+int kda_gemm_epilogue(const void* A, int64_t lda, const void* B, int64_t ldb, const float* bias,
+                      kda_activation activation, const void* residual, int64_t residual_ld,
+                      kda_dtype residual_dtype, void* C, int64_t ldc, int64_t M, int64_t N, int64_t K,
+                      kda_dtype ab_dtype, kda_dtype c_dtype, void* hip_stream);
+
+/* ------------------------------------------------------------------------
  * Size helpers. kda_state_bytes(64, 128, 128, KDA_F32) = 4,194,304: one
  * [64,128,128] FP32 matrix per layer, 252 MiB over 63 layers (flozi.net page,
  * section "KDA replaces a token list with a recurrent matrix").

@@ -1,0 +1,94 @@
+"""Host-side validation of the block's entry points (residual + RMSNorm, GEMM
+with an epilogue): every rejected call below is refused before anything reaches
+the device, with the documented status. No GPU is needed."""
+import pytest
+import torch
+
+from gated_delta_rule_02_amd import kda as K
+from tests.test_abi_cpu import call, fake
+
+INVALID, UNSUPPORTED = K.KDA_ERR_INVALID_ARG, K.KDA_ERR_UNSUPPORTED
+
+
+def norm(fp8=False, **over):
+    a = dict(x=fake(1), x_ld=512, xd=K.KDA_BF16, r=fake(2), r_ld=512, ro=fake(3), ro_ld=512, rd=K.KDA_BF16, w=fake(4),
+             M=7, K=512, eps=1e-6, y=fake(5), y_ld=512, yd=K.KDA_BF16, s=fake(6), s_ld=4)
+    a.update(over)
+    tail = (a["y"], a["y_ld"], a["s"], a["s_ld"]) if fp8 else (a["y"], a["y_ld"], a["yd"])
+    return call("kda_add_rmsnorm_fp8" if fp8 else "kda_add_rmsnorm", a["x"], a["x_ld"], a["xd"], a["r"], a["r_ld"],
+                a["ro"], a["ro_ld"], a["rd"], a["w"], a["M"], a["K"], a["eps"], *tail, None)[0]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_add_rmsnorm_validation(fp8):
+    assert norm(fp8, M=0) == K.KDA_OK  # nothing to do
+    for name in ("x", "w", "y"):
+        assert norm(fp8, **{name: None}) == INVALID, name
+    assert norm(fp8, M=-1) == INVALID and norm(fp8, M=1 << 31) == INVALID
+    assert norm(fp8, K=0) == INVALID and norm(fp8, K=12) == UNSUPPORTED
+    for name in ("x_ld", "r_ld", "ro_ld", "y_ld"):
+        assert norm(fp8, **{name: 504}) == INVALID, name
+        assert norm(fp8, **{name: 516}) == INVALID, name
+    assert norm(fp8, eps=-1.0) == INVALID and norm(fp8, eps=float("nan")) == INVALID
+    assert norm(fp8, xd=5) == INVALID and norm(fp8, rd=-1) == INVALID
+    assert norm(fp8, r=None) == INVALID  # residual_out without a residual
+    for name in ("x", "r", "ro", "w"):
+        assert norm(fp8, **{name: fake(7) + 8}) == INVALID, name
+    # outputs over inputs, or over each other
+    assert norm(fp8, y=fake(1)) == INVALID and norm(fp8, y=fake(2) + 64) == INVALID and norm(fp8, y=fake(3)) == INVALID
+    assert norm(fp8, ro=fake(1)) == INVALID and norm(fp8, ro=fake(4)) == INVALID
+    assert norm(fp8, ro=fake(2) + 16) == INVALID              # shifted in place
+    assert norm(fp8, ro=fake(2), ro_ld=520) == INVALID        # in place with another stride
+    if fp8:
+        assert norm(fp8, K=520, x_ld=520, r_ld=520, ro_ld=520, y_ld=520) == UNSUPPORTED
+        assert norm(fp8, s=None) == INVALID and norm(fp8, s_ld=3) == INVALID
+        assert norm(fp8, s=fake(5)) == INVALID and norm(fp8, s=fake(1)) == INVALID
+        assert norm(fp8, y=fake(5) + 4) == INVALID
+    else:
+        assert norm(fp8, yd=3) == INVALID and norm(fp8, y=fake(5) + 8) == INVALID
+
+
+def gemm(**over):
+    a = dict(A=fake(1), lda=256, B=fake(2), ldb=256, bias=fake(3), act=2, r=fake(4), ldr=100, rd=K.KDA_F32, C=fake(5),
+             ldc=100, M=9, N=100, K=256, abd=K.KDA_BF16, cd=K.KDA_F32)
+    a.update(over)
+    return call("kda_gemm_epilogue", a["A"], a["lda"], a["B"], a["ldb"], a["bias"], a["act"], a["r"], a["ldr"], a["rd"],
+                a["C"], a["ldc"], a["M"], a["N"], a["K"], a["abd"], a["cd"], None)[0]
+
+
+def test_gemm_epilogue_validation():
+    assert gemm(M=0) == K.KDA_OK
+    for name in ("A", "B", "C"):
+        assert gemm(**{name: None}) == INVALID, name
+        assert gemm(**{name: fake(8) + 8}) == INVALID, name
+    assert gemm(r=fake(8) + 4) == INVALID and gemm(bias=fake(8) + 4) == INVALID
+    assert gemm(abd=K.KDA_F32) == UNSUPPORTED and gemm(abd=2) == INVALID and gemm(cd=9) == INVALID and gemm(rd=9) == INVALID
+    assert gemm(act=-1) == INVALID and gemm(act=5) == INVALID
+    assert gemm(M=-1) == INVALID and gemm(N=0) == INVALID and gemm(K=0) == INVALID and gemm(K=252) == UNSUPPORTED
+    assert gemm(lda=248) == INVALID and gemm(ldb=260) == INVALID and gemm(ldc=96) == INVALID and gemm(ldc=102) == INVALID
+    assert gemm(ldr=96) == INVALID and gemm(ldr=101) == INVALID
+    assert gemm(C=fake(1)) == INVALID and gemm(C=fake(2) + 64) == INVALID and gemm(C=fake(3)) == INVALID
+    # the residual in place: only as the same matrix
+    assert gemm(r=fake(5) + 16) == INVALID and gemm(r=fake(5), ldr=104) == INVALID
+    assert gemm(r=fake(5), rd=K.KDA_BF16) == INVALID
+
+
+def test_binding_refuses_shapes_types_and_host_tensors():
+    x, w = torch.zeros(4, 256), torch.ones(256)
+    with pytest.raises(ValueError, match="GPU"):
+        K.kda_add_rmsnorm(x, w, torch.empty_like(x))
+    with pytest.raises(ValueError, match="shape"):
+        K.kda_add_rmsnorm(x, w, torch.empty(4, 128), residual=torch.zeros(3, 256))
+    with pytest.raises(TypeError, match="norm_weight"):
+        K.kda_add_rmsnorm(x, w[:8], torch.empty_like(x))
+    with pytest.raises(ValueError, match="contiguous"):
+        K.kda_add_rmsnorm(x.t().contiguous().t(), w, torch.empty_like(x))
+    A, B = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(8, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="activation"):
+        K.kda_gemm_epilogue(A, B, torch.empty(4, 8), activation="tanh")
+    with pytest.raises(ValueError, match="shape"):
+        K.kda_gemm_epilogue(A, B, torch.empty(8, 4))
+    with pytest.raises(TypeError, match="bias"):
+        K.kda_gemm_epilogue(A, B, torch.empty(4, 8), bias=torch.zeros(8, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="GPU"):
+        K.kda_gemm_epilogue(A, B, torch.empty(4, 8))
