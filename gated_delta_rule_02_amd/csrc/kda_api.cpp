@@ -435,6 +435,121 @@ int kda_output_norm_gate_fp8(const void* o, kda_dtype o_dtype, const void* gate,
     return hip_status(launch_norm_gate_fp8(a, static_cast<hipStream_t>(hip_stream)), "kda_output_norm_gate_fp8");
 }
 
+// ---------------------------------------------------------------- draft trees
+static int check_tree(const char* fn, const int32_t* parents, int B, int num_nodes, int H)
+{
+    REQUIRE(B >= 1 && H >= 1 && num_nodes >= 1, KDA_ERR_INVALID_ARG, "%s: B, H and num_nodes must be >= 1", fn);
+    REQUIRE(num_nodes <= 64, KDA_ERR_UNSUPPORTED, "%s: at most 64 nodes per tree (got %d)", fn, num_nodes);
+    REQUIRE((int64_t)B * H <= 0x7fffffff && (int64_t)B * num_nodes <= 0x7fffffff, KDA_ERR_INVALID_ARG,
+            "%s: B*H or B*num_nodes too large", fn);
+    REQUIRE(parents && (uintptr_t)parents % 4 == 0, KDA_ERR_INVALID_ARG, "%s: parents null or misaligned", fn);
+    return KDA_OK;
+}
+
+int kda_decode_tree(const void* q, const void* k, const void* v, const void* g, const void* beta, kda_dtype in_dtype,
+                    const int32_t* parents, int B, int num_nodes, int H, int dk, int dv, float scale,
+                    float lower_bound, const void* state, kda_dtype state_dtype, void* o, kda_dtype out_dtype,
+                    float* writes, void* hip_stream)
+{
+    const char* fn = "kda_decode_tree";
+    REQUIRE(q && k && v && g && beta && state && o, KDA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+    REQUIRE(valid_dtype(in_dtype) && valid_dtype(out_dtype) && valid_dtype(state_dtype), KDA_ERR_INVALID_ARG,
+            "%s: bad dtype", fn);
+    REQUIRE(dk == 128 && dv == 128, KDA_ERR_UNSUPPORTED, "%s: only dk = dv = 128 is supported (got %d, %d)", fn, dk, dv);
+    if (int rc = check_tree(fn, parents, B, num_nodes, H); rc != KDA_OK) return rc;
+    if (int rc = check_lower_bound(fn, lower_bound, false); rc != KDA_OK) return rc;
+    for (const void* p : {q, k, v, g, beta, state, (const void*)o, (const void*)writes})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t rows = (size_t)B * num_nodes * H, ei = esize(in_dtype);
+    const Range ro = rng(o, rows * 128 * esize(out_dtype)), rw = rng(writes, writes ? rows * 128 * 4 : 0);
+    for (Range r : {rng(q, rows * 128 * ei), rng(k, rows * 128 * ei), rng(v, rows * 128 * ei), rng(g, rows * 128 * ei),
+                    rng(beta, rows * ei), rng(parents, (size_t)B * num_nodes * 4),
+                    rng(state, (size_t)B * H * 128 * 128 * esize(state_dtype))})
+        REQUIRE(!overlap(r, ro) && !overlap(r, rw), KDA_ERR_INVALID_ARG, "%s: o or writes overlaps an input", fn);
+    REQUIRE(!overlap(ro, rw), KDA_ERR_INVALID_ARG, "%s: o overlaps writes", fn);
+    TreeArgs a{};
+    a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.parents = parents;
+    a.state = state; a.o = o; a.writes = writes;
+    a.B = B; a.N = num_nodes; a.H = H; a.scale = scale; a.lower_bound = lower_bound;
+    a.in_dtype = (DType)in_dtype; a.out_dtype = (DType)out_dtype; a.state_dtype = (DType)state_dtype;
+    return hip_status(launch_decode_tree(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_decode_tree_commit(const void* k, const void* g, kda_dtype in_dtype, const float* writes,
+                           const int32_t* parents, const int32_t* accepted, int B, int num_nodes, int H, int dk, int dv,
+                           float lower_bound, void* state, kda_dtype state_dtype, void* hip_stream)
+{
+    const char* fn = "kda_decode_tree_commit";
+    REQUIRE(k && g && writes && accepted && state, KDA_ERR_INVALID_ARG, "%s: null tensor pointer", fn);
+    REQUIRE(valid_dtype(in_dtype) && valid_dtype(state_dtype), KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    REQUIRE(dk == 128 && dv == 128, KDA_ERR_UNSUPPORTED, "%s: only dk = dv = 128 is supported (got %d, %d)", fn, dk, dv);
+    if (int rc = check_tree(fn, parents, B, num_nodes, H); rc != KDA_OK) return rc;
+    if (int rc = check_lower_bound(fn, lower_bound, false); rc != KDA_OK) return rc;
+    for (const void* p : {k, g, (const void*)writes, (const void*)state})
+        REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    REQUIRE((uintptr_t)accepted % 4 == 0, KDA_ERR_INVALID_ARG, "%s: accepted misaligned", fn);
+    const size_t rows = (size_t)B * num_nodes * H, ei = esize(in_dtype);
+    const Range rs = rng(state, (size_t)B * H * 128 * 128 * esize(state_dtype));
+    for (Range r : {rng(k, rows * 128 * ei), rng(g, rows * 128 * ei), rng(writes, rows * 128 * 4),
+                    rng(parents, (size_t)B * num_nodes * 4), rng(accepted, (size_t)B * 4)})
+        REQUIRE(!overlap(r, rs), KDA_ERR_INVALID_ARG, "%s: state overlaps an input", fn);
+    TreeArgs a{};
+    a.k = k; a.g = g; a.parents = parents; a.accepted = accepted; a.writes_in = writes; a.state_out = state;
+    a.B = B; a.N = num_nodes; a.H = H; a.lower_bound = lower_bound;
+    a.in_dtype = (DType)in_dtype; a.state_dtype = (DType)state_dtype;
+    return hip_status(launch_tree_commit(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+// checks shared by the convolution's two tree entries
+static int check_conv_tree(const char* fn, const void* x, int64_t x_ld, const void* conv_state, const int32_t* parents,
+                           kda_dtype dtype, int B, int num_nodes, int C, int W)
+{
+    REQUIRE(x && conv_state, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(valid_dtype(dtype), KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    if (int rc = check_tree(fn, parents, B, num_nodes, 1); rc != KDA_OK) return rc;
+    REQUIRE(C >= 128 && C % 128 == 0, KDA_ERR_UNSUPPORTED, "%s: C must be a positive multiple of 128 (got %d)", fn, C);
+    REQUIRE(W >= 2 && W <= 8, KDA_ERR_UNSUPPORTED, "%s: W must be in [2, 8] (got %d)", fn, W);
+    REQUIRE(x_ld >= C && x_ld % 8 == 0, KDA_ERR_INVALID_ARG, "%s: x_ld must be >= C and a multiple of 8", fn);
+    REQUIRE(aligned16(x) && aligned16(conv_state), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    return KDA_OK;
+}
+
+int kda_conv_tree(const void* x, int64_t x_ld, const void* conv_state, const int32_t* parents, const void* weight,
+                  const void* bias, kda_dtype dtype, int B, int num_nodes, int C, int W, int apply_silu,
+                  int l2norm_group, float l2norm_eps, void* y, void* hip_stream)
+{
+    const char* fn = "kda_conv_tree";
+    if (int rc = check_conv_tree(fn, x, x_ld, conv_state, parents, dtype, B, num_nodes, C, W); rc != KDA_OK) return rc;
+    REQUIRE(weight && y, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(l2norm_group == 0 || l2norm_group == 128, KDA_ERR_UNSUPPORTED, "%s: l2norm_group must be 0 or 128 (got %d)", fn,
+            l2norm_group);
+    for (const void* p : {weight, bias, (const void*)y})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t es = esize(dtype), rows = (size_t)B * num_nodes;
+    const Range ry = rng(y, rows * C * es);
+    for (Range r : {rng(x, ((rows - 1) * x_ld + C) * es), rng(conv_state, (size_t)B * (W - 1) * C * es),
+                    rng(parents, rows * 4), rng(weight, (size_t)C * W * es), rng(bias, bias ? (size_t)C * es : 0)})
+        REQUIRE(!overlap(r, ry), KDA_ERR_INVALID_ARG, "%s: y overlaps another tensor", fn);
+    ConvTreeArgs a{x, x_ld, const_cast<void*>(conv_state), parents, nullptr, weight, bias, y, B, num_nodes, C, W,
+                   apply_silu ? 1 : 0, l2norm_group, l2norm_eps, (DType)dtype};
+    return hip_status(launch_conv_tree(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_conv_tree_commit(const void* x, int64_t x_ld, const int32_t* parents, const int32_t* accepted, kda_dtype dtype,
+                         int B, int num_nodes, int C, int W, void* conv_state, void* hip_stream)
+{
+    const char* fn = "kda_conv_tree_commit";
+    if (int rc = check_conv_tree(fn, x, x_ld, conv_state, parents, dtype, B, num_nodes, C, W); rc != KDA_OK) return rc;
+    REQUIRE(accepted && (uintptr_t)accepted % 4 == 0, KDA_ERR_INVALID_ARG, "%s: accepted null or misaligned", fn);
+    const size_t es = esize(dtype), rows = (size_t)B * num_nodes;
+    const Range rs = rng(conv_state, (size_t)B * (W - 1) * C * es);
+    for (Range r : {rng(x, ((rows - 1) * x_ld + C) * es), rng(parents, rows * 4), rng(accepted, (size_t)B * 4)})
+        REQUIRE(!overlap(r, rs), KDA_ERR_INVALID_ARG, "%s: conv_state overlaps an input", fn);
+    ConvTreeArgs a{x, x_ld, conv_state, parents, accepted, nullptr, nullptr, nullptr, B, num_nodes, C, W, 0, 0, 0.0f,
+                   (DType)dtype};
+    return hip_status(launch_conv_tree(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
 // ---------------------------------------------------------------- residual + RMSNorm
 static int add_rmsnorm_impl(const char* fn, const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual,
                             int64_t residual_ld, void* residual_out, int64_t residual_out_ld,

@@ -165,6 +165,39 @@ struct NormGateFp8Args {
 };
 hipError_t launch_norm_gate_fp8(const NormGateFp8Args& a, hipStream_t s);
 
+// trees of drafted tokens: N nodes per sequence under its state (verification
+// and commit; the unused side's pointers are null)
+struct TreeArgs {
+    const void *q, *k, *v, *g, *beta;  // [B, N, H, .] in in_dtype
+    const int32_t* parents;            // [B, N]
+    const int32_t* accepted;           // [B] (commit)
+    const void* state;                 // [B, H, 128, 128] in state_dtype (verification: read)
+    void* state_out;                   // the same (commit: in place)
+    void* o;                           // [B, N, H, 128] in out_dtype
+    float* writes;                     // [B, N, H, 128] or null
+    const float* writes_in;            // the same (commit)
+    int B, N, H;
+    float scale, lower_bound;
+    DType in_dtype, out_dtype, state_dtype;
+};
+hipError_t launch_decode_tree(const TreeArgs& a, hipStream_t s);
+hipError_t launch_tree_commit(const TreeArgs& a, hipStream_t s);
+
+// the prologue convolution along the trees' paths; with accepted set, the commit
+// of the history (weight, bias and y unused)
+struct ConvTreeArgs {
+    const void* x;  // B * N rows
+    int64_t x_ld;
+    void* hist;  // [B, W-1, C]
+    const int32_t *parents, *accepted;
+    const void *weight, *bias;
+    void* y;  // [B * N, C]
+    int B, N, C, W, apply_silu, l2_group;
+    float l2_eps;
+    DType dtype;
+};
+hipError_t launch_conv_tree(const ConvTreeArgs& a, hipStream_t s);
+
 // h = x + res (res may be null); res_out = h (null: not stored); y = RMSNorm(h) w,
 // stored in y_dtype, or, with scales set, as E4M3 codes with one scale per 128 columns
 struct AddNormArgs {

@@ -50,6 +50,10 @@ _SIGS = {
     "kda_gate_prologue": (_I, [_P, _I64, _P, _I64, _P, _I64, _I, _I, _F, _I, _P, _P, _I, _P]),
     "kda_output_norm_gate": (_I, [_P, _I, _P, _I64, _P, _I64, _I, _I, _F, _P, _I, _P]),
     "kda_gemm": (_I, [_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
+    "kda_decode_tree": (_I, [_P] * 5 + [_I, _P, _I, _I, _I, _I, _I, _F, _F, _P, _I, _P, _I, _P, _P]),
+    "kda_decode_tree_commit": (_I, [_P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _I, _P]),
+    "kda_conv_tree": (_I, [_P, _I64, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P]),
+    "kda_conv_tree_commit": (_I, [_P, _I64, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "kda_add_rmsnorm": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _I64, _I, _P]),
     "kda_add_rmsnorm_fp8": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _I64, _P, _I64, _P]),
     "kda_gemm_epilogue": (_I, [_P, _I64, _P, _I64, _P, _I, _P, _I64, _I, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
@@ -488,6 +492,92 @@ def _call_on(name, tensors, stream, *args):
         return _call(name, *args, _stream(stream))
     with torch.cuda.device(device):
         return _call(name, *args, _stream(stream))
+
+
+def _tensor(name, t, shape, dtype=None):
+    """Checks a dense tensor: shape, contiguous, dtype (if given)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    return _dense(t, name)
+
+
+def kda_decode_tree(q, k, v, g, beta, parents, state, o, writes=None, scale=1.0, lower_bound=-5.0, stream=None):
+    """Verify a tree of drafts per sequence. q,k,g,v [B,N,H,128], beta [B,N,H] (one
+    dtype), parents int32 [B,N] (-1 the state, or a node before; anything else
+    marks an absent node), state [B,H,128,128] (float32 or bfloat16, read only), o
+    [B,N,H,128]; writes float32 [B,N,H,128] or None, for kda_decode_tree_commit."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, N, H, 128]")
+    B, N, H, dk = q.shape
+    for n_, t_, s_ in (("q", q, q.shape), ("k", k, q.shape), ("v", v, (B, N, H, v.shape[-1])), ("g", g, q.shape),
+                       ("beta", beta, (B, N, H))):
+        _tensor(n_, t_, s_, q.dtype)
+    dv = v.shape[-1]
+    _tensor("parents", parents, (B, N), torch.int32)
+    _tensor("state", state, (B, H, dk, dv))
+    _tensor("o", o, (B, N, H, dv))
+    _tensor("writes", writes, (B, N, H, dv), torch.float32)
+    _call_on("kda_decode_tree", (q, k, v, g, beta, parents, state, o, writes), stream, _ptr(q), _ptr(k), _ptr(v),
+             _ptr(g), _ptr(beta), _dt(q), _ptr(parents), B, N, H, dk, dv, scale, lower_bound, _ptr(state), _dt(state),
+             _ptr(o), _dt(o), _ptr(writes))
+    return o
+
+
+def kda_decode_tree_commit(k, g, writes, parents, accepted, state, lower_bound=-5.0, stream=None):
+    """state[b] <- the state after node accepted[b] (int32 [B], device) of the tree
+    that kda_decode_tree verified with these k, g and parents, and that gave
+    writes; any other value of accepted leaves state[b] as it is."""
+    if k.dim() != 4:
+        raise ValueError("k must be [B, N, H, 128]")
+    B, N, H, dk = k.shape
+    dv = writes.shape[-1]
+    _tensor("k", k, k.shape)
+    _tensor("g", g, k.shape, k.dtype)
+    _tensor("writes", writes, (B, N, H, dv), torch.float32)
+    _tensor("parents", parents, (B, N), torch.int32)
+    _tensor("accepted", accepted, (B,), torch.int32)
+    _tensor("state", state, (B, H, dk, dv))
+    _call_on("kda_decode_tree_commit", (k, g, writes, parents, accepted, state), stream, _ptr(k), _ptr(g), _dt(k),
+             _ptr(writes), _ptr(parents), _ptr(accepted), B, N, H, dk, dv, lower_bound, _ptr(state), _dt(state))
+    return state
+
+
+def _conv_tree_sizes(x, conv_state, parents):
+    B, N = parents.shape
+    W, C = conv_state.shape[1] + 1, conv_state.shape[2]
+    _rows("x", x, (B * N, C))
+    _tensor("conv_state", conv_state, (B, W - 1, C), x.dtype)
+    _tensor("parents", parents, (B, N), torch.int32)
+    return B, N, C, W
+
+
+def kda_conv_tree(x, conv_state, parents, weight, y, bias=None, apply_silu=True, l2norm_group=0, l2norm_eps=1e-6,
+                  stream=None):
+    """The prologue convolution over trees of drafts: x rows [B*N, C] (row strides
+    allowed), conv_state [B,W-1,C] (read only), parents int32 [B,N] (as
+    kda_decode_tree), weight [C,W], y [B*N,C]."""
+    B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
+    _tensor("weight", weight, (C, W), x.dtype)
+    _tensor("bias", bias, (C,), x.dtype)
+    _tensor("y", y, (B * N, C), x.dtype)
+    _call_on("kda_conv_tree", (x, conv_state, parents, weight, y, bias), stream, _ptr(x), _ld(x), _ptr(conv_state),
+             _ptr(parents), _ptr(weight), _ptr(bias), _dt(x), B, N, C, W, int(bool(apply_silu)), l2norm_group,
+             l2norm_eps, _ptr(y))
+    return y
+
+
+def kda_conv_tree_commit(x, parents, accepted, conv_state, stream=None):
+    """conv_state[b] <- the last W-1 inputs of itself followed by the path to node
+    accepted[b] of the tree (x, parents as for kda_conv_tree), in place."""
+    B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
+    _tensor("accepted", accepted, (B,), torch.int32)
+    _call_on("kda_conv_tree_commit", (x, parents, accepted, conv_state), stream, _ptr(x), _ld(x), _ptr(parents),
+             _ptr(accepted), _dt(x), B, N, C, W, _ptr(conv_state))
+    return conv_state
 
 
 def _add_rmsnorm_args(x, norm_weight, residual, residual_out):

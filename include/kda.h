@@ -324,6 +324,53 @@ int kda_decode_commit(const void* token_states, const int32_t* accepted, int B, 
                       int dv, void* state, kda_dtype state_dtype, void* hip_stream);
 
 /* ------------------------------------------------------------------------
+ * kda_decode_tree -- verify a tree of draft tokens per sequence.
+ *
+ * The recurrence along every root path of a tree of num_nodes drafted tokens
+ * whose root is the sequence's state (a chain of drafts is kda_decode_multi; the
+ * draft head is that of the same page and section). Node i follows node
+ * parents[i], so o of node i is what kda_decode_multi gives for the last token of
+ * the path to i. All nodes read the state once; no state is written and none is
+ * formed per node. writes receives the delta-rule writes
+ * u_i = beta_i (v_i - S'^T k_i), from which kda_decode_tree_commit forms the state
+ * after any node.
+ *
+ * q, k, g [B, num_nodes, H, dk], v [B, num_nodes, H, dv], beta [B, num_nodes, H]:
+ *         in_dtype.
+ * parents int32 [B, num_nodes], device: -1 (the node follows the state itself) or
+ *         the index of a node before it (parents[i] < i). Any other value marks the
+ *         node as absent, as are the nodes below an absent one: their o and writes
+ *         are zero whatever their inputs hold (unused places of a ragged batch).
+ * state   [B, H, dk, dv] in state_dtype, read only.
+ * o       [B, num_nodes, H, dv] out_dtype.
+ * writes  float32 [B, num_nodes, H, dv] or NULL (verification only).
+ * Everything is computed in float32 (o rounded once, when stored). lower_bound as
+ * for kda_decode_step. Neither output may overlap another tensor.
+ * Supported: dk = dv = 128, B, H >= 1, 1 <= num_nodes <= 64.
+ * ---------------------------------------------------------------------- */
+int kda_decode_tree(const void* q, const void* k, const void* v, const void* g, const void* beta, kda_dtype in_dtype,
+                    const int32_t* parents, int B, int num_nodes, int H, int dk, int dv, float scale,
+                    float lower_bound, const void* state, kda_dtype state_dtype, void* o, kda_dtype out_dtype,
+                    float* writes, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_decode_tree_commit -- the state after the accepted path of a tree.
+ *
+ * state[b] becomes the state after node accepted[b] and the nodes above it,
+ * formed from the state before the tree, the path's k, g and writes (as given to
+ * and received from kda_decode_tree): one read and one write of the state.
+ *
+ * accepted  int32 [B], device: a node of the tree. Any other value, or an absent
+ *           node, leaves state[b] as it is.
+ * state     [B, H, dk, dv] in state_dtype, updated in place (float32 arithmetic,
+ *           bfloat16 rounded to nearest even when stored).
+ * The rest as kda_decode_tree.
+ * ---------------------------------------------------------------------- */
+int kda_decode_tree_commit(const void* k, const void* g, kda_dtype in_dtype, const float* writes,
+                           const int32_t* parents, const int32_t* accepted, int B, int num_nodes, int H, int dk, int dv,
+                           float lower_bound, void* state, kda_dtype state_dtype, void* hip_stream);
+
+/* ------------------------------------------------------------------------
  * kda_state_convert -- states between float32 and bfloat16 storage.
  *
  * The state may be held in BF16 between decode steps ("Ling-3.1-flash: What
@@ -481,6 +528,35 @@ int kda_conv_prefill(const void* x, int64_t x_ld, int64_t num_tokens, int C, int
                      const void* weight, const void* bias, const void* conv_state_in,
                      void* conv_state_out, int apply_silu, int l2norm_group, float l2norm_eps,
                      void* y, int64_t y_ld, kda_dtype dtype, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_conv_tree -- the prologue convolution over trees of draft tokens.
+ *
+ * As kda_conv_state_update, for every node of a tree of drafts (parents as for
+ * kda_decode_tree): the window of node i is the last W inputs of the conv state
+ * followed by the path to i. The conv state is only read. An absent node's row of
+ * y is zero.
+ *
+ * x           B * num_nodes rows of C (node i of sequence b: row b * num_nodes + i
+ *             at x + row * x_ld)
+ * conv_state  [B, W-1, C], oldest first, read only
+ * y           [B * num_nodes, C], must not overlap another tensor
+ * The rest as kda_conv_state_update; 1 <= num_nodes <= 64.
+ * ---------------------------------------------------------------------- */
+int kda_conv_tree(const void* x, int64_t x_ld, const void* conv_state, const int32_t* parents, const void* weight,
+                  const void* bias, kda_dtype dtype, int B, int num_nodes, int C, int W, int apply_silu,
+                  int l2norm_group, float l2norm_eps, void* y, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_conv_tree_commit -- the conv state after the accepted path of a tree.
+ *
+ * conv_state[b] becomes the last W-1 inputs of itself followed by the path to
+ * node accepted[b] (bit copies, in place); an accepted value that is no node, or
+ * an absent node, leaves it as it is. Arguments as kda_conv_tree and
+ * kda_decode_tree_commit; conv_state must not overlap an input.
+ * ---------------------------------------------------------------------- */
+int kda_conv_tree_commit(const void* x, int64_t x_ld, const int32_t* parents, const int32_t* accepted, kda_dtype dtype,
+                         int B, int num_nodes, int C, int W, void* conv_state, void* hip_stream);
 
 /* ------------------------------------------------------------------------
  * kda_gate_prologue -- log-retention and write strength from projections.
