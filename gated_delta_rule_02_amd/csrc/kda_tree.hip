@@ -17,6 +17,8 @@
 // accepted path are all that a commit needs. The decays are products of the
 // alphas taken along the path, never quotients: exact for every floor down to
 // -inf, and a path that has decayed to nothing contributes nothing.
+#include <utility>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -175,72 +177,263 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 }
 
 // ------------------------------------------------------------ verification
-// One workgroup per (sequence, head), a thread per value channel.
-template <typename TIN, typename TOUT, typename TS, int NP>
-__global__ __launch_bounds__(128) void decode_tree_kernel(TreeArgs a)
+// One workgroup of four wavefronts per (sequence, head); wavefront w takes value
+// channels 32 w .. 32 w + 31. Four phases:
+//   load   the wavefront's 128 x 32 part of S0 into registers (64 for a float32
+//          state), used last but issued first: the rest of the workgroup's work
+//          up to the products runs while it arrives;
+//   walk   16 lanes per node walk up its path with the running decay, forming
+//          the node's products with every node above it (P with q_i, A with k_i)
+//          and, at the end, the decayed rows D(i) k_i and D(i) q_i. Only pairs on
+//          a path are formed;
+//   read   [D k; D q] S0 on the float32 matrix instruction (float32 products
+//          and sums: the results are held to float32 accuracy), two 16-column tiles
+//          per wavefront, rows from LDS, S0 from the registers;
+//   solve  u by forward substitution, each lane a value channel, the remainders
+//          of all nodes in registers: after u_j every r_i below takes - A_ij u_j,
+//          independent operations; then o += P u by the matrix instruction on the
+//          accumulators that already hold (D q) S0.
+// NP: N rounded up to 8, 16, 32 or 64.
+template <int NP> constexpr int kTreeWaves = NP <= 16 ? 4 : (NP == 32 ? 2 : 1);  // wavefronts per SIMD (LDS, registers)
+
+// f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
+// constants from the start (a loop unrolled late left the 32 remainders of the
+// substitution in one 32-register tuple, copied and spilled at every update).
+template <typename F, int... I>
+__device__ __forceinline__ void static_for(F&& f, std::integer_sequence<int, I...>)
 {
-    __shared__ float s_k[NP][D], s_al[NP][D], s_kt[NP][D], s_qt[NP][D];  // s_k holds the writes u later
-    __shared__ float s_A[NP][NP], s_P[NP][NP];
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f)
+{
+    static_for(f, std::make_integer_sequence<int, N>{});
+}
+
+// Sum over aligned groups of 16 lanes, in every lane (rotations within the row).
+template <int ROR>
+__device__ __forceinline__ float add_ror(float v)
+{
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + ROR, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float v) { return add_ror<1>(add_ror<2>(add_ror<4>(add_ror<8>(v)))); }
+
+// Two consecutive state elements, streamed once.
+__device__ __forceinline__ f32x2 state2(const float* p) { return __builtin_nontemporal_load(reinterpret_cast<const f32x2*>(p)); }
+__device__ __forceinline__ f32x2 unpack2(f32x2 v) { return v; }
+__device__ __forceinline__ uint32_t state2(const bf16_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)); }
+__device__ __forceinline__ f32x2 unpack2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
+
+template <typename TIN, typename TOUT, typename TS, int NP>
+__global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeArgs a)
+{
+    constexpr int LD = D + 4;                  // row of the decayed rows: 16 rows at one column meet distinct banks
+    constexpr int LP = NP + 4;
+    constexpr int MT = 2 * NP / 16;            // row tiles: D k, then D q (NP = 8: one tile holds both)
+    constexpr int MO = NP >= 16 ? NP / 16 : 1;  // row tiles of o, the last MO
+    __shared__ __attribute__((aligned(16))) float s_row[2 * NP][LD];  // D k and D q; then (D k) S0 and the writes u
+    __shared__ __attribute__((aligned(16))) float s_k[NP][D], s_al[NP][D];
+    // P[i][j] = q_i . D(i,j) k_j at [i][j] (j <= i), A[i][j] = k_i . D(i,j) k_j at [j][i] (j < i)
+    __shared__ __attribute__((aligned(16))) float s_pa[NP][LP];
+    __shared__ float s_beta[NP];
+    __shared__ int s_par[64];
     const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int m16 = lane & 15, q4 = lane >> 4;
     const int N = a.N;
+
+    // load: element s of group g is row 16 g + 4 q4 + s, columns 32 w + 2 m16 and + 1
+    // (a uniform base, a 32-bit lane offset and constants: one address register)
+    const TS* S = static_cast<const TS*>(a.state) + (size_t)bh * D * D + 32 * wave;
+    const uint32_t s_off = 4 * q4 * D + 2 * m16;
+    decltype(state2(S)) raw[8][4];
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) raw[g][s] = state2(S + 16 * g * D + (s_off + s * D));
+
     const int parent = tree_parent(a.parents + (size_t)b * N, N);
-    auto at = [&](int i) { return ((size_t)b * N + i) * a.H + h; };  // row of [B, N, H, .]
-    for (int i = 0; i < N; ++i) {
-        if (__builtin_amdgcn_readlane(parent, i) == -2) continue;
-        s_k[i][t] = ld(static_cast<const TIN*>(a.k) + at(i) * D + t);
-        s_al[i][t] = __expf(fmaxf(ld(static_cast<const TIN*>(a.g) + at(i) * D + t), a.lower_bound));
-    }
-    __syncthreads();
-    // products of each node with the nodes above it, walking up
-    for (int i = wave; i < N; i += 2) {
-        if (__builtin_amdgcn_readlane(parent, i) == -2) continue;
-        const f32x2 q = ld2(static_cast<const TIN*>(a.q) + at(i) * D + 2 * lane);
-        const f32x2 k = ld2(&s_k[i][2 * lane]);
-        f32x2 decay = {1.0f, 1.0f};
-        for (int j = i; j >= 0; j = __builtin_amdgcn_readlane(parent, j)) {
-            const f32x2 kj = ld2(&s_k[j][2 * lane]) * decay;
-            const float pq = wave_sum(q.x * kj.x + q.y * kj.y), pk = wave_sum(k.x * kj.x + k.y * kj.y);
-            if (lane == 0) {
-                s_P[i][j] = pq;
-                s_A[i][j] = pk;
-            }
-            decay *= ld2(&s_al[j][2 * lane]);
-        }
-        *reinterpret_cast<f32x2*>(&s_kt[i][2 * lane]) = k * decay;
-        *reinterpret_cast<f32x2*>(&s_qt[i][2 * lane]) = q * decay;
-    }
-    __syncthreads();
-    const TS* S = static_cast<const TS*>(a.state) + (size_t)bh * D * D + t;
-    for (int i0 = 0; i0 < N; i0 += 8) {
-        float tk[8], tq[8];
+    const uint64_t there = __ballot(parent != -2);  // lanes past N hold -2
+    auto row_of = [&](int i) { return ((size_t)b * N + i) * a.H + h; };
+    if (wave == 0) s_par[lane] = parent;
+    for (int i = t >> 5; i < N; i += 8) {
+        const int c = 4 * (t & 31);
+        if (!(there >> i & 1)) continue;
+        *reinterpret_cast<f32x4*>(&s_k[i][c]) = ld4(static_cast<const TIN*>(a.k) + row_of(i) * D + c);
+        f32x4 g = ld4(static_cast<const TIN*>(a.g) + row_of(i) * D + c);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) tk[n] = tq[n] = 0.0f;
-        for (int r = 0; r < D; ++r) {
-            const float s = ld(S + (size_t)r * D);
+        for (int e = 0; e < 4; ++e) g[e] = __expf(fmaxf(g[e], a.lower_bound));
+        *reinterpret_cast<f32x4*>(&s_al[i][c]) = g;
+    }
+    if (t < NP) s_beta[t] = there >> t & 1 ? ld(static_cast<const TIN*>(a.beta) + row_of(t)) : 0.0f;
+    for (int e = t; e < NP * LP; e += 256) (&s_pa[0][0])[e] = 0.0f;
+    __syncthreads();
+
+    // walk: node i by 16 lanes, lane channels 4 m16 .. and 64 + 4 m16 ..
+    for (int i = 4 * wave + q4; i < NP; i += 16) {
+        int j = i < N && (there >> i & 1) ? i : -1;
+        f32x4 q[2], k[2], decay[2];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                tk[n] += s_kt[(i0 + n) & (NP - 1)][r] * s;
-                tq[n] += s_qt[(i0 + n) & (NP - 1)][r] * s;
+        for (int p = 0; p < 2; ++p) {
+            q[p] = k[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+            decay[p] = f32x4{1.f, 1.f, 1.f, 1.f};
+            if (j >= 0) {
+                q[p] = ld4(static_cast<const TIN*>(a.q) + row_of(i) * D + 64 * p + 4 * m16);
+                k[p] = *reinterpret_cast<const f32x4*>(&s_k[i][64 * p + 4 * m16]);
             }
         }
+        while (j >= 0) {
+            float pq = 0.0f, pk = 0.0f;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-            const int i = i0 + n;
-            if (i >= N) break;
-            float u = 0.0f, o = 0.0f;
-            if (__builtin_amdgcn_readlane(parent, i) != -2) {
-                for (int j = __builtin_amdgcn_readlane(parent, i); j >= 0; j = __builtin_amdgcn_readlane(parent, j)) {
-                    u += s_A[i][j] * s_k[j][t];
-                    o += s_P[i][j] * s_k[j][t];
+            for (int p = 0; p < 2; ++p) {
+                const f32x4 kj = *reinterpret_cast<const f32x4*>(&s_k[j][64 * p + 4 * m16]) * decay[p];
+                decay[p] *= *reinterpret_cast<const f32x4*>(&s_al[j][64 * p + 4 * m16]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    pq += q[p][e] * kj[e];
+                    pk += k[p][e] * kj[e];
                 }
-                u = ld(static_cast<const TIN*>(a.beta) + at(i)) *
-                    (ld(static_cast<const TIN*>(a.v) + at(i) * D + t) - tk[n] - u);
-                o = a.scale * (tq[n] + o + s_P[i][i] * u);
-                s_k[i][t] = u;
             }
-            st(static_cast<TOUT*>(a.o) + at(i) * D + t, o);
-            if (a.writes) a.writes[at(i) * D + t] = u;
+            pq = sum16(pq);
+            pk = sum16(pk);
+            if (m16 == 0) {
+                s_pa[i][j] = pq;
+                if (j != i) s_pa[j][i] = pk;
+            }
+            j = s_par[j];
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            *reinterpret_cast<f32x4*>(&s_row[i][64 * p + 4 * m16]) = k[p] * decay[p];
+            *reinterpret_cast<f32x4*>(&s_row[NP + i][64 * p + 4 * m16]) = q[p] * decay[p];
+        }
+    }
+    __syncthreads();
+
+    // read: lane (m16, q4) gives row m16 of a tile, K element 16 g + 4 q4 + s in
+    // step (g, s), and takes rows 4 q4 + e of column tile c (columns 2 m16 + c)
+    f32x4 acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) acc[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        f32x4 row[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) row[m] = *reinterpret_cast<const f32x4*>(&s_row[16 * m + m16][16 * g + 4 * q4]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const f32x2 st = unpack2(raw[g][s]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[m][s], st[c], acc[m][c], 0, 0, 0);
+        }
+    }
+    __syncthreads();  // s_row is read: its halves now hold (D k) S0 and u, each wavefront its own columns
+    const int c2 = 32 * wave + 2 * m16;
+#pragma unroll
+    for (int m = 0; m < MO; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (NP >= 16 || q4 < 2)
+                *reinterpret_cast<f32x2*>(&s_row[16 * m + 4 * q4 + e][c2]) = f32x2{acc[m][0][e], acc[m][1][e]};
+
+    __builtin_amdgcn_sched_barrier(0);
+
+    // solve: both halves of the wavefront hold the same channel and the same values
+    const int col = 32 * wave + (lane & 31), half = lane >> 5;
+    float r[NP];
+    static_for<NP>([&](auto i) {
+        // no branch: a place past the end reads the last node's, an absent one its own
+        const TIN* vi = static_cast<const TIN*>(a.v) + row_of(min((int)i, N - 1)) * D;
+        const float v = ld(vi + (uint32_t)col) - s_row[i][col];
+        r[i] = there >> i & 1 ? v : 0.0f;
+        if constexpr (i % 16 == 15) __builtin_amdgcn_sched_barrier(0);
+    });
+    // An infinite or NaN write must reach the nodes below it and no others, but
+    // the sums below run over all nodes with coefficients 0 where there is no
+    // path. So such a write enters the sums as 0, and is noted: it and what lies
+    // below it become NaN at the end. (No branch in here: the compiler would sink
+    // the updates past it, to where their r is used, and keep every A alive.)
+    uint64_t bad = 0;
+    static_for<NP>([&](auto J) {
+        constexpr int j = J;
+        const float u = there >> j & 1 ? s_beta[j] * r[j] : 0.0f;
+        const bool fine = fabsf(u) < __builtin_inff();
+        const float w = fine ? u : 0.0f;
+        if (!fine) bad |= (uint64_t)1 << j;
+        s_row[NP + j][col] = w;
+        static_for<NP / 4>([&](auto n) {
+            if constexpr (4 * n + 3 > j) {
+                const f32x4 A = *reinterpret_cast<const f32x4*>(&s_pa[j][4 * n]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * n + e > j) r[4 * n + e] -= A[e] * w;
+            }
+        });
+        // rows of A at most two ahead: all of them at once spill
+        if constexpr (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+    });
+    const bool any_bad = __any(bad != 0);
+    if (a.writes) {
+        const int cw = 32 * wave + 4 * (lane & 7);
+#pragma unroll
+        for (int i0 = 0; i0 < NP; i0 += 8) {
+            const int i = i0 + (lane >> 3);
+            if (i < N)
+                __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(&s_row[NP + i][cw]),
+                                            reinterpret_cast<f32x4*>(a.writes + row_of(i) * D + cw));
+        }
+    }
+    // o: the last MO row tiles hold (D q) S0; add P u
+#pragma unroll
+    for (int g = 0; g < (NP + 15) / 16; ++g) {
+        f32x2 u[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int k = 16 * g + 4 * q4 + s;
+            u[s] = f32x2{0.f, 0.f};
+            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const f32x2*>(&s_row[NP + (k & (NP - 1))][c2]);
+        }
+#pragma unroll
+        for (int m = g; m < MO; ++m) {
+            const int i = NP >= 16 ? 16 * m + m16 : m16 - 8;  // the node of this lane's row
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = 16 * g + 4 * q4 + s;
+                const float p = k <= i ? s_pa[i & (NP - 1)][k & (NP - 1)] : 0.0f;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    acc[MT - MO + m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, u[s][c], acc[MT - MO + m][c], 0, 0, 0);
+            }
+        }
+    }
+    TOUT* o = static_cast<TOUT*>(a.o);
+#pragma unroll
+    for (int m = 0; m < MO; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = (NP >= 16 ? 16 * m : -8) + 4 * q4 + e;
+            if (i < 0 || i >= N) continue;
+            f32x2 v = {a.scale * acc[MT - MO + m][0][e], a.scale * acc[MT - MO + m][1][e]};
+            if (!(there >> i & 1)) v = f32x2{0.f, 0.f};
+            TOUT* p = o + row_of(i) * D + c2;
+            if constexpr (sizeof(TOUT) == 4) *reinterpret_cast<f32x2*>(p) = v;
+            else *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
+        }
+    if (any_bad) {
+        // rare: NaN for every write that is not finite and for what lies below it
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): over the stores above
+        for (int i = 0; i < N; ++i) {
+            uint64_t above = 0;
+            for (int j = __builtin_amdgcn_readlane(parent, i); j >= 0; j = __builtin_amdgcn_readlane(parent, j))
+                above |= (uint64_t)1 << j;
+            if (!(there >> i & 1) || half) continue;
+            if (!(bad & (above | (uint64_t)1 << i))) continue;
+            if (a.writes) a.writes[row_of(i) * D + col] = __builtin_nanf("");
+            st(o + row_of(i) * D + col, __builtin_nanf(""));
         }
     }
 }
@@ -323,8 +516,10 @@ __global__ __launch_bounds__(CommitMap<TS>::kThreads) void tree_commit_kernel(Tr
 template <typename TIN, typename TOUT, typename TS>
 hipError_t launch_tree_t(const TreeArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(128);
-    if (a.N <= 16) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 16>), grid, block, 0, s, a);
+    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
+    if (a.N <= 8) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 8>), grid, block, 0, s, a);
+    else if (a.N <= 16) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 16>), grid, block, 0, s, a);
+    else if (a.N <= 32) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 32>), grid, block, 0, s, a);
     else hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 64>), grid, block, 0, s, a);
     return hipGetLastError();
 }

@@ -463,46 +463,63 @@ def kda_output_norm_gate_fp8(o, gate, norm_weight, y_codes, y_scales, eps=1e-6, 
     return y_codes, y_scales
 
 
-def _rows(name, t, shape, dtype=None):
-    """Checks a row-strided 2-D tensor: shape, contiguous rows, dtype (if given)."""
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape):
+# --------------------------------------------------------------------------
+# The calls below are made once per token of a decode step, where their host
+# time counts as much as the kernels': one metadata query per fact, the raw
+# stream and the bound function taken directly.
+_DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
+_fns = {}
+
+
+def _code(t, name):
+    c = _DTYPES.get(t.dtype)
+    if c is None:
+        raise TypeError("%s: unsupported dtype %s (float32 or bfloat16 expected)" % (name, t.dtype))
+    return c
+
+
+def _mat(name, t, shape):
+    """Row stride of a [rows, columns] tensor of this shape with contiguous rows
+    (a single row's stride means nothing: its width, rounded up)."""
+    if t.shape != shape:
         raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    ld, one = t.stride()
+    if one != 1 and shape[1] != 1:
         raise ValueError("%s rows must be contiguous" % name)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    return t
+    return ld if shape[0] != 1 else (shape[1] + 15) // 16 * 16
 
 
-def _ld(t):
-    """Row stride of a 2-D tensor (a single row's stride means nothing: its width, rounded up)."""
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 15) // 16 * 16
+def _tensor(name, t, shape):
+    """A dense tensor of this shape."""
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _type(name, t, dtype):
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
 
 
 def _call_on(name, tensors, stream, *args):
-    """_call with the tensors' device current and, without a stream, that
-    device's current stream; tensors on several devices are refused."""
-    device = tensors[0].device
+    """_call on the device that holds all of the tensors (None left out), made
+    current for the call; without a stream on that device's current one."""
+    index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("%s: tensors on several devices (%s, %s)" % (name, device, t.device))
-    if device.index == torch.cuda.current_device():
-        return _call(name, *args, _stream(stream))
-    with torch.cuda.device(device):
-        return _call(name, *args, _stream(stream))
-
-
-def _tensor(name, t, shape, dtype=None):
-    """Checks a dense tensor: shape, contiguous, dtype (if given)."""
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s (got %s)" % (name, tuple(shape), tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s must be %s" % (name, dtype))
-    return _dense(t, name)
+        if t is not None and (t.get_device() != index or index < 0):
+            raise ValueError("%s: all tensors must be on one GPU device (got %s and %s)" % (name, tensors[0].device, t.device))
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != KDA_OK:
+        raise KDAError(name, rc, lib().kda_last_error().decode())
 
 
 def kda_decode_tree(q, k, v, g, beta, parents, state, o, writes=None, scale=1.0, lower_bound=-5.0, stream=None):
@@ -510,20 +527,23 @@ def kda_decode_tree(q, k, v, g, beta, parents, state, o, writes=None, scale=1.0,
     dtype), parents int32 [B,N] (-1 the state, or a node before; anything else
     marks an absent node), state [B,H,128,128] (float32 or bfloat16, read only), o
     [B,N,H,128]; writes float32 [B,N,H,128] or None, for kda_decode_tree_commit."""
-    if q.dim() != 4:
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be [B, N, H, 128]")
-    B, N, H, dk = q.shape
-    for n_, t_, s_ in (("q", q, q.shape), ("k", k, q.shape), ("v", v, (B, N, H, v.shape[-1])), ("g", g, q.shape),
-                       ("beta", beta, (B, N, H))):
-        _tensor(n_, t_, s_, q.dtype)
+    B, N, H, dk = shape
     dv = v.shape[-1]
-    _tensor("parents", parents, (B, N), torch.int32)
-    _tensor("state", state, (B, H, dk, dv))
-    _tensor("o", o, (B, N, H, dv))
-    _tensor("writes", writes, (B, N, H, dv), torch.float32)
-    _call_on("kda_decode_tree", (q, k, v, g, beta, parents, state, o, writes), stream, _ptr(q), _ptr(k), _ptr(v),
-             _ptr(g), _ptr(beta), _dt(q), _ptr(parents), B, N, H, dk, dv, scale, lower_bound, _ptr(state), _dt(state),
-             _ptr(o), _dt(o), _ptr(writes))
+    vshape = (B, N, H, dv)
+    _tensor("q", q, shape), _tensor("k", k, shape), _tensor("g", g, shape), _tensor("v", v, vshape)
+    _tensor("beta", beta, (B, N, H)), _tensor("parents", parents, (B, N)), _tensor("state", state, (B, H, dk, dv))
+    _tensor("o", o, vshape)
+    xd = q.dtype
+    _type("k", k, xd), _type("g", g, xd), _type("v", v, xd), _type("beta", beta, xd), _type("parents", parents, torch.int32)
+    if writes is not None:
+        _tensor("writes", writes, vshape), _type("writes", writes, torch.float32)
+    _call_on("kda_decode_tree", (q, k, v, g, beta, parents, state, o, writes), stream, q.data_ptr(), k.data_ptr(),
+             v.data_ptr(), g.data_ptr(), beta.data_ptr(), _code(q, "q"), parents.data_ptr(), B, N, H, dk, dv, scale,
+             lower_bound, state.data_ptr(), _code(state, "state"), o.data_ptr(), _code(o, "o"),
+             None if writes is None else writes.data_ptr())
     return o
 
 
@@ -531,28 +551,27 @@ def kda_decode_tree_commit(k, g, writes, parents, accepted, state, lower_bound=-
     """state[b] <- the state after node accepted[b] (int32 [B], device) of the tree
     that kda_decode_tree verified with these k, g and parents, and that gave
     writes; any other value of accepted leaves state[b] as it is."""
-    if k.dim() != 4:
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("k must be [B, N, H, 128]")
-    B, N, H, dk = k.shape
+    B, N, H, dk = shape
     dv = writes.shape[-1]
-    _tensor("k", k, k.shape)
-    _tensor("g", g, k.shape, k.dtype)
-    _tensor("writes", writes, (B, N, H, dv), torch.float32)
-    _tensor("parents", parents, (B, N), torch.int32)
-    _tensor("accepted", accepted, (B,), torch.int32)
-    _tensor("state", state, (B, H, dk, dv))
-    _call_on("kda_decode_tree_commit", (k, g, writes, parents, accepted, state), stream, _ptr(k), _ptr(g), _dt(k),
-             _ptr(writes), _ptr(parents), _ptr(accepted), B, N, H, dk, dv, lower_bound, _ptr(state), _dt(state))
+    _tensor("k", k, shape), _tensor("g", g, shape), _tensor("writes", writes, (B, N, H, dv))
+    _tensor("parents", parents, (B, N)), _tensor("accepted", accepted, (B,)), _tensor("state", state, (B, H, dk, dv))
+    _type("g", g, k.dtype), _type("writes", writes, torch.float32)
+    _type("parents", parents, torch.int32), _type("accepted", accepted, torch.int32)
+    _call_on("kda_decode_tree_commit", (k, g, writes, parents, accepted, state), stream, k.data_ptr(), g.data_ptr(),
+             _code(k, "k"), writes.data_ptr(), parents.data_ptr(), accepted.data_ptr(), B, N, H, dk, dv, lower_bound,
+             state.data_ptr(), _code(state, "state"))
     return state
 
 
 def _conv_tree_sizes(x, conv_state, parents):
     B, N = parents.shape
-    W, C = conv_state.shape[1] + 1, conv_state.shape[2]
-    _rows("x", x, (B * N, C))
-    _tensor("conv_state", conv_state, (B, W - 1, C), x.dtype)
-    _tensor("parents", parents, (B, N), torch.int32)
-    return B, N, C, W
+    b, w1, C = conv_state.shape
+    _tensor("conv_state", conv_state, (B, w1, C)), _tensor("parents", parents, (B, N))
+    _type("conv_state", conv_state, x.dtype), _type("parents", parents, torch.int32)
+    return _mat("x", x, (B * N, C)), B, N, C, w1 + 1
 
 
 def kda_conv_tree(x, conv_state, parents, weight, y, bias=None, apply_silu=True, l2norm_group=0, l2norm_eps=1e-6,
@@ -560,37 +579,43 @@ def kda_conv_tree(x, conv_state, parents, weight, y, bias=None, apply_silu=True,
     """The prologue convolution over trees of drafts: x rows [B*N, C] (row strides
     allowed), conv_state [B,W-1,C] (read only), parents int32 [B,N] (as
     kda_decode_tree), weight [C,W], y [B*N,C]."""
-    B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
-    _tensor("weight", weight, (C, W), x.dtype)
-    _tensor("bias", bias, (C,), x.dtype)
-    _tensor("y", y, (B * N, C), x.dtype)
-    _call_on("kda_conv_tree", (x, conv_state, parents, weight, y, bias), stream, _ptr(x), _ld(x), _ptr(conv_state),
-             _ptr(parents), _ptr(weight), _ptr(bias), _dt(x), B, N, C, W, int(bool(apply_silu)), l2norm_group,
-             l2norm_eps, _ptr(y))
+    ld, B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
+    _tensor("weight", weight, (C, W)), _tensor("y", y, (B * N, C))
+    _type("weight", weight, x.dtype), _type("y", y, x.dtype)
+    if bias is not None:
+        _tensor("bias", bias, (C,)), _type("bias", bias, x.dtype)
+    _call_on("kda_conv_tree", (x, conv_state, parents, weight, y, bias), stream, x.data_ptr(), ld, conv_state.data_ptr(),
+             parents.data_ptr(), weight.data_ptr(), None if bias is None else bias.data_ptr(), _code(x, "x"), B, N, C, W,
+             1 if apply_silu else 0, l2norm_group, l2norm_eps, y.data_ptr())
     return y
 
 
 def kda_conv_tree_commit(x, parents, accepted, conv_state, stream=None):
     """conv_state[b] <- the last W-1 inputs of itself followed by the path to node
     accepted[b] of the tree (x, parents as for kda_conv_tree), in place."""
-    B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
-    _tensor("accepted", accepted, (B,), torch.int32)
-    _call_on("kda_conv_tree_commit", (x, parents, accepted, conv_state), stream, _ptr(x), _ld(x), _ptr(parents),
-             _ptr(accepted), _dt(x), B, N, C, W, _ptr(conv_state))
+    ld, B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
+    _tensor("accepted", accepted, (B,)), _type("accepted", accepted, torch.int32)
+    _call_on("kda_conv_tree_commit", (x, parents, accepted, conv_state), stream, x.data_ptr(), ld, parents.data_ptr(),
+             accepted.data_ptr(), _code(x, "x"), B, N, C, W, conv_state.data_ptr())
     return conv_state
 
 
 def _add_rmsnorm_args(x, norm_weight, residual, residual_out):
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [M, K]")
-    _rows("x", x, x.shape)
-    _rows("residual", residual, x.shape)
-    _rows("residual_out", residual_out, x.shape, None if residual is None else residual.dtype)
-    if norm_weight.dtype != torch.float32 or tuple(norm_weight.shape) != (x.shape[1],):
-        raise TypeError("norm_weight must be float32 [K]")
-    r, ro = residual, residual_out
-    return (_ptr(x), _ld(x), _dt(x), _ptr(r), 0 if r is None else _ld(r), _ptr(ro), 0 if ro is None else _ld(ro),
-            KDA_F32 if r is None else _dt(r), _ptr(_dense(norm_weight, "norm_weight")), x.shape[0], x.shape[1])
+    if norm_weight.shape != shape[1:] or norm_weight.dtype != torch.float32 or not norm_weight.is_contiguous():
+        raise TypeError("norm_weight must be dense float32 [K]")
+    res = (None, 0, None, 0, KDA_F32)
+    if residual is not None:
+        rd = _code(residual, "residual")
+        res = (residual.data_ptr(), _mat("residual", residual, shape), None, 0, rd)
+        if residual_out is not None:
+            _type("residual_out", residual_out, residual.dtype)
+            res = res[:2] + (residual_out.data_ptr(), _mat("residual_out", residual_out, shape), rd)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    return (x.data_ptr(), _mat("x", x, shape), _code(x, "x")) + res + (norm_weight.data_ptr(), shape[0], shape[1])
 
 
 def kda_add_rmsnorm(x, norm_weight, y, residual=None, residual_out=None, eps=1e-6, stream=None):
@@ -598,8 +623,8 @@ def kda_add_rmsnorm(x, norm_weight, y, residual=None, residual_out=None, eps=1e-
     y [M, K] (row strides allowed; float32 or bfloat16 each), norm_weight float32
     [K]; residual_out (the residual's dtype) may be residual itself."""
     args = _add_rmsnorm_args(x, norm_weight, residual, residual_out)
-    _rows("y", y, x.shape)
-    _call_on("kda_add_rmsnorm", (x, norm_weight, y, residual, residual_out), stream, *args, eps, _ptr(y), _ld(y), _dt(y))
+    _call_on("kda_add_rmsnorm", (x, norm_weight, y, residual, residual_out), stream, *args, eps, y.data_ptr(),
+             _mat("y", y, x.shape), _code(y, "y"))
     return y
 
 
@@ -607,10 +632,10 @@ def kda_add_rmsnorm_fp8(x, norm_weight, codes, scales, residual=None, residual_o
     """kda_add_rmsnorm with y quantized as kda_quantize_fp8 does: codes uint8
     [M, K] (E4M3), scales float32 [M, K/128]; K a multiple of 128."""
     args = _add_rmsnorm_args(x, norm_weight, residual, residual_out)
-    _rows("codes", codes, x.shape, torch.uint8)
-    _rows("scales", scales, (x.shape[0], x.shape[1] // 128), torch.float32)
+    _type("codes", codes, torch.uint8), _type("scales", scales, torch.float32)
+    M, K = x.shape
     _call_on("kda_add_rmsnorm_fp8", (x, norm_weight, codes, scales, residual, residual_out), stream, *args, eps,
-             _ptr(codes), _ld(codes), _ptr(scales), _ld(scales))
+             codes.data_ptr(), _mat("codes", codes, x.shape), scales.data_ptr(), _mat("scales", scales, (M, K // 128)))
     return codes, scales
 
 
@@ -618,22 +643,26 @@ def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stre
     """C[M,N] = act(A[M,K] B[N,K]^T + bias) + residual (bfloat16 A and B; C and the
     residual float32 or bfloat16; rows may be strided). bias float32 [N];
     activation one of ACTIVATIONS; residual may be C itself."""
-    if A.dim() != 2 or B.dim() != 2:
-        raise ValueError("A must be [M, K] and B [N, K]")
-    if activation not in ACTIVATIONS:
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError("activation must be one of %s (got %r)" % (sorted(ACTIVATIONS), activation))
-    M, K = A.shape
-    N = B.shape[0]
-    _rows("A", A, (M, K))
-    _rows("B", B, (N, K), A.dtype)
-    _rows("C", C, (M, N))
-    _rows("residual", residual, (M, N))
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,)):
-        raise TypeError("bias must be float32 [N]")
-    r = residual
-    _call_on("kda_gemm_epilogue", (A, B, C, bias, residual), stream, _ptr(A), _ld(A), _ptr(B), _ld(B),
-             _ptr(_dense(bias, "bias")), ACTIVATIONS[activation], _ptr(r), 0 if r is None else _ld(r),
-             KDA_F32 if r is None else _dt(r), _ptr(C), _ld(C), M, N, K, _dt(A), _dt(C))
+    ashape, bshape = A.shape, B.shape
+    if len(ashape) != 2 or len(bshape) != 2 or ashape[1] != bshape[1]:
+        raise ValueError("A must be [M, K] and B [N, K] (got %s, %s)" % (tuple(ashape), tuple(bshape)))
+    M, K = ashape
+    N = bshape[0]
+    shape = (M, N)
+    _type("B", B, A.dtype)
+    pb = pr = None
+    ldr, rd = 0, KDA_F32
+    if bias is not None:
+        _tensor("bias", bias, bshape[:1]), _type("bias", bias, torch.float32)
+        pb = bias.data_ptr()
+    if residual is not None:
+        pr, ldr, rd = residual.data_ptr(), _mat("residual", residual, shape), _code(residual, "residual")
+    _call_on("kda_gemm_epilogue", (A, B, C, bias, residual), stream, A.data_ptr(), _mat("A", A, ashape), B.data_ptr(),
+             _mat("B", B, bshape), pb, act, pr, ldr, rd, C.data_ptr(), _mat("C", C, shape), M, N, K, _code(A, "A"),
+             _code(C, "C"))
     return C
 
 
