@@ -440,8 +440,10 @@ static int check_tree(const char* fn, const int32_t* parents, int B, int num_nod
 {
     REQUIRE(B >= 1 && H >= 1 && num_nodes >= 1, KDA_ERR_INVALID_ARG, "%s: B, H and num_nodes must be >= 1", fn);
     REQUIRE(num_nodes <= 64, KDA_ERR_UNSUPPORTED, "%s: at most 64 nodes per tree (got %d)", fn, num_nodes);
-    REQUIRE((int64_t)B * H <= 0x7fffffff && (int64_t)B * num_nodes <= 0x7fffffff, KDA_ERR_INVALID_ARG,
-            "%s: B*H or B*num_nodes too large", fn);
+    // (a tree's rows are addressed through 32-bit offsets)
+    REQUIRE((int64_t)B * H <= 0x7fffffff && (int64_t)B * num_nodes <= 0x7fffffff &&
+                (int64_t)num_nodes * H * 128 <= 0x7fffffff,
+            KDA_ERR_INVALID_ARG, "%s: B*H, B*num_nodes or num_nodes*H too large", fn);
     REQUIRE(parents && (uintptr_t)parents % 4 == 0, KDA_ERR_INVALID_ARG, "%s: parents null or misaligned", fn);
     return KDA_OK;
 }

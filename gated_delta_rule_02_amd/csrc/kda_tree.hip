@@ -30,11 +30,14 @@ constexpr int kMaxNodes = 64;  // one lane of a wavefront per node
 
 // The parent of this lane's node: -1 (the state), a node, or -2 (absent, itself
 // or through a node above it). Every lane of the wavefront takes part.
-__device__ __forceinline__ int tree_parent(const int32_t* parents, int N)
+__device__ __forceinline__ int load_parent(const int32_t* parents, int N)
 {
     const int lane = threadIdx.x & 63;
-    int p = lane < N ? parents[lane] : -2;
-    if (p < -1 || p >= lane) p = -2;
+    return lane < N ? parents[lane] : -2;
+}
+__device__ __forceinline__ int tree_parent(int p)  // p: load_parent()
+{
+    if (p < -1 || p >= (int)(threadIdx.x & 63)) p = -2;
     // pointer doubling: after s steps `up` is the 2^s-th node above, or -1 / -2
     int up = p;
 #pragma unroll
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(256) void conv_tree_kernel(ConvTreeArgs a)
 {
     const int blocks = (a.N + NB - 1) / NB;
     const int b = blockIdx.x / blocks, i0 = (blockIdx.x % blocks) * NB;
-    const int parent = tree_parent(a.parents + (size_t)b * a.N, a.N);
+    const int parent = tree_parent(load_parent(a.parents + (size_t)b * a.N, a.N));
     // The lanes hold the tree: none of them may leave before the last readlane
     // (a lane that has left has no value to read). Lanes past C, in a wavefront
     // that has some inside, work on channel 0 and store nothing.
@@ -152,7 +155,7 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 {
     constexpr int NV = 8 * (int)sizeof(T) / 16;
     const int b = blockIdx.x;
-    const int parent = tree_parent(a.parents + (size_t)b * a.N, a.N);
+    const int parent = tree_parent(load_parent(a.parents + (size_t)b * a.N, a.N));
     const int acc = a.accepted[b];
     if (acc < 0 || acc >= a.N || __builtin_amdgcn_readlane(parent, acc & 63) == -2) return;  // uniform
     int at[W - 1];
@@ -189,16 +192,21 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 //   read   [D k; D q] S0 on the float32 matrix instruction (float32 products
 //          and sums: the results are held to float32 accuracy), two 16-column tiles
 //          per wavefront, rows from LDS, S0 from the registers;
-//   solve  u by forward substitution, each lane a value channel, the remainders
-//          of all nodes in registers: after u_j every r_i below takes - A_ij u_j,
-//          independent operations; then o += P u by the matrix instruction on the
-//          accumulators that already hold (D q) S0.
+//   solve  u by forward substitution in blocks of 16 nodes: the blocks before
+//          by the matrix instruction on the accumulators that hold (D k) S0 - v,
+//          then within the block each lane a value channel, the block's
+//          remainders in registers (after u_j every r_i takes - A_ij u_j,
+//          independent operations); then o += P u by the matrix instruction on
+//          the accumulators that hold (D q) S0.
 // NP: N rounded up to 8, 16, 32 or 64.
-template <int NP> constexpr int kTreeWaves = NP <= 16 ? 4 : (NP == 32 ? 2 : 1);  // wavefronts per SIMD (LDS, registers)
+#ifndef TREE_W
+#define TREE_W 4
+#endif
+template <int NP> constexpr int kTreeWaves = NP <= 16 ? TREE_W : (NP == 32 ? 2 : 1);  // wavefronts per SIMD (LDS, registers)
 
 // f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
-// constants from the start (a loop unrolled late left the 32 remainders of the
-// substitution in one 32-register tuple, copied and spilled at every update).
+// constants from the start (a loop unrolled late left the remainders of the
+// substitution in one tuple of registers, copied and spilled at every update).
 template <typename F, int... I>
 __device__ __forceinline__ void static_for(F&& f, std::integer_sequence<int, I...>)
 {
@@ -218,15 +226,38 @@ __device__ __forceinline__ float add_ror(float v)
 }
 __device__ __forceinline__ float sum16(float v) { return add_ror<1>(add_ror<2>(add_ror<4>(add_ror<8>(v)))); }
 
+// Four or two consecutive inputs as they are stored.
+template <typename T> struct Raw;
+template <> struct Raw<float> {
+    typedef f32x4 R4;
+    typedef f32x2 R2;
+    __device__ static f32x4 f4(const R4& v) { return v; }
+    __device__ static f32x2 f2(const R2& v) { return v; }
+};
+template <> struct Raw<bf16_t> {
+    typedef uint2 R4;
+    typedef uint32_t R2;
+    __device__ static f32x2 f2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
+    __device__ static f32x4 f4(const uint2& u)
+    {
+        const f32x2 a = f2(u.x), b = f2(u.y);
+        return f32x4{a.x, a.y, b.x, b.y};
+    }
+};
+
 // Two consecutive state elements, streamed once.
 __device__ __forceinline__ f32x2 state2(const float* p) { return __builtin_nontemporal_load(reinterpret_cast<const f32x2*>(p)); }
 __device__ __forceinline__ f32x2 unpack2(f32x2 v) { return v; }
 __device__ __forceinline__ uint32_t state2(const bf16_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)); }
 __device__ __forceinline__ f32x2 unpack2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
 
+#ifndef TREE_AHEAD
+#define TREE_AHEAD (NP > 16 || sizeof(TS) == 2)
+#endif
 template <typename TIN, typename TOUT, typename TS, int NP>
 __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeArgs a)
 {
+    constexpr bool kAhead = TREE_AHEAD;
     constexpr int LD = D + 4;                  // row of the decayed rows: 16 rows at one column meet distinct banks
     constexpr int LP = NP + 4;
     constexpr int MT = 2 * NP / 16;            // row tiles: D k, then D q (NP = 8: one tile holds both)
@@ -242,7 +273,39 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     const int m16 = lane & 15, q4 = lane >> 4;
     const int N = a.N;
 
-    // load: element s of group g is row 16 g + 4 q4 + s, columns 32 w + 2 m16 and + 1
+    // load. First what the walk needs, then the state: loads return in order, so
+    // the walk waits for the small ones alone and runs while the state arrives.
+    // (Places past the end read the last node's rows; unused.)
+    typedef Raw<TIN> R;
+    constexpr int KR = NP / 8, WR = (NP + 15) / 16;  // rows of k and g a thread, nodes a 16-lane group walks
+    const size_t base = ((size_t)b * N * a.H + h) * D;
+    auto at = [&](int i) { return (uint32_t)min(i, N - 1) * (uint32_t)(a.H * D); };  // row of node i from `base`
+    const TIN* pk = static_cast<const TIN*>(a.k) + base;
+    const TIN* pg = static_cast<const TIN*>(a.g) + base;
+    const TIN* pq_ = static_cast<const TIN*>(a.q) + base;
+    const TIN* pv = static_cast<const TIN*>(a.v) + base;
+    const int c2 = 32 * wave + 2 * m16;  // this lane's two value channels
+    const int parent_in = load_parent(a.parents + (size_t)b * N, N);
+    typename R::R4 rk[KR], rg[KR], rq[WR][2];
+    typename R::R2 rv[MO][4];
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+        const uint32_t o = at((t >> 5) + 8 * r) + 4 * (t & 31);
+        rk[r] = *reinterpret_cast<const typename R::R4*>(pk + o);
+        rg[r] = *reinterpret_cast<const typename R::R4*>(pg + o);
+    }
+#pragma unroll
+    for (int r = 0; r < WR; ++r)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            rq[r][p] = *reinterpret_cast<const typename R::R4*>(pq_ + at(16 * r + 4 * wave + q4) + 64 * p + 4 * m16);
+#pragma unroll
+    for (int m = 0; m < MO; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rv[m][e] = *reinterpret_cast<const typename R::R2*>(pv + at(16 * m + 4 * q4 + e) + c2);
+    const float beta = ld(static_cast<const TIN*>(a.beta) + ((size_t)b * N + min(t, N - 1)) * a.H + h);
+    asm volatile("" ::: "memory");
+    // element s of group g is row 16 g + 4 q4 + s, columns c2 and c2 + 1
     // (a uniform base, a 32-bit lane offset and constants: one address register)
     const TS* S = static_cast<const TS*>(a.state) + (size_t)bh * D * D + 32 * wave;
     const uint32_t s_off = 4 * q4 * D + 2 * m16;
@@ -251,47 +314,92 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     for (int g = 0; g < 8; ++g)
 #pragma unroll
         for (int s = 0; s < 4; ++s) raw[g][s] = state2(S + 16 * g * D + (s_off + s * D));
+    asm volatile("" ::: "memory");
 
-    const int parent = tree_parent(a.parents + (size_t)b * N, N);
+    const int parent = tree_parent(parent_in);
     const uint64_t there = __ballot(parent != -2);  // lanes past N hold -2
     auto row_of = [&](int i) { return ((size_t)b * N + i) * a.H + h; };
     if (wave == 0) s_par[lane] = parent;
-    for (int i = t >> 5; i < N; i += 8) {
-        const int c = 4 * (t & 31);
-        if (!(there >> i & 1)) continue;
-        *reinterpret_cast<f32x4*>(&s_k[i][c]) = ld4(static_cast<const TIN*>(a.k) + row_of(i) * D + c);
-        f32x4 g = ld4(static_cast<const TIN*>(a.g) + row_of(i) * D + c);
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+        const int i = (t >> 5) + 8 * r, c = 4 * (t & 31);
+        f32x4 g = R::f4(rg[r]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[e] = __expf(fmaxf(g[e], a.lower_bound));
+        *reinterpret_cast<f32x4*>(&s_k[i][c]) = R::f4(rk[r]);
         *reinterpret_cast<f32x4*>(&s_al[i][c]) = g;
     }
-    if (t < NP) s_beta[t] = there >> t & 1 ? ld(static_cast<const TIN*>(a.beta) + row_of(t)) : 0.0f;
+    if (t < NP) s_beta[t] = beta;
     for (int e = t; e < NP * LP; e += 256) (&s_pa[0][0])[e] = 0.0f;
-    __syncthreads();
+    lds_barrier();
+
+    // the products' accumulators: rows 4 q4 + e of a tile, columns c2 and c2 + 1.
+    // The tiles of (D k) S0 start at -v, so that they end at minus the
+    // substitution's right-hand side.
+    f32x4 acc[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            acc[m][0][e] = acc[m][1][e] = 0.0f;
+            if (m < MO && (NP >= 16 || q4 < 2)) {
+                const f32x2 v = R::f2(rv[m][e]);
+                acc[m][0][e] = -v.x;
+                acc[m][1][e] = -v.y;
+            }
+        }
 
     // walk: node i by 16 lanes, lane channels 4 m16 .. and 64 + 4 m16 ..
-    for (int i = 4 * wave + q4; i < NP; i += 16) {
-        int j = i < N && (there >> i & 1) ? i : -1;
+#pragma unroll
+    for (int n = 0; n < WR; ++n) {
+        const int i = 16 * n + 4 * wave + q4;
+        if (i >= NP) break;
+        int j = there >> i & 1 ? i : -1;
         f32x4 q[2], k[2], decay[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             q[p] = k[p] = f32x4{0.f, 0.f, 0.f, 0.f};
             decay[p] = f32x4{1.f, 1.f, 1.f, 1.f};
             if (j >= 0) {
-                q[p] = ld4(static_cast<const TIN*>(a.q) + row_of(i) * D + 64 * p + 4 * m16);
+                q[p] = R::f4(rq[n][p]);
                 k[p] = *reinterpret_cast<const f32x4*>(&s_k[i][64 * p + 4 * m16]);
             }
         }
+        // kAhead: k and alpha of the next node up are read while this one's products run
+        f32x4 kj[2] = {k[0], k[1]}, al[2];
+        auto read_al = [&](int n) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) al[p] = *reinterpret_cast<const f32x4*>(&s_al[n][64 * p + 4 * m16]);
+        };
+        auto read_k = [&](int n, f32x4* to) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) to[p] = *reinterpret_cast<const f32x4*>(&s_k[n][64 * p + 4 * m16]);
+        };
+        int up = j;
+        if (j >= 0) {
+            up = s_par[j];
+            if constexpr (kAhead) read_al(j);
+        }
         while (j >= 0) {
+            const int next = max(up, 0), up2 = s_par[next];
+            f32x4 kn[2], an[2];
+            if constexpr (kAhead) {
+                read_k(next, kn);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) an[p] = *reinterpret_cast<const f32x4*>(&s_al[next][64 * p + 4 * m16]);
+            } else {
+                read_k(j, kj);
+                read_al(j);
+            }
             float pq = 0.0f, pk = 0.0f;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const f32x4 kj = *reinterpret_cast<const f32x4*>(&s_k[j][64 * p + 4 * m16]) * decay[p];
-                decay[p] *= *reinterpret_cast<const f32x4*>(&s_al[j][64 * p + 4 * m16]);
+                kj[p] *= decay[p];
+                decay[p] *= al[p];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    pq += q[p][e] * kj[e];
-                    pk += k[p][e] * kj[e];
+                    pq += q[p][e] * kj[p][e];
+                    pk += k[p][e] * kj[p][e];
                 }
             }
             pq = sum16(pq);
@@ -300,7 +408,15 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
                 s_pa[i][j] = pq;
                 if (j != i) s_pa[j][i] = pk;
             }
-            j = s_par[j];
+            j = up;
+            up = up2;
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    kj[p] = kn[p];
+                    al[p] = an[p];
+                }
+            }
         }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -308,15 +424,10 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
             *reinterpret_cast<f32x4*>(&s_row[NP + i][64 * p + 4 * m16]) = q[p] * decay[p];
         }
     }
-    __syncthreads();
+    lds_barrier();
 
     // read: lane (m16, q4) gives row m16 of a tile, K element 16 g + 4 q4 + s in
     // step (g, s), and takes rows 4 q4 + e of column tile c (columns 2 m16 + c)
-    f32x4 acc[MT][2];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) acc[m][c] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
         f32x4 row[MT];
@@ -331,50 +442,54 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
                 for (int c = 0; c < 2; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[m][s], st[c], acc[m][c], 0, 0, 0);
         }
     }
-    __syncthreads();  // s_row is read: its halves now hold (D k) S0 and u, each wavefront its own columns
-    const int c2 = 32 * wave + 2 * m16;
-#pragma unroll
-    for (int m = 0; m < MO; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (NP >= 16 || q4 < 2)
-                *reinterpret_cast<f32x2*>(&s_row[16 * m + 4 * q4 + e][c2]) = f32x2{acc[m][0][e], acc[m][1][e]};
-
+    lds_barrier();  // s_row is read: its halves now hold (D k) S0 and u, each wavefront its own columns
     __builtin_amdgcn_sched_barrier(0);
 
     // solve: both halves of the wavefront hold the same channel and the same values
     const int col = 32 * wave + (lane & 31), half = lane >> 5;
-    float r[NP];
-    static_for<NP>([&](auto i) {
-        // no branch: a place past the end reads the last node's, an absent one its own
-        const TIN* vi = static_cast<const TIN*>(a.v) + row_of(min((int)i, N - 1)) * D;
-        const float v = ld(vi + (uint32_t)col) - s_row[i][col];
-        r[i] = there >> i & 1 ? v : 0.0f;
-        if constexpr (i % 16 == 15) __builtin_amdgcn_sched_barrier(0);
-    });
     // An infinite or NaN write must reach the nodes below it and no others, but
     // the sums below run over all nodes with coefficients 0 where there is no
     // path. So such a write enters the sums as 0, and is noted: it and what lies
     // below it become NaN at the end. (No branch in here: the compiler would sink
     // the updates past it, to where their r is used, and keep every A alive.)
     uint64_t bad = 0;
-    static_for<NP>([&](auto J) {
-        constexpr int j = J;
-        const float u = there >> j & 1 ? s_beta[j] * r[j] : 0.0f;
-        const bool fine = fabsf(u) < __builtin_inff();
-        const float w = fine ? u : 0.0f;
-        if (!fine) bad |= (uint64_t)1 << j;
-        s_row[NP + j][col] = w;
-        static_for<NP / 4>([&](auto n) {
-            if constexpr (4 * n + 3 > j) {
-                const f32x4 A = *reinterpret_cast<const f32x4*>(&s_pa[j][4 * n]);
+    static_for<MO>([&](auto I) {
+        // the blocks before: (D k) S0 - v + A u on the accumulators
+        static_for<I>([&](auto J) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (4 * n + e > j) r[4 * n + e] -= A[e] * w;
+            for (int s = 0; s < 4; ++s) {
+                const int k = 16 * J + 4 * q4 + s;
+                const float A = s_pa[k][16 * I + m16];
+                const f32x2 u = *reinterpret_cast<const f32x2*>(&s_row[NP + k][c2]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) acc[I][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(A, u[c], acc[I][c], 0, 0, 0);
             }
         });
-        // rows of A at most two ahead: all of them at once spill
-        if constexpr (j % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (NP >= 16 || q4 < 2)
+                *reinterpret_cast<f32x2*>(&s_row[16 * I + 4 * q4 + e][c2]) = f32x2{acc[I][0][e], acc[I][1][e]};
+        // within the block
+        constexpr int BN_ = NP < 16 ? NP : 16, i0 = 16 * I;
+        float r[BN_];
+        static_for<BN_>([&](auto n) { r[n] = -s_row[i0 + n][col]; });
+        static_for<BN_>([&](auto J) {
+            constexpr int j = J;
+            const float u = there >> (i0 + j) & 1 ? s_beta[i0 + j] * r[j] : 0.0f;
+            const bool fine = fabsf(u) < __builtin_inff();
+            const float w = fine ? u : 0.0f;
+            if (!fine) bad |= (uint64_t)1 << (i0 + j);
+            s_row[NP + i0 + j][col] = w;
+            static_for<BN_ / 4>([&](auto n) {
+                if constexpr (4 * n + 3 > j) {
+                    const f32x4 A = *reinterpret_cast<const f32x4*>(&s_pa[i0 + j][i0 + 4 * n]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * n + e > j) r[4 * n + e] -= A[e] * w;
+                }
+            });
+        });
+        __builtin_amdgcn_sched_barrier(0);
     });
     const bool any_bad = __any(bad != 0);
     if (a.writes) {
@@ -461,7 +576,7 @@ __global__ __launch_bounds__(CommitMap<TS>::kThreads) void tree_commit_kernel(Tr
     __shared__ float s_decay[D];
     const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
     const int N = a.N, t = threadIdx.x;
-    const int parent = tree_parent(a.parents + (size_t)b * N, N);
+    const int parent = tree_parent(load_parent(a.parents + (size_t)b * N, N));
     const int acc = a.accepted[b];
     if (acc < 0 || acc >= N || __builtin_amdgcn_readlane(parent, acc & 63) == -2) return;  // uniform over the workgroup
     const int c0 = kCols * (t % M::kLanesPerRow), rg = t / M::kLanesPerRow;
