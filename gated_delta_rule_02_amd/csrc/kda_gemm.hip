@@ -24,6 +24,8 @@
 // 8-byte (bfloat16) access.
 // The fallback (any K multiple of 8): 128 x 128 tiles, 2 x 2 wavefronts of
 // 64 x 64, K steps of 32 through double-buffered LDS.
+#include <cmath>
+
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -67,6 +69,20 @@ __device__ __forceinline__ f32x4 epilogue4(const GemmArgs& a, int64_t row, int64
         v += a.r_dtype == F32 ? ld4(static_cast<const float*>(a.res) + i) : ld4(static_cast<const bf16_t*>(a.res) + i);
     }
     return v;
+}
+
+// Workgroup -> tile of the epilogue entry's tiled kernels. Workgroup ids go round
+// the 8 XCDs, each with an L2 of its own: every XCD takes one contiguous eighth of
+// the tile list, and the list runs through the M tiles of a group of 8, then the
+// N tiles, then the groups, so that the tiles of an XCD that run together share
+// their rows of A and B.
+__device__ __forceinline__ void xcd_tile(int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    const int T = tiles_m * tiles_n, xcd = blockIdx.x & 7, per = T >> 3, rem = T & 7;
+    const int tile = xcd * per + min(xcd, rem) + (int)(blockIdx.x >> 3);
+    const int g = tile / (8 * tiles_n), rows = min(8, tiles_m - 8 * g), r = tile - g * 8 * tiles_n;
+    tm = 8 * g + r % rows;
+    tn = r / rows;
 }
 
 // Columns col .. col + 3 of a row's residual (0 past N).
@@ -268,7 +284,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // tiles: consecutive workgroup ids run down a column of M tiles, so the
     // workgroups resident together share B tiles and a few A tiles
     const int tiles_m = (int)((a.M + TM - 1) / TM);
-    const int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    int tm = blockIdx.x % tiles_m, tn = blockIdx.x / tiles_m;
+    if constexpr (EPI) xcd_tile(tiles_m, (int)((a.N + TNW - 1) / TNW), tm, tn);
     const int64_t m0 = (int64_t)tm * TM, n0 = (int64_t)tn * TNW;
 
     // operand rows past M or N read as zero through the descriptor ranges
@@ -501,7 +518,9 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a)
     const int m16 = lane & 15, q4 = lane >> 4;
     const int wm = (wave / WN) * (TMx / WM), wn = (wave % WN) * (TNx / WN);
     const int tiles_m = (int)((a.M + TMx - 1) / TMx);
-    const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * TMx, n0 = (int64_t)(blockIdx.x / tiles_m) * TNx;
+    int tm, tn;
+    xcd_tile(tiles_m, (int)((a.N + TNx - 1) / TNx), tm, tn);
+    const int64_t m0 = (int64_t)tm * TMx, n0 = (int64_t)tn * TNx;
     const int64_t rows_a = min<int64_t>(TMx, a.M - m0), rows_b = min<int64_t>(TNx, a.N - n0);
     const rsrc_t ra = make_rsrc(static_cast<const bf16_t*>(a.A) + m0 * a.lda, ((rows_a - 1) * a.lda + a.K) * 2);
     const rsrc_t rb = make_rsrc(static_cast<const bf16_t*>(a.B) + n0 * a.ldb, ((rows_b - 1) * a.ldb + a.K) * 2);
@@ -564,91 +583,106 @@ __global__ __launch_bounds__(WM * WN * 64) void gemm_tile_kernel(GemmArgs a)
     tile_epilogue<TC, NI, NJ>(a, acc, reinterpret_cast<float*>(smem) + wave * kEpiFloats<NJ>, m0 + wm, n0 + wn);
 }
 
-// ------------------------------------------------------------ few rows
-// C for up to 16 MT rows of A (decode): bound by reading B once. A workgroup
-// takes 16 rows of B (columns of C) and its KS wavefronts a KS-th of K each;
-// fragments go straight from memory into registers, kFewDepth K steps of 64 (a
-// row's 128-byte line) in flight at a time, and the partial tiles are summed
-// in LDS. Rows past M and N repeat the last one (their results are dropped), so
-// every address is inside its matrix; the last, partial K step masks its lanes.
-constexpr int kFewDepth = 4;
-
-template <typename TC, int MT, int KS>
-__global__ __launch_bounds__(KS * 64) void gemm_few_kernel(GemmArgs a)
+// ------------------------------------------------------------ small tiles, K split
+// 16 MT x 16 NT tiles of C by KS wavefronts that split K: wavefront w takes the
+// K steps w, w + KS, ... of 64 on its own, through its own ring of S LDS stages, so
+// that the loop has no barrier, a fragment read from LDS serves MT (NT) products,
+// and every wavefront keeps S - 1 steps of loads under way. What bounds it is how
+// fast a compute unit takes in the (16 MT + 16 NT) rows of its tile, so the
+// launcher picks the tile that gives every compute unit the fewest bytes. The
+// partial tiles are summed in LDS in a fixed order, a row of MFMA tiles per
+// wavefront. Rows past M or N and chunks past K lie outside the descriptors and
+// read as zero.
+template <typename TC, int MT, int NT, int KS, int S>
+__global__ __launch_bounds__(KS * 64) void gemm_ring_kernel(GemmArgs a)
 {
-    __shared__ f32x4 part[KS - 1][MT][64];
+    constexpr int kStage = (MT + NT) * 2048;      // bytes: 16 (MT + NT) rows of 128
+    constexpr int kRing = S * kStage, kPart = MT * NT * 1024;
+    constexpr int kCopies = 2 * (MT + NT);        // 1 KiB copies per stage
+    static_assert(kPart + kEpiFloats<NT> * 4 <= kRing, "a partial tile and the epilogue's rows fit the ring");
+    static_assert(KS * kRing <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[KS * kRing];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m16 = lane & 15, q4 = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    // this wavefront's K range, in whole steps of 64
-    const int64_t steps = (a.K + 63) / 64;
-    const int64_t s0 = steps * wave / KS, s1 = steps * (wave + 1) / KS;
-    const bf16_t* pb = static_cast<const bf16_t*>(a.B) + min<int64_t>(n0 + m16, a.N - 1) * a.ldb + 8 * q4;
-    const bf16_t* pa[MT];
+    int tm, tn;
+    xcd_tile((int)((a.M + 16 * MT - 1) / (16 * MT)), (int)((a.N + 16 * NT - 1) / (16 * NT)), tm, tn);
+    const int64_t m0 = (int64_t)tm * 16 * MT, n0 = (int64_t)tn * 16 * NT;
+    const int rows_a = (int)min<int64_t>(16 * MT, a.M - m0), rows_b = (int)min<int64_t>(16 * NT, a.N - n0);
+    const rsrc_t ra = make_rsrc(static_cast<const bf16_t*>(a.A) + m0 * a.lda, ((rows_a - 1) * a.lda + a.K) * 2);
+    const rsrc_t rb = make_rsrc(static_cast<const bf16_t*>(a.B) + n0 * a.ldb, ((rows_b - 1) * a.ldb + a.K) * 2);
+    uint8_t* ring = smem + wave * kRing;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)ring;
+    const int lrow = lane >> 3, lslot = lane & 7;
+    const int nk = (int)((a.K + 63) / 64), mine = (nk - wave + KS - 1) / KS;  // this wavefront's steps
+    auto copy = [&](int i) {
+        const int kt = wave + i * KS, st = i % S;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+            const bool isa = c < 2 * MT;
+            const int r = 8 * (isa ? c : c - 2 * MT) + lrow;
+            const int k = kt * 64 + (lslot ^ ((r >> 1) & 7)) * 8;
+            const int off = k < a.K && r < (isa ? rows_a : rows_b) ? (int)((r * (isa ? a.lda : a.ldb) + k) * 2)
+                                                                   : (int)0x80000000;  // outside either descriptor
+            lds_void* dst = (lds_void*)(uintptr_t)(lds0 + st * kStage + c * 1024);
+            if (isa) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, off, 0, 0, 0);
+            else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, off, 0, 0, 0);
+        }
+    };
+    f32x4 acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        pa[i] = static_cast<const bf16_t*>(a.A) + min<int64_t>(16 * i + m16, a.M - 1) * a.lda + 8 * q4;
-    f32x4 acc[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto product = [&](const u32x4_t& fb, const u32x4_t& fa, f32x4& c) {
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb), __builtin_bit_cast(bf16x8, fa), c, 0,
-                                                    0, 0);
-    };
-    int64_t s = s0;
-    for (; s + kFewDepth <= s1 && (s + kFewDepth) * 64 <= a.K; s += kFewDepth) {
-        u32x4_t fb[kFewDepth][2], fa[kFewDepth][2][MT];
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int d = 0; d < kFewDepth; ++d)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t k = (s + d) * 64 + 32 * h;
-                fb[d][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(pb + k));
-#pragma unroll
-                for (int i = 0; i < MT; ++i) fa[d][h][i] = ld16(pa[i] + k);
-            }
-#pragma unroll
-        for (int d = 0; d < kFewDepth; ++d)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) product(fb[d][h], fa[d][h][i], acc[i]);
-    }
-    for (; s < s1; ++s)
+    for (int p = 0; p < S - 1; ++p)
+        if (p < mine) copy(p);
+    for (int i = 0; i < mine; ++i) {
+        // this step's copies have landed (the later steps' may be under way), and
+        // the last step's fragments, whose stage is refilled now, are read
+        constexpr int kAhead = (S - 2) * kCopies;
+        static_assert(kAhead < 64, "copies the wait can count");
+        asm volatile("" ::: "memory");
+        if (i + S - 1 <= mine) __builtin_amdgcn_s_waitcnt(0x0070 | (kAhead & 15) | ((kAhead >> 4) << 14));
+        else __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        asm volatile("" ::: "memory");
+        if (i + S - 1 < mine) copy(i + S - 1);
+        const uint8_t* sa = ring + (i % S) * kStage;
+        const uint8_t* sb = sa + MT * 2048;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t k = s * 64 + 32 * h;
-            const bool in = k + 8 * q4 < a.K;  // K is a multiple of 8: a lane's 8 elements are in or out together
-            const u32x4_t zero = {0u, 0u, 0u, 0u};
-            const u32x4_t fb = in ? ld16(pb + k) : zero;
+            u32x4_t fa[MT], fb[NT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) product(fb, in ? ld16(pa[i] + k) : zero, acc[i]);
+            for (int m = 0; m < MT; ++m) fa[m] = *reinterpret_cast<const u32x4_t*>(sa + swz(16 * m + m16, 4 * h + q4));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) fb[n] = *reinterpret_cast<const u32x4_t*>(sb + swz(16 * n + m16, 4 * h + q4));
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[n]),
+                                                                        __builtin_bit_cast(bf16x8, fa[m]), acc[m][n], 0,
+                                                                        0, 0);
         }
-    // acc[i] holds C^T: lane (m16, q4) element e is C[row 16i + m16][column n0 + 4 q4 + e]
-    if (wave > 0) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i) part[wave - 1][i][lane] = acc[i];
     }
-    __syncthreads();
-    if (wave > 0) return;
+    // every wavefront's partial tile at the start of its ring
+    f32x4* part = reinterpret_cast<f32x4*>(ring);
 #pragma unroll
-    for (int w = 0; w < KS - 1; ++w)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[i] += part[w][i][lane];
-    TC* Cp = static_cast<TC*>(a.C);
-    const int64_t col = n0 + 4 * q4;
+        for (int n = 0; n < NT; ++n) part[(m * NT + n) * 64 + lane] = acc[m][n];
+    lds_barrier();
+#pragma unroll 1
+    for (int m = wave; m < MT; m += KS) {
+        f32x4 sum[1][NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t row = 16 * i + m16;
-        if (row >= a.M) continue;
-        if (col + 3 < a.N) {
-            st4(Cp + row * a.ldc + col, epilogue4(a, row, col, acc[i]));
-        } else {
+        for (int n = 0; n < NT; ++n) {
+            sum[0][n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (col + e < a.N) st(Cp + row * a.ldc + col + e, epilogue1(a, row, col + e, acc[i][e]));
+            for (int w = 0; w < KS; ++w)
+                sum[0][n] += *reinterpret_cast<const f32x4*>(smem + w * kRing + ((m * NT + n) * 64 + lane) * 16);
         }
+        tile_epilogue<TC, 1, NT>(a, sum, reinterpret_cast<float*>(ring + kPart), m0 + 16 * m, n0);
     }
 }
 
@@ -705,23 +739,6 @@ hipError_t launch_gemm(const GemmArgs& a, hipStream_t s)
 
 namespace {
 
-template <typename TC>
-hipError_t launch_few(const GemmArgs& a, hipStream_t s)
-{
-    const dim3 grid((unsigned)((a.N + 15) / 16)), block(256);
-    switch ((a.M + 15) / 16) {
-        case 1: hipLaunchKernelGGL((gemm_few_kernel<TC, 1, 4>), grid, block, 0, s, a); break;
-        case 2: hipLaunchKernelGGL((gemm_few_kernel<TC, 2, 4>), grid, block, 0, s, a); break;
-        case 3: hipLaunchKernelGGL((gemm_few_kernel<TC, 3, 4>), grid, block, 0, s, a); break;
-        default: hipLaunchKernelGGL((gemm_few_kernel<TC, 4, 4>), grid, block, 0, s, a); break;
-    }
-    return hipGetLastError();
-}
-
-}  // namespace
-
-namespace {
-
 template <typename TC, int TMx, int TNx, int WM, int WN, int STAGES>
 hipError_t launch_tile(const GemmArgs& a, hipStream_t s)
 {
@@ -731,16 +748,56 @@ hipError_t launch_tile(const GemmArgs& a, hipStream_t s)
 }
 
 template <typename TC>
+hipError_t launch_256(const GemmArgs& a, hipStream_t s)
+{
+    const int64_t tiles = ((a.M + TM - 1) / TM) * ((a.N + TN - 1) / TN);
+    hipLaunchKernelGGL((gemm256_kernel<TC, 8, true>), dim3((unsigned)tiles), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename TC, int MT, int NT, int KS, int S>
+hipError_t launch_ring(const GemmArgs& a, hipStream_t s)
+{
+    const int64_t tiles = ((a.M + 16 * MT - 1) / (16 * MT)) * ((a.N + 16 * NT - 1) / (16 * NT));
+    hipLaunchKernelGGL((gemm_ring_kernel<TC, MT, NT, KS, S>), dim3((unsigned)tiles), dim3(KS * 64), 0, s, a);
+    return hipGetLastError();
+}
+
+// The form with the least cost: rounds of tiles over the 256 compute units, times the
+// rows of A and B that a tile takes in (K values each), times what a row costs in that form
+// relative to the K-split tiles. Those are bound by taking their rows in, so any
+// tile costs about its rows (measured at K = 8192, us per row and round: 64 x 64
+// 0.28, 96 x 64 0.245, 64 x 32 0.28, 32 x 32 0.33); the 128 x 128 tiles cost 0.30 a
+// row; the 256 x 256 tiles 0.42 (bound by the matrix instructions instead, and the
+// only ones that reach 1.3 PFLOP/s). 4096 columns, K = 8192, us, this choice | the
+// next tile up: 16 rows 14.5 | 15.2, 64 rows 21.0 | 27.6, 96 rows 23.2 | 32.2, 192
+// rows 32.5 | 36.0, 333 rows 38.8 | 72, 1024 rows 79 | 203, 4096 rows 220 | 302.
+template <typename TC>
 hipError_t launch_epilogue(const GemmArgs& a, hipStream_t s)
 {
-    if (a.M <= 64) return launch_few<TC>(a, s);
-    auto tiles = [&](int64_t tm, int64_t tn) { return ((a.M + tm - 1) / tm) * ((a.N + tn - 1) / tn); };
-    if (a.K % 64 == 0 && tiles(256, 256) >= 256) {
-        hipLaunchKernelGGL((gemm256_kernel<TC, 8, true>), dim3((unsigned)tiles(256, 256)), dim3(256), 0, s, a);
-        return hipGetLastError();
+    struct Form {
+        int tm, tn;
+        float row;
+        hipError_t (*launch)(const GemmArgs&, hipStream_t);
+    };
+    static const Form forms[] = {
+        {16, 16, 1.0f, launch_ring<TC, 1, 1, 8, 4>},   {16, 32, 1.0f, launch_ring<TC, 1, 2, 4, 6>},
+        {32, 16, 1.0f, launch_ring<TC, 2, 1, 4, 6>},   {32, 32, 1.0f, launch_ring<TC, 2, 2, 4, 4>},
+        {64, 32, 1.0f, launch_ring<TC, 4, 2, 4, 3>},   {32, 64, 1.0f, launch_ring<TC, 2, 4, 4, 3>},
+        {48, 64, 1.0f, launch_ring<TC, 3, 4, 4, 2>},   {64, 64, 1.0f, launch_ring<TC, 4, 4, 4, 2>},
+        {96, 64, 1.0f, launch_ring<TC, 6, 4, 4, 2>},   {128, 64, 1.0f, launch_ring<TC, 8, 4, 3, 2>},
+        {128, 128, 1.05f, launch_tile<TC, 128, 128, 4, 2, 4>},
+        {256, 256, 1.45f, launch_256<TC>},  // last: K a multiple of 64 only
+    };
+    constexpr int n = sizeof(forms) / sizeof(forms[0]);
+    const Form* best = nullptr;
+    double least = 0.0;
+    for (int f = 0; f < (a.K % 64 == 0 ? n : n - 1); ++f) {
+        const double tiles = (double)((a.M + forms[f].tm - 1) / forms[f].tm) * (double)((a.N + forms[f].tn - 1) / forms[f].tn);
+        const double cost = std::ceil(tiles / 256.0) * (forms[f].tm + forms[f].tn) * forms[f].row;
+        if (!best || cost < least) best = &forms[f], least = cost;
     }
-    if (tiles(128, 128) >= 256) return launch_tile<TC, 128, 128, 2, 2, 3>(a, s);
-    return launch_tile<TC, 64, 64, 2, 2, 4>(a, s);
+    return best->launch(a, s);
 }
 
 }  // namespace

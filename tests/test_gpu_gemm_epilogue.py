@@ -151,3 +151,25 @@ def test_gemm_epilogue_captured():
             K.kda_gemm_epilogue(A, B, D, bias=b, activation="silu", residual=D)
             torch.cuda.synchronize()
             assert torch.equal(C, D)
+
+
+@pytest.mark.parametrize("M,N,k", [
+    (16, 4096, 136), (9, 8200, 72), (30, 4104, 200), (33, 8192, 136), (64, 4104, 72), (90, 4096, 136), (100, 8190, 72),
+    (192, 4096, 200), (250, 4100, 136), (330, 4104, 72), (333, 4096, 328), (500, 4096, 136), (515, 4104, 72), (1030, 4096, 72),
+    (1000, 4100, 136), (2050, 4096, 64), (4100, 4096, 128), (7000, 260, 192), (5000, 36, 72), (1, 41024, 64),
+])
+def test_gemm_epilogue_wide(M, N, k):
+    """Sizes that fill the compute units once or several times over, in whole and
+    ragged tiles: each tile form, with everything in the epilogue."""
+    announce("gemm_epilogue wide M=%d N=%d K=%d" % (M, N, k))
+    pad = (0, 8, -N % 4)
+    A, B, b, res = make(M, N, k, M + N, pad)
+    r = res[:, :N].bfloat16() if (M + N) % 3 == 0 else res[:, :N]
+    if r.dtype == BF:
+        r = torch.nn.functional.pad(r, (0, pad[2]))[:, :N]
+    C = torch.full((M, N + pad[2]), float("nan"), dtype=BF if M % 2 else F, device="cuda")
+    K.kda_gemm_epilogue(A, B, C[:, :N], bias=b, activation="silu", residual=r)
+    torch.cuda.synchronize()
+    ref, tol = expected(A, B, b, "silu", r)
+    assert check(C[:, :N], ref, tol)
+    assert torch.isnan(C[:, N:]).all()
