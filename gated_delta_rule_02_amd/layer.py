@@ -70,8 +70,27 @@ class KDAMixer:
         T = x.shape[0]
         P = self._buf("P", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm(x, self.W_in, P)
+        return P, self._columns(P)
+
+    def _columns(self, P):
         W = self.W
-        return P, [P[:, i * W:(i + 1) * W] for i in range(5)] + [P[:, 5 * W:5 * W + self.H]]
+        return [P[:, i * W:(i + 1) * W] for i in range(5)] + [P[:, 5 * W:5 * W + self.H]]
+
+    def projections_of_norm(self, x, residual, norm_weight, eps):
+        """The columns of RMSNorm(x + residual) norm_weight W_in^T (bf16); the
+        residual (or None) is updated in place."""
+        T, hidden = x.shape
+        y = self._buf("ny", (T, hidden), torch.bfloat16)
+        K.kda_add_rmsnorm(x, norm_weight, y, residual=residual, residual_out=residual, eps=eps)
+        P = self._buf("nP", (T, self.W_in.shape[0]), torch.bfloat16)
+        K.kda_gemm_epilogue(y, self.W_in, P)
+        return self._columns(P)
+
+    def output_into(self, o, gp, hidden, tag):
+        """hidden += (RMSNorm(o) x w x sigmoid(gate)) W_o^T, in the product's epilogue."""
+        y = self._buf(tag + "y", (o.shape[0], self.W), torch.bfloat16)
+        K.kda_output_norm_gate(o, gp, self.norm_w, y, eps=self.rms_eps)
+        K.kda_gemm_epilogue(y, self.Wo, hidden, residual=hidden)
 
     def output(self, o, gp, tag=""):
         """y = RMSNorm(o) x w x sigmoid(gate) (bf16), out = y W_o^T (float32)."""
@@ -86,9 +105,18 @@ class KDAMixer:
                 conv_state_in=None, conv_state_out=None, return_parts=False):
         """x [T, hidden] bf16 (packed sequences if cu_seqlens is given) ->
         out [T, hidden] float32. Optional conv states are [3, N, 3, H*128]."""
-        T = x.shape[0]
-        H, W = self.H, self.W
-        P, (qp, kp, vp, fp, gp, bp) = self.projections(x)
+        P, cols = self.projections(x)
+        o, qkv = self._core(cols, cu_seqlens, cu_seqlens_host, initial_state, final_state, conv_state_in, conv_state_out)
+        out, y = self.output(o, cols[4])
+        if return_parts:
+            return out, dict(q=qkv[0], k=qkv[1], v=qkv[2], o=o, y=y, P=P)
+        return out
+
+    def _core(self, cols, cu_seqlens=None, cu_seqlens_host=None, initial_state=None, final_state=None,
+              conv_state_in=None, conv_state_out=None):
+        """Convolutions, gate and prefill of the projection columns -> o, (q, k, v)."""
+        qp, kp, vp, fp, _, bp = cols
+        T, H, W = qp.shape[0], self.H, self.W
         qkv = []
         for i, (src, l2) in enumerate(((qp, D), (kp, D), (vp, 0))):
             y = self._buf("c%d" % i, (T, W), torch.bfloat16)
@@ -103,18 +131,20 @@ class KDAMixer:
         K.kda_prefill_gated(qkv[0], qkv[1], qkv[2], fp, bp, self.A_log, o, cu_seqlens=cu_seqlens,
                             cu_seqlens_host=cu_seqlens_host, initial_state=initial_state,
                             final_state=final_state, scale=self.scale, lower_bound=self.lower_bound)
-        out, y = self.output(o, gp)
-        if return_parts:
-            return out, dict(q=qkv[0], k=qkv[1], v=qkv[2], o=o, y=y, P=P)
-        return out
+        return o, qkv
 
     def decode(self, x, state, conv_states):
         """One token per sequence: x [B, hidden] bf16; state float32 [B, H, 128, 128]
         and conv_states bf16 [3, B, 3, H*128] are updated in place. Returns
         out [B, hidden] float32."""
-        B = x.shape[0]
-        H, W = self.H, self.W
-        P, (qp, kp, vp, fp, gp, bp) = self.projections(x)
+        _, cols = self.projections(x)
+        o = self._core_decode(cols, state, conv_states)
+        out, _ = self.output(o, cols[4], tag="d")
+        return out
+
+    def _core_decode(self, cols, state, conv_states):
+        qp, kp, vp, fp, _, bp = cols
+        B, H, W = qp.shape[0], self.H, self.W
         qkv = []
         for i, (src, l2) in enumerate(((qp, D), (kp, D), (vp, 0))):
             y = self._buf("dc%d" % i, (B, W), torch.bfloat16)
@@ -127,8 +157,100 @@ class KDAMixer:
         o = self._buf("do", (B, H, D), torch.float32)
         K.kda_decode_step(qkv[0], qkv[1], qkv[2], g, beta, state, o, scale=self.scale,
                           lower_bound=self.lower_bound)
-        out, _ = self.output(o, gp, tag="d")
-        return out
+        return o
+
+    def decode_tree(self, x, parents, state, conv_states):
+        """Verify a tree of drafted tokens per sequence: x [B, N, hidden] bf16,
+        parents int32 [B, N] (as kda_decode_tree), state [B, H, 128, 128]
+        (float32 or bfloat16) and conv_states bf16 [3, B, 3, H*128] only read.
+        Returns out [B, N, hidden] float32 and the DraftTree that commits an
+        accepted path (both valid until the next call)."""
+        B, N, hidden = x.shape
+        _, cols = self.projections(x.reshape(B * N, hidden))
+        o, tree = self._core_tree(cols, parents, state, conv_states)
+        out, _ = self.output(o.view(B * N, self.H, D), cols[4], tag="t")
+        return out.view(B, N, hidden), tree
+
+    def _core_tree(self, cols, parents, state, conv_states):
+        qp, kp, vp, fp, _, bp = cols
+        B, N = parents.shape
+        H, W = self.H, self.W
+        qkv = []
+        for i, (src, l2) in enumerate(((qp, D), (kp, D), (vp, 0))):
+            y = self._buf("tc%d" % i, (B * N, W), torch.bfloat16)
+            K.kda_conv_tree(src, conv_states[i], parents, self.conv[i], y, apply_silu=True, l2norm_group=l2,
+                            l2norm_eps=self.l2_eps)
+            qkv.append(y.view(B, N, H, D))
+        g = self._buf("tg", (B * N, H, D), torch.bfloat16)
+        beta = self._buf("tbeta", (B * N, H), torch.bfloat16)
+        K.kda_gate_prologue(fp, bp, self.A_log, g, beta, H, D, lower_bound=self.lower_bound)
+        o = self._buf("to", (B, N, H, D), torch.float32)
+        writes = self._buf("tw", (B, N, H, D), torch.float32)
+        g = g.view(B, N, H, D)
+        K.kda_decode_tree(qkv[0], qkv[1], qkv[2], g, beta.view(B, N, H), parents, state, o, writes, scale=self.scale,
+                          lower_bound=self.lower_bound)
+        return o, DraftTree(self, parents, (qp, kp, vp), qkv[1], g, writes)
+
+
+class DraftTree:
+    """What a mixer's verification of a tree leaves for its commit (buffers of
+    the mixer: valid until its next verification)."""
+
+    def __init__(self, mixer, parents, inputs, k, g, writes):
+        self.mixer, self.parents, self.inputs, self.k, self.g, self.writes = mixer, parents, inputs, k, g, writes
+
+    def commit(self, accepted, state, conv_states):
+        """state and conv_states (those that were verified against) advance in place
+        along the path to node accepted[b] (int32 [B]; any other value: unchanged)."""
+        K.kda_decode_tree_commit(self.k, self.g, self.writes, self.parents, accepted, state,
+                                 lower_bound=self.mixer.lower_bound)
+        for x, cs in zip(self.inputs, conv_states):
+            K.kda_conv_tree_commit(x, self.parents, accepted, cs)
+
+
+class KDABlock:
+    """A mixer in its pre-norm residual block: hidden += mixer(RMSNorm(hidden) norm_weight).
+
+    The residual stream `hidden` (bfloat16 or float32 rows) is updated in place.
+    With bfloat16 weights the output projection adds into it (the product's
+    epilogue). With block-FP8 weights the block's output is returned as `delta`,
+    and the next block adds it while it normalises: one pass then updates the
+    stream, norms it and quantizes the projections' input. So every method takes
+    the delta still to be added (None: nothing) and returns the one it leaves
+    (None: added); `finish` adds a last one."""
+
+    def __init__(self, mixer, norm_weight, eps=1e-6):
+        self.mixer, self.norm_weight, self.eps = mixer, norm_weight, eps
+
+    def _enter(self, hidden, delta):
+        """hidden += delta in place; the projections of its norm -> their columns."""
+        m = self.mixer
+        x, residual = (hidden, None) if delta is None else (delta, hidden)
+        return m.projections_of_norm(x, residual, self.norm_weight, self.eps)
+
+    def forward(self, hidden, delta=None, **states):
+        """Prefill: hidden [T, width] rows, states as KDAMixer.forward's arguments."""
+        cols = self._enter(hidden, delta)
+        o, _ = self.mixer._core(cols, **states)
+        return self.mixer.output_into(o, cols[4], hidden, tag="b")
+
+    def decode(self, hidden, state, conv_states, delta=None):
+        """One token per sequence: hidden [B, width], states updated in place."""
+        cols = self._enter(hidden, delta)
+        o = self.mixer._core_decode(cols, state, conv_states)
+        return self.mixer.output_into(o, cols[4], hidden, tag="bd")
+
+    def decode_tree(self, hidden, parents, state, conv_states, delta=None):
+        """A tree of drafts per sequence: hidden [B * N, width]. Returns (delta, DraftTree)."""
+        cols = self._enter(hidden, delta)
+        o, tree = self.mixer._core_tree(cols, parents, state, conv_states)
+        return self.mixer.output_into(o.view(hidden.shape[0], self.mixer.H, D), cols[4], hidden, tag="bt"), tree
+
+    def finish(self, hidden, delta, norm_weight, y):
+        """After the last block: y = RMSNorm(hidden + delta) norm_weight, hidden += delta."""
+        if delta is None:
+            return K.kda_add_rmsnorm(hidden, norm_weight, y, eps=self.eps)
+        return K.kda_add_rmsnorm(delta, norm_weight, y, residual=hidden, residual_out=hidden, eps=self.eps)
 
 
 class DecodeGraph:
@@ -203,8 +325,21 @@ class KDAMixerFP8(KDAMixer):
         K.kda_quantize_fp8(x, xq, xs)
         P = self._buf("P", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm_fp8(xq, xs, self.W_in, self.W_in_s, P)
-        W = self.W
-        return P, [P[:, i * W:(i + 1) * W] for i in range(5)] + [P[:, 5 * W:5 * W + self.H]]
+        return P, self._columns(P)
+
+    def projections_of_norm(self, x, residual, norm_weight, eps):
+        """As KDAMixer's, the norm quantized in the same pass."""
+        T, hidden = x.shape
+        xq = self._buf("nq", (T, hidden), torch.uint8)
+        xs = self._buf("ns", (T, hidden // 128), torch.float32)
+        K.kda_add_rmsnorm_fp8(x, norm_weight, xq, xs, residual=residual, residual_out=residual, eps=eps)
+        P = self._buf("nP", (T, self.W_in.shape[0]), torch.bfloat16)
+        K.kda_gemm_fp8(xq, xs, self.W_in, self.W_in_s, P)
+        return self._columns(P)
+
+    def output_into(self, o, gp, hidden, tag):
+        """The block's output, left for the next norm to add."""
+        return self.output(o, gp, tag)[0]
 
     def output(self, o, gp, tag=""):
         """The epilogue quantized per (token, head), then out = Y W_o^T (float32)."""
