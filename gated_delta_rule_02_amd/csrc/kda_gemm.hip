@@ -785,7 +785,7 @@ hipError_t launch_epilogue(const GemmArgs& a, hipStream_t s)
         {32, 16, 1.0f, launch_ring<TC, 2, 1, 4, 6>},   {32, 32, 1.0f, launch_ring<TC, 2, 2, 4, 4>},
         {64, 32, 1.0f, launch_ring<TC, 4, 2, 4, 3>},   {32, 64, 1.0f, launch_ring<TC, 2, 4, 4, 3>},
         {48, 64, 1.0f, launch_ring<TC, 3, 4, 4, 2>},   {64, 64, 1.0f, launch_ring<TC, 4, 4, 4, 2>},
-        {96, 64, 1.0f, launch_ring<TC, 6, 4, 4, 2>},   {128, 64, 1.0f, launch_ring<TC, 8, 4, 3, 2>},
+        {96, 64, 1.0f, launch_ring<TC, 6, 4, 4, 2>},   {128, 64, 1.2f, launch_ring<TC, 8, 4, 3, 2>},
         {128, 128, 1.05f, launch_tile<TC, 128, 128, 4, 2, 4>},
         {256, 256, 1.45f, launch_256<TC>},  // last: K a multiple of 64 only
     };
