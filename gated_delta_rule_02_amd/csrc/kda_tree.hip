@@ -35,30 +35,17 @@ __device__ __forceinline__ int load_parent(const int32_t* parents, int N)
     const int lane = threadIdx.x & 63;
     return lane < N ? parents[lane] : -2;
 }
-__device__ __forceinline__ int tree_parent(int p, uint64_t& above)  // p: load_parent(); above: the path to this node
+__device__ __forceinline__ int tree_parent(int p)  // p: load_parent()
 {
-    const int lane = threadIdx.x & 63;
-    if (p < -1 || p >= lane) p = -2;
-    // pointer doubling: after s steps `up` is the 2^s-th node above, or -1 / -2,
-    // and `lo`, `hi` hold the nodes up to it
-    int up = p, lo = lane < 32 ? 1 << lane : 0, hi = lane < 32 ? 0 : 1 << (lane - 32);
+    if (p < -1 || p >= (int)(threadIdx.x & 63)) p = -2;
+    // pointer doubling: after s steps `up` is the 2^s-th node above, or -1 / -2
+    int up = p;
 #pragma unroll
     for (int s = 0; s < 6; ++s) {
-        const int from = max(up, 0);
-        const int far = __shfl(up, from, 64), l2 = __shfl(lo, from, 64), h2 = __shfl(hi, from, 64);
-        if (up >= 0) {
-            up = far;
-            lo |= l2;
-            hi |= h2;
-        }
+        const int far = __shfl(up, max(up, 0), 64);
+        if (up >= 0) up = far;
     }
-    above = up == -2 ? 0 : (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo;
     return up == -2 ? -2 : p;
-}
-__device__ __forceinline__ int tree_parent(int p)
-{
-    uint64_t above;
-    return tree_parent(p, above);
 }
 
 // Sum over aligned groups of 16 lanes, in every lane (rotations within the row).
@@ -223,36 +210,29 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 }
 
 // ------------------------------------------------------------ verification
-// One workgroup of four wavefronts per (sequence, head); wavefront w takes channels
-// 32 w .. 32 w + 31 (of the keys, then of the values). Phases:
-//   load   the nodes' inputs, then the wavefront's 128 x 32 part of S0 into registers
-//          (64 for a float32 state): used last, so that it arrives while the rest
-//          of the work up to the products runs;
-//   decay  G_i, the sum of the log-retentions on the path to i, as a matrix
-//          product of the ancestor relation with g; per channel c a center
-//          C = max_i |G_i| / 2, so that exp(G + C) and exp(-G - C) both stay
-//          within exp(+-75);
-//   pairs  all P[i][j] = q_i . D(i,j) k_j and A[i][j] = k_i . D(i,j) k_j at once as
-//          the product of rows exp(G_i + C) (q_i, k_i) with rows exp(-G_j - C) k_j,
-//          kept where j lies above i (P[i][i] = q_i . k_i apart from it, exactly);
-//   read   [D k; D q] S0 (the rows times exp(-C)), two 16-column tiles per
-//          wavefront, rows from LDS, S0 from the registers;
+// One workgroup of four wavefronts per (sequence, head); wavefront w takes value
+// channels 32 w .. 32 w + 31. Four phases:
+//   load   the wavefront's 128 x 32 part of S0 into registers (64 for a float32
+//          state), used last but issued first: the rest of the workgroup's work
+//          up to the products runs while it arrives;
+//   walk   16 lanes per node walk up its path with the running decay, forming
+//          the node's products with every node above it (P with q_i, A with k_i)
+//          and, at the end, the decayed rows D(i) k_i and D(i) q_i. Only pairs on
+//          a path are formed;
+//   read   [D k; D q] S0 on the float32 matrix instruction (float32 products
+//          and sums: the results are held to float32 accuracy), two 16-column tiles
+//          per wavefront, rows from LDS, S0 from the registers;
 //   solve  u by forward substitution in blocks of 16 nodes: the blocks before
 //          by the matrix instruction on the accumulators that hold (D k) S0 - v,
 //          then within the block each lane a value channel, the block's
 //          remainders in registers (after u_j every r_i takes - A_ij u_j,
 //          independent operations); then o += P u by the matrix instruction on
 //          the accumulators that hold (D q) S0.
-// All products are on the float32 matrix instruction: float32 products and sums,
-// the results are held to float32 accuracy.
-// Where the centered factors do not hold (a path with |G| over 150, a positive or
-// non-finite G, a finite key or query entry over 1e4) the workgroup walks instead:
-// 16 lanes per node go up its path with the running product of the alphas and
-// form the pairs one by one, for any decays. Every workgroup walked at first, and
-// that was the longest phase: of 64 trees of 32 nodes (float32 states, 64 heads) it took 73
-// of 188 us, of 32 trees of 64 nodes 154 of 320.
 // NP: N rounded up to 8, 16, 32 or 64.
-template <int NP> constexpr int kTreeWaves = NP <= 16 ? 4 : (NP == 32 ? 2 : 1);  // wavefronts per SIMD (LDS, registers)
+#ifndef TREE_W
+#define TREE_W 4
+#endif
+template <int NP> constexpr int kTreeWaves = NP <= 16 ? TREE_W : (NP == 32 ? 2 : 1);  // wavefronts per SIMD (LDS, registers)
 
 // f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
 // constants from the start (a loop unrolled late left the remainders of the
@@ -268,25 +248,23 @@ __device__ __forceinline__ void static_for(F&& f)
     static_for(f, std::make_integer_sequence<int, N>{});
 }
 
-// exp(x) for |x| <= 150 on the hardware base-2 exponential, with the argument's
-// rounding made up for: x log2(e) in two parts (the rounding alone would cost |x|
-// half-steps of the result, seven digits down to five at the far end).
-__device__ __forceinline__ float exp_full(float x)
-{
-    const float t = x * kLog2e;
-    const float r = fmaf(x, kLog2e, -t) + x * 1.92596303e-8f;  // log2(e) - float(log2(e))
-    return __builtin_amdgcn_exp2f(t) * fmaf(r, kLn2, 1.0f);
-}
-
-// Two consecutive inputs as they are stored.
+// Four or two consecutive inputs as they are stored.
 template <typename T> struct Raw;
 template <> struct Raw<float> {
+    typedef f32x4 R4;
     typedef f32x2 R2;
+    __device__ static f32x4 f4(const R4& v) { return v; }
     __device__ static f32x2 f2(const R2& v) { return v; }
 };
 template <> struct Raw<bf16_t> {
+    typedef uint2 R4;
     typedef uint32_t R2;
     __device__ static f32x2 f2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
+    __device__ static f32x4 f4(const uint2& u)
+    {
+        const f32x2 a = f2(u.x), b = f2(u.y);
+        return f32x4{a.x, a.y, b.x, b.y};
+    }
 };
 
 // Two consecutive state elements, streamed once.
@@ -295,48 +273,58 @@ __device__ __forceinline__ f32x2 unpack2(f32x2 v) { return v; }
 __device__ __forceinline__ uint32_t state2(const bf16_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)); }
 __device__ __forceinline__ f32x2 unpack2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
 
+#ifndef TREE_AHEAD
+#define TREE_AHEAD (NP > 16 || sizeof(TS) == 2)
+#endif
 template <typename TIN, typename TOUT, typename TS, int NP>
 __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeArgs a)
 {
+    constexpr bool kAhead = TREE_AHEAD;
     constexpr int LD = D + 4;                  // row of the decayed rows: 16 rows at one column meet distinct banks
     constexpr int LP = NP + 4;
     constexpr int MT = 2 * NP / 16;            // row tiles: D k, then D q (NP = 8: one tile holds both)
-    constexpr int MO = NP >= 16 ? NP / 16 : 1;  // row tiles of the nodes (of o: the last MO)
+    constexpr int MO = NP >= 16 ? NP / 16 : 1;  // row tiles of o, the last MO
     __shared__ __attribute__((aligned(16))) float s_row[2 * NP][LD];  // D k and D q; then (D k) S0 and the writes u
-    __shared__ __attribute__((aligned(16))) float s_kh[NP][LD];       // exp(-G - C) k
+    __shared__ __attribute__((aligned(16))) float s_k[NP][D], s_al[NP][D];
     // P[i][j] = q_i . D(i,j) k_j at [i][j] (j <= i), A[i][j] = k_i . D(i,j) k_j at [j][i] (j < i)
     __shared__ __attribute__((aligned(16))) float s_pa[NP][LP];
-    __shared__ __attribute__((aligned(16))) float s_er[D];  // exp(-C): s_row to D k and D q
-    __shared__ float s_beta[NP], s_diag[4][NP];
-    __shared__ uint64_t s_anc[64];
-    __shared__ int s_par[64], s_walk[4];
+    __shared__ float s_beta[NP];
+    __shared__ int s_par[64];
     const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
     const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int m16 = lane & 15, q4 = lane >> 4;
     const int N = a.N;
 
-    // load. First the inputs, then the state: loads return in order, so what
-    // follows waits for the inputs alone and runs while the state arrives.
+    // load. First what the walk needs, then the state: loads return in order, so
+    // the walk waits for the small ones alone and runs while the state arrives.
     // (Places past the end read the last node's rows; unused.)
     typedef Raw<TIN> R;
-    typedef typename R::R2 R2;
+    constexpr int KR = NP / 8, WR = (NP + 15) / 16;  // rows of k and g a thread, nodes a 16-lane group walks
     const size_t base = ((size_t)b * N * a.H + h) * D;
     auto at = [&](int i) { return (uint32_t)min(i, N - 1) * (uint32_t)(a.H * D); };  // row of node i from `base`
-    const int c2 = 32 * wave + 2 * m16;  // this lane's two channels
-    auto in2 = [&](const void* p, int i) { return *reinterpret_cast<const R2*>(static_cast<const TIN*>(p) + base + (at(i) + c2)); };
+    const TIN* pk = static_cast<const TIN*>(a.k) + base;
+    const TIN* pg = static_cast<const TIN*>(a.g) + base;
+    const TIN* pq_ = static_cast<const TIN*>(a.q) + base;
+    const TIN* pv = static_cast<const TIN*>(a.v) + base;
+    const int c2 = 32 * wave + 2 * m16;  // this lane's two value channels
     const int parent_in = load_parent(a.parents + (size_t)b * N, N);
-    R2 rg[NP / 4], rk[MO][4], rq[MO][4], rv[MO][4];
+    typename R::R4 rk[KR], rg[KR], rq[WR][2];
+    typename R::R2 rv[MO][4];
 #pragma unroll
-    for (int s = 0; s < NP / 4; ++s) rg[s] = in2(a.g, 4 * s + q4);
+    for (int r = 0; r < KR; ++r) {
+        const uint32_t o = at((t >> 5) + 8 * r) + 4 * (t & 31);
+        rk[r] = *reinterpret_cast<const typename R::R4*>(pk + o);
+        rg[r] = *reinterpret_cast<const typename R::R4*>(pg + o);
+    }
+#pragma unroll
+    for (int r = 0; r < WR; ++r)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            rq[r][p] = *reinterpret_cast<const typename R::R4*>(pq_ + at(16 * r + 4 * wave + q4) + 64 * p + 4 * m16);
 #pragma unroll
     for (int m = 0; m < MO; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * m + 4 * q4 + e;
-            rk[m][e] = in2(a.k, i);
-            rq[m][e] = in2(a.q, i);
-            rv[m][e] = in2(a.v, i);
-        }
+        for (int e = 0; e < 4; ++e) rv[m][e] = *reinterpret_cast<const typename R::R2*>(pv + at(16 * m + 4 * q4 + e) + c2);
     const float beta = ld(static_cast<const TIN*>(a.beta) + ((size_t)b * N + min(t, N - 1)) * a.H + h);
     asm volatile("" ::: "memory");
     // element s of group g is row 16 g + 4 q4 + s, columns c2 and c2 + 1
@@ -350,81 +338,23 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
         for (int s = 0; s < 4; ++s) raw[g][s] = state2(S + 16 * g * D + (s_off + s * D));
     asm volatile("" ::: "memory");
 
-    uint64_t anc;
-    const int parent = tree_parent(parent_in, anc);
+    const int parent = tree_parent(parent_in);
     const uint64_t there = __ballot(parent != -2);  // lanes past N hold -2
     auto row_of = [&](int i) { return ((size_t)b * N + i) * a.H + h; };
-    // every wavefront writes the same tree and reads its own writes: no barrier
-    s_par[lane] = parent;
-    s_anc[lane] = anc;
+    if (wave == 0) s_par[lane] = parent;
+#pragma unroll
+    for (int r = 0; r < KR; ++r) {
+        const int i = (t >> 5) + 8 * r, c = 4 * (t & 31);
+        f32x4 g = R::f4(rg[r]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = __expf(fmaxf(g[e], a.lower_bound));
+        *reinterpret_cast<f32x4*>(&s_k[i][c]) = R::f4(rk[r]);
+        *reinterpret_cast<f32x4*>(&s_al[i][c]) = g;
+    }
     if (t < NP) s_beta[t] = beta;
+    for (int e = t; e < NP * LP; e += 256) (&s_pa[0][0])[e] = 0.0f;
+    lds_barrier();
 
-    // decay: G of the lane's nodes (16 m + 4 q4 + e) and channels. An absent
-    // node's g counts as 0 (it lies on no path, but 0 times NaN would not be).
-    f32x4 G[MO][2];
-#pragma unroll
-    for (int m = 0; m < MO; ++m) {
-        G[m][0] = G[m][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const uint64_t path = s_anc[16 * m + m16];
-#pragma unroll
-        for (int s = 0; s < min(4 * m + 4, NP / 4); ++s) {
-            const int j = 4 * s + q4;
-            const f32x2 g = R::f2(rg[s]);
-            const bool live = there >> j & 1;
-            const float on = path >> j & 1 ? 1.0f : 0.0f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                G[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(on, live ? fmaxf(g[c], a.lower_bound) : 0.0f, G[m][c], 0, 0, 0);
-        }
-    }
-    uint32_t top[2] = {0, 0};  // the largest |G| of a channel, as bits (NaN above all)
-    bool walk = false;
-#pragma unroll
-    for (int m = 0; m < MO; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * m + 4 * q4 + e;
-            const bool live = (NP >= 16 || q4 < 2) && (there >> i & 1);
-            const f32x2 k = R::f2(rk[m][e]), q = R::f2(rq[m][e]);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                top[c] = max(top[c], __float_as_uint(G[m][c][e]) & 0x7fffffffu);
-                walk |= G[m][c][e] > 0.0f;
-                const float big = fmaxf(fabsf(k[c]), fabsf(q[c]));
-                walk |= live && big > 1e4f && big < __builtin_inff();
-            }
-        }
-    float half_top[2];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], 16, 64));
-        top[c] = max(top[c], (uint32_t)__shfl_xor((int)top[c], 32, 64));
-        walk |= top[c] > __float_as_uint(150.0f);
-        half_top[c] = 0.5f * __uint_as_float(top[c]);
-    }
-    walk = __any(walk);
-    if (lane == 0) s_walk[wave] = walk;
-    if (q4 == 0) *reinterpret_cast<f32x2*>(&s_er[c2]) = f32x2{exp_full(-half_top[0]), exp_full(-half_top[1])};
-#pragma unroll
-    for (int m = 0; m < MO; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * m + 4 * q4 + e;
-            if (NP < 16 && q4 >= 2) break;
-            f32x2 k = R::f2(rk[m][e]), q = R::f2(rq[m][e]), down, up;
-            if (!(there >> i & 1)) k = q = f32x2{0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float x = G[m][c][e] + half_top[c];
-                down[c] = exp_full(x);
-                up[c] = exp_full(-x);
-            }
-            *reinterpret_cast<f32x2*>(&s_row[i][c2]) = k * down;
-            *reinterpret_cast<f32x2*>(&s_row[NP + i][c2]) = q * down;
-            *reinterpret_cast<f32x2*>(&s_kh[i][c2]) = k * up;
-            const float qk = sum16(q.x * k.x + q.y * k.y);
-            if (m16 == 0) s_diag[wave][i] = qk;
-        }
     // the products' accumulators: rows 4 q4 + e of a tile, columns c2 and c2 + 1.
     // The tiles of (D k) S0 start at -v, so that they end at minus the
     // substitution's right-hand side.
@@ -440,105 +370,83 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
                 acc[m][1][e] = -v.y;
             }
         }
-    lds_barrier();
 
-    if (!(s_walk[0] | s_walk[1] | s_walk[2] | s_walk[3])) {
-        // pairs: tiles of (k or q rows of node block m) x (node block n <= m), dealt to the wavefronts
-        constexpr int kTiles = MO * (MO + 1) / 2;
-        for (int tile = wave; tile < (NP >= 16 ? 2 * kTiles : 1); tile += 4) {
-            const int p = tile < kTiles ? tile : tile - kTiles;
-            int m = 0;
-            while ((m + 1) * (m + 2) / 2 <= p) ++m;
-            const int n = p - m * (m + 1) / 2, r0 = 16 * m + (tile < kTiles ? 0 : NP), j = 16 * n + m16;
-            f32x4 dot = {0.f, 0.f, 0.f, 0.f};
+    // walk: node i by 16 lanes, lane channels 4 m16 .. and 64 + 4 m16 ..
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(&s_row[r0 + m16][16 * g + 4 * q4]);
-                const f32x4 y = *reinterpret_cast<const f32x4*>(&s_kh[j & (NP - 1)][16 * g + 4 * q4]);
+    for (int n = 0; n < WR; ++n) {
+        const int i = 16 * n + 4 * wave + q4;
+        if (i >= NP) break;
+        int j = there >> i & 1 ? i : -1;
+        f32x4 q[2], k[2], decay[2];
 #pragma unroll
-                for (int s = 0; s < 4; ++s) dot = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s], y[s], dot, 0, 0, 0);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 4 * q4 + e, i = NP >= 16 ? 16 * m + row : row & 7;
-                const bool is_q = NP >= 16 ? tile >= kTiles : row >= 8;
-                if (j >= NP || j > i) continue;
-                const float v = s_anc[i] >> j & 1 ? dot[e] : 0.0f;
-                if (!is_q) {
-                    if (j < i) s_pa[j][i] = v;
-                } else {
-                    s_pa[i][j] = j < i ? v : s_diag[0][i] + s_diag[1][i] + s_diag[2][i] + s_diag[3][i];
-                }
+        for (int p = 0; p < 2; ++p) {
+            q[p] = k[p] = f32x4{0.f, 0.f, 0.f, 0.f};
+            decay[p] = f32x4{1.f, 1.f, 1.f, 1.f};
+            if (j >= 0) {
+                q[p] = R::f4(rq[n][p]);
+                k[p] = *reinterpret_cast<const f32x4*>(&s_k[i][64 * p + 4 * m16]);
             }
         }
-    } else {
-        // alpha in the rows of D k, k in s_kh; the decayed rows wait in registers
-        // until everyone has walked
+        // kAhead: k and alpha of the next node up are read while this one's products run
+        f32x4 kj[2] = {k[0], k[1]}, al[2];
+        auto read_al = [&](int n) {
 #pragma unroll
-        for (int s = 0; s < NP / 4; ++s) {
-            f32x2 g = R::f2(rg[s]);
+            for (int p = 0; p < 2; ++p) al[p] = *reinterpret_cast<const f32x4*>(&s_al[n][64 * p + 4 * m16]);
+        };
+        auto read_k = [&](int n, f32x4* to) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) g[c] = __expf(fmaxf(g[c], a.lower_bound));
-            *reinterpret_cast<f32x2*>(&s_row[4 * s + q4][c2]) = g;
+            for (int p = 0; p < 2; ++p) to[p] = *reinterpret_cast<const f32x4*>(&s_k[n][64 * p + 4 * m16]);
+        };
+        int up = j;
+        if (j >= 0) {
+            up = s_par[j];
+            if constexpr (kAhead) read_al(j);
         }
+        while (j >= 0) {
+            const int next = max(up, 0), up2 = s_par[next];
+            f32x4 kn[2], an[2];
+            if constexpr (kAhead) {
+                read_k(next, kn);
 #pragma unroll
-        for (int m = 0; m < MO; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (NP >= 16 || q4 < 2) *reinterpret_cast<f32x2*>(&s_kh[16 * m + 4 * q4 + e][c2]) = R::f2(rk[m][e]);
-        if (t < D) s_er[t] = 1.0f;
-        for (int e = t; e < NP * LP; e += 256) (&s_pa[0][0])[e] = 0.0f;
-        lds_barrier();
-        constexpr int WR = (NP + 15) / 16;  // nodes a 16-lane group walks; lane channels 4 m16 .. and 64 + 4 m16 ..
-        f32x4 kd[WR][2], qd[WR][2];
-#pragma unroll
-        for (int n = 0; n < WR; ++n) {
-            const int i = 16 * n + 4 * wave + q4;
-            int j = i < NP && (there >> i & 1) ? i : -1;
+                for (int p = 0; p < 2; ++p) an[p] = *reinterpret_cast<const f32x4*>(&s_al[next][64 * p + 4 * m16]);
+            } else {
+                read_k(j, kj);
+                read_al(j);
+            }
+            float pq = 0.0f, pk = 0.0f;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                kd[n][p] = qd[n][p] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if (j >= 0) {
-                    qd[n][p] = ld4(static_cast<const TIN*>(a.q) + base + (at(i) + 64 * p + 4 * m16));
-                    kd[n][p] = *reinterpret_cast<const f32x4*>(&s_kh[i][64 * p + 4 * m16]);
+                kj[p] *= decay[p];
+                decay[p] *= al[p];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    pq += q[p][e] * kj[p][e];
+                    pk += k[p][e] * kj[p][e];
                 }
             }
-            while (j >= 0) {
-                float pq = 0.0f, pk = 0.0f;
+            pq = sum16(pq);
+            pk = sum16(pk);
+            if (m16 == 0) {
+                s_pa[i][j] = pq;
+                if (j != i) s_pa[j][i] = pk;
+            }
+            j = up;
+            up = up2;
+            if constexpr (kAhead) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const f32x4 kj = *reinterpret_cast<const f32x4*>(&s_kh[j][64 * p + 4 * m16]);
-                    const f32x4 al = *reinterpret_cast<const f32x4*>(&s_row[j][64 * p + 4 * m16]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pq += qd[n][p][e] * kj[e];
-                        pk += kd[n][p][e] * kj[e];
-                    }
-                    qd[n][p] *= al;
-                    kd[n][p] *= al;
+                    kj[p] = kn[p];
+                    al[p] = an[p];
                 }
-                pq = sum16(pq);
-                pk = sum16(pk);
-                if (m16 == 0) {
-                    s_pa[i][j] = pq;
-                    if (j != i) s_pa[j][i] = pk;
-                }
-                j = s_par[j];
             }
         }
-        lds_barrier();
 #pragma unroll
-        for (int n = 0; n < WR; ++n) {
-            const int i = 16 * n + 4 * wave + q4;
-            if (i >= NP) break;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                *reinterpret_cast<f32x4*>(&s_row[i][64 * p + 4 * m16]) = kd[n][p];
-                *reinterpret_cast<f32x4*>(&s_row[NP + i][64 * p + 4 * m16]) = qd[n][p];
-            }
+        for (int p = 0; p < 2; ++p) {
+            *reinterpret_cast<f32x4*>(&s_row[i][64 * p + 4 * m16]) = k[p] * decay[p];
+            *reinterpret_cast<f32x4*>(&s_row[NP + i][64 * p + 4 * m16]) = q[p] * decay[p];
         }
-        lds_barrier();
     }
+    lds_barrier();
 
     // read: lane (m16, q4) gives row m16 of a tile, K element 16 g + 4 q4 + s in
     // step (g, s), and takes rows 4 q4 + e of column tile c (columns 2 m16 + c)
@@ -546,9 +454,7 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     for (int g = 0; g < 8; ++g) {
         f32x4 row[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            row[m] = *reinterpret_cast<const f32x4*>(&s_row[16 * m + m16][16 * g + 4 * q4]) *
-                     *reinterpret_cast<const f32x4*>(&s_er[16 * g + 4 * q4]);
+        for (int m = 0; m < MT; ++m) row[m] = *reinterpret_cast<const f32x4*>(&s_row[16 * m + m16][16 * g + 4 * q4]);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const f32x2 st = unpack2(raw[g][s]);
