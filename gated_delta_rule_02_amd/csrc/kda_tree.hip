@@ -210,29 +210,34 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 }
 
 // ------------------------------------------------------------ verification
-// One workgroup of four wavefronts per (sequence, head); wavefront w takes value
-// channels 32 w .. 32 w + 31. Four phases:
-//   load   the wavefront's 128 x 32 part of S0 into registers (64 for a float32
-//          state), used last but issued first: the rest of the workgroup's work
-//          up to the products runs while it arrives;
+// One workgroup per (sequence, head), of NW wavefronts that take 128 / NW value
+// channels each. Four phases:
+//   load   the nodes' inputs, then the wavefront's columns of S0 into registers:
+//          used last, so that the work up to the products runs while they arrive;
 //   walk   16 lanes per node walk up its path with the running decay, forming
 //          the node's products with every node above it (P with q_i, A with k_i)
 //          and, at the end, the decayed rows D(i) k_i and D(i) q_i. Only pairs on
 //          a path are formed;
 //   read   [D k; D q] S0 on the float32 matrix instruction (float32 products
-//          and sums: the results are held to float32 accuracy), two 16-column tiles
-//          per wavefront, rows from LDS, S0 from the registers;
+//          and sums: the results are held to float32 accuracy), rows from LDS, S0
+//          from the registers;
 //   solve  u by forward substitution in blocks of 16 nodes: the blocks before
 //          by the matrix instruction on the accumulators that hold (D k) S0 - v,
 //          then within the block each lane a value channel, the block's
 //          remainders in registers (after u_j every r_i takes - A_ij u_j,
 //          independent operations); then o += P u by the matrix instruction on
 //          the accumulators that hold (D q) S0.
+// What bounds it (float32 states, 64 heads): up to 16 nodes HBM, 128 trees of 16
+// nodes 158 us = 5.1 TB/s (a copy reaches 5.1), 64 of 8 nodes 55 us = 6.1 TB/s; above,
+// the walk (of 64 trees of 32 nodes it took 73 of 188 us, skipped for the measurement) and the
+// products (54 us).
 // NP: N rounded up to 8, 16, 32 or 64.
-#ifndef TREE_W
-#define TREE_W 4
-#endif
-template <int NP> constexpr int kTreeWaves = NP <= 16 ? TREE_W : (NP == 32 ? 2 : 1);  // wavefronts per SIMD (LDS, registers)
+// NW wavefronts: 4, and 8 for NP = 64, where LDS leaves room for one workgroup a
+// compute unit and 4 wavefronts left a SIMD with one to cover every latency of
+// the walk and the substitution (32 trees of 64 nodes, 64 heads: 320 | 275 us with 4 | 8;
+// 64 of 32 nodes 178 | 189, so 4 there).
+template <int NP> constexpr int kTreeWaves = NP == 64 ? 8 : 4;
+template <int NP> constexpr int kTreePerSimd = NP <= 16 ? 4 : 2;  // wavefronts per SIMD (by LDS and registers)
 
 // f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
 // constants from the start (a loop unrolled late left the remainders of the
@@ -248,38 +253,38 @@ __device__ __forceinline__ void static_for(F&& f)
     static_for(f, std::make_integer_sequence<int, N>{});
 }
 
-// Four or two consecutive inputs as they are stored.
-template <typename T> struct Raw;
-template <> struct Raw<float> {
+// Four, or CT (1 or 2), consecutive values as they are stored, and as floats.
+template <int CT> using cols_t = float __attribute__((ext_vector_type(CT)));
+template <typename T, int CT> struct Raw;
+template <int CT> struct Raw<float, CT> {
     typedef f32x4 R4;
-    typedef f32x2 R2;
+    typedef cols_t<CT> RC;
     __device__ static f32x4 f4(const R4& v) { return v; }
-    __device__ static f32x2 f2(const R2& v) { return v; }
+    __device__ static cols_t<CT> fc(const RC& v) { return v; }
 };
-template <> struct Raw<bf16_t> {
+template <int CT> struct Raw<bf16_t, CT> {
     typedef uint2 R4;
-    typedef uint32_t R2;
-    __device__ static f32x2 f2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
+    typedef uint16_t RC __attribute__((ext_vector_type(CT)));
     __device__ static f32x4 f4(const uint2& u)
     {
-        const f32x2 a = f2(u.x), b = f2(u.y);
-        return f32x4{a.x, a.y, b.x, b.y};
+        return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                     __uint_as_float(u.y & 0xffff0000u)};
+    }
+    __device__ static cols_t<CT> fc(const RC& u)
+    {
+        cols_t<CT> f;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) f[c] = bf16_to_f32(u[c]);
+        return f;
     }
 };
 
-// Two consecutive state elements, streamed once.
-__device__ __forceinline__ f32x2 state2(const float* p) { return __builtin_nontemporal_load(reinterpret_cast<const f32x2*>(p)); }
-__device__ __forceinline__ f32x2 unpack2(f32x2 v) { return v; }
-__device__ __forceinline__ uint32_t state2(const bf16_t* p) { return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p)); }
-__device__ __forceinline__ f32x2 unpack2(uint32_t u) { return f32x2{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}; }
-
-#ifndef TREE_AHEAD
-#define TREE_AHEAD (NP > 16 || sizeof(TS) == 2)
-#endif
 template <typename TIN, typename TOUT, typename TS, int NP>
-__global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeArgs a)
+__global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_tree_kernel(TreeArgs a)
 {
-    constexpr bool kAhead = TREE_AHEAD;
+    constexpr int NW = kTreeWaves<NP>, CT = 8 / NW, CW = 16 * CT;  // value channels: CT column tiles a wavefront
+    constexpr bool kAhead = NP > 16 || sizeof(TS) == 2;            // (with a float32 state the registers do not suffice)
+    typedef cols_t<CT> cols;
     constexpr int LD = D + 4;                  // row of the decayed rows: 16 rows at one column meet distinct banks
     constexpr int LP = NP + 4;
     constexpr int MT = 2 * NP / 16;            // row tiles: D k, then D q (NP = 8: one tile holds both)
@@ -298,21 +303,22 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     // load. First what the walk needs, then the state: loads return in order, so
     // the walk waits for the small ones alone and runs while the state arrives.
     // (Places past the end read the last node's rows; unused.)
-    typedef Raw<TIN> R;
-    constexpr int KR = NP / 8, WR = (NP + 15) / 16;  // rows of k and g a thread, nodes a 16-lane group walks
+    typedef Raw<TIN, CT> R;
+    typedef Raw<TS, CT> RS;
+    constexpr int KR = NP / (2 * NW), WR = (NP + 4 * NW - 1) / (4 * NW);  // rows of k and g a thread, nodes a 16-lane group walks
     const size_t base = ((size_t)b * N * a.H + h) * D;
     auto at = [&](int i) { return (uint32_t)min(i, N - 1) * (uint32_t)(a.H * D); };  // row of node i from `base`
     const TIN* pk = static_cast<const TIN*>(a.k) + base;
     const TIN* pg = static_cast<const TIN*>(a.g) + base;
     const TIN* pq_ = static_cast<const TIN*>(a.q) + base;
     const TIN* pv = static_cast<const TIN*>(a.v) + base;
-    const int c2 = 32 * wave + 2 * m16;  // this lane's two value channels
+    const int c2 = CW * wave + CT * m16;  // this lane's CT value channels
     const int parent_in = load_parent(a.parents + (size_t)b * N, N);
     typename R::R4 rk[KR], rg[KR], rq[WR][2];
-    typename R::R2 rv[MO][4];
+    typename R::RC rv[MO][4];
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
-        const uint32_t o = at((t >> 5) + 8 * r) + 4 * (t & 31);
+        const uint32_t o = at((t >> 5) + 2 * NW * r) + 4 * (t & 31);
         rk[r] = *reinterpret_cast<const typename R::R4*>(pk + o);
         rg[r] = *reinterpret_cast<const typename R::R4*>(pg + o);
     }
@@ -320,22 +326,23 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     for (int r = 0; r < WR; ++r)
 #pragma unroll
         for (int p = 0; p < 2; ++p)
-            rq[r][p] = *reinterpret_cast<const typename R::R4*>(pq_ + at(16 * r + 4 * wave + q4) + 64 * p + 4 * m16);
+            rq[r][p] = *reinterpret_cast<const typename R::R4*>(pq_ + at(4 * NW * r + 4 * wave + q4) + 64 * p + 4 * m16);
 #pragma unroll
     for (int m = 0; m < MO; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) rv[m][e] = *reinterpret_cast<const typename R::R2*>(pv + at(16 * m + 4 * q4 + e) + c2);
+        for (int e = 0; e < 4; ++e) rv[m][e] = *reinterpret_cast<const typename R::RC*>(pv + at(16 * m + 4 * q4 + e) + c2);
     const float beta = ld(static_cast<const TIN*>(a.beta) + ((size_t)b * N + min(t, N - 1)) * a.H + h);
     asm volatile("" ::: "memory");
-    // element s of group g is row 16 g + 4 q4 + s, columns c2 and c2 + 1
-    // (a uniform base, a 32-bit lane offset and constants: one address register)
-    const TS* S = static_cast<const TS*>(a.state) + (size_t)bh * D * D + 32 * wave;
-    const uint32_t s_off = 4 * q4 * D + 2 * m16;
-    decltype(state2(S)) raw[8][4];
+    // element s of group g is row 16 g + 4 q4 + s, columns c2 .. (streamed once; a
+    // uniform base, a 32-bit lane offset and constants: one address register)
+    const TS* S = static_cast<const TS*>(a.state) + (size_t)bh * D * D + CW * wave;
+    const uint32_t s_off = 4 * q4 * D + CT * m16;
+    typename RS::RC raw[8][4];
 #pragma unroll
     for (int g = 0; g < 8; ++g)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) raw[g][s] = state2(S + 16 * g * D + (s_off + s * D));
+        for (int s = 0; s < 4; ++s) 
+            raw[g][s] = __builtin_nontemporal_load(reinterpret_cast<const typename RS::RC*>(S + 16 * g * D + (s_off + s * D)));
     asm volatile("" ::: "memory");
 
     const int parent = tree_parent(parent_in);
@@ -344,7 +351,7 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     if (wave == 0) s_par[lane] = parent;
 #pragma unroll
     for (int r = 0; r < KR; ++r) {
-        const int i = (t >> 5) + 8 * r, c = 4 * (t & 31);
+        const int i = (t >> 5) + 2 * NW * r, c = 4 * (t & 31);
         f32x4 g = R::f4(rg[r]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[e] = __expf(fmaxf(g[e], a.lower_bound));
@@ -352,29 +359,27 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
         *reinterpret_cast<f32x4*>(&s_al[i][c]) = g;
     }
     if (t < NP) s_beta[t] = beta;
-    for (int e = t; e < NP * LP; e += 256) (&s_pa[0][0])[e] = 0.0f;
+    for (int e = t; e < NP * LP; e += 64 * NW) (&s_pa[0][0])[e] = 0.0f;
     lds_barrier();
 
-    // the products' accumulators: rows 4 q4 + e of a tile, columns c2 and c2 + 1.
+    // the products' accumulators: rows 4 q4 + e of a tile, columns c2 ...
     // The tiles of (D k) S0 start at -v, so that they end at minus the
     // substitution's right-hand side.
-    f32x4 acc[MT][2];
+    f32x4 acc[MT][CT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            acc[m][0][e] = acc[m][1][e] = 0.0f;
-            if (m < MO && (NP >= 16 || q4 < 2)) {
-                const f32x2 v = R::f2(rv[m][e]);
-                acc[m][0][e] = -v.x;
-                acc[m][1][e] = -v.y;
-            }
+            cols v = 0.0f;
+            if (m < MO && (NP >= 16 || q4 < 2)) v = R::fc(rv[m][e]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[m][c][e] = -v[c];
         }
 
     // walk: node i by 16 lanes, lane channels 4 m16 .. and 64 + 4 m16 ..
 #pragma unroll
     for (int n = 0; n < WR; ++n) {
-        const int i = 16 * n + 4 * wave + q4;
+        const int i = 4 * NW * n + 4 * wave + q4;
         if (i >= NP) break;
         int j = there >> i & 1 ? i : -1;
         f32x4 q[2], k[2], decay[2];
@@ -449,7 +454,7 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     lds_barrier();
 
     // read: lane (m16, q4) gives row m16 of a tile, K element 16 g + 4 q4 + s in
-    // step (g, s), and takes rows 4 q4 + e of column tile c (columns 2 m16 + c)
+    // step (g, s), and takes rows 4 q4 + e of column tile c (columns CT m16 + c)
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
         f32x4 row[MT];
@@ -457,18 +462,18 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
         for (int m = 0; m < MT; ++m) row[m] = *reinterpret_cast<const f32x4*>(&s_row[16 * m + m16][16 * g + 4 * q4]);
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
-            const f32x2 st = unpack2(raw[g][s]);
+            const cols st = RS::fc(raw[g][s]);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[m][s], st[c], acc[m][c], 0, 0, 0);
+                for (int c = 0; c < CT; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[m][s], st[c], acc[m][c], 0, 0, 0);
         }
     }
     lds_barrier();  // s_row is read: its halves now hold (D k) S0 and u, each wavefront its own columns
     __builtin_amdgcn_sched_barrier(0);
 
-    // solve: both halves of the wavefront hold the same channel and the same values
-    const int col = 32 * wave + (lane & 31), half = lane >> 5;
+    // solve: the 64 / CW lanes of a channel hold the same values
+    const int col = CW * wave + (lane & (CW - 1));
     // An infinite or NaN write must reach the nodes below it and no others, but
     // the sums below run over all nodes with coefficients 0 where there is no
     // path. So such a write enters the sums as 0, and is noted: it and what lies
@@ -482,43 +487,56 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
             for (int s = 0; s < 4; ++s) {
                 const int k = 16 * J + 4 * q4 + s;
                 const float A = s_pa[k][16 * I + m16];
-                const f32x2 u = *reinterpret_cast<const f32x2*>(&s_row[NP + k][c2]);
+                const cols u = *reinterpret_cast<const cols*>(&s_row[NP + k][c2]);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) acc[I][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(A, u[c], acc[I][c], 0, 0, 0);
+                for (int c = 0; c < CT; ++c) acc[I][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(A, u[c], acc[I][c], 0, 0, 0);
             }
         });
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (NP >= 16 || q4 < 2)
-                *reinterpret_cast<f32x2*>(&s_row[16 * I + 4 * q4 + e][c2]) = f32x2{acc[I][0][e], acc[I][1][e]};
+            if (NP >= 16 || q4 < 2) {
+                cols v;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) v[c] = acc[I][c][e];
+                *reinterpret_cast<cols*>(&s_row[16 * I + 4 * q4 + e][c2]) = v;
+            }
         // within the block
         constexpr int BN_ = NP < 16 ? NP : 16, i0 = 16 * I;
-        float r[BN_];
-        static_for<BN_>([&](auto n) { r[n] = -s_row[i0 + n][col]; });
+        float r[BN_], beta_[BN_];
+        static_for<BN_>([&](auto n) {
+            r[n] = -s_row[i0 + n][col];
+            beta_[n] = s_beta[i0 + n];
+        });
+        // row j of A is read while row j - 1 is used
+        f32x4 A[2][BN_ / 4];
+        auto read_A = [&](auto J) {
+            static_for<BN_ / 4>([&](auto n) {
+                if constexpr (4 * n + 3 > J) A[J % 2][n] = *reinterpret_cast<const f32x4*>(&s_pa[i0 + J][i0 + 4 * n]);
+            });
+        };
+        read_A(std::integral_constant<int, 0>{});
         static_for<BN_>([&](auto J) {
             constexpr int j = J;
-            const float u = there >> (i0 + j) & 1 ? s_beta[i0 + j] * r[j] : 0.0f;
+            if constexpr (j + 1 < BN_) read_A(std::integral_constant<int, j + 1>{});
+            const float u = there >> (i0 + j) & 1 ? beta_[j] * r[j] : 0.0f;
             const bool fine = fabsf(u) < __builtin_inff();
             const float w = fine ? u : 0.0f;
             if (!fine) bad |= (uint64_t)1 << (i0 + j);
             s_row[NP + i0 + j][col] = w;
-            static_for<BN_ / 4>([&](auto n) {
-                if constexpr (4 * n + 3 > j) {
-                    const f32x4 A = *reinterpret_cast<const f32x4*>(&s_pa[i0 + j][i0 + 4 * n]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * n + e > j) r[4 * n + e] -= A[e] * w;
-                }
+            static_for<BN_>([&](auto n) {
+                if constexpr (n > j) r[n] -= A[j % 2][n / 4][n % 4] * w;
             });
+            __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead, and no further
         });
         __builtin_amdgcn_sched_barrier(0);
     });
     const bool any_bad = __any(bad != 0);
     if (a.writes) {
-        const int cw = 32 * wave + 4 * (lane & 7);
+        constexpr int kLanes = CW / 4;  // of a row
+        const int cw = CW * wave + 4 * (lane % kLanes);
 #pragma unroll
-        for (int i0 = 0; i0 < NP; i0 += 8) {
-            const int i = i0 + (lane >> 3);
+        for (int i0 = 0; i0 < NP; i0 += 64 / kLanes) {
+            const int i = i0 + lane / kLanes;
             if (i < N)
                 __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(&s_row[NP + i][cw]),
                                             reinterpret_cast<f32x4*>(a.writes + row_of(i) * D + cw));
@@ -527,12 +545,12 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
     // o: the last MO row tiles hold (D q) S0; add P u
 #pragma unroll
     for (int g = 0; g < (NP + 15) / 16; ++g) {
-        f32x2 u[4];
+        cols u[4];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int k = 16 * g + 4 * q4 + s;
-            u[s] = f32x2{0.f, 0.f};
-            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const f32x2*>(&s_row[NP + (k & (NP - 1))][c2]);
+            u[s] = 0.0f;
+            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const cols*>(&s_row[NP + (k & (NP - 1))][c2]);
         }
 #pragma unroll
         for (int m = g; m < MO; ++m) {
@@ -542,7 +560,7 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
                 const int k = 16 * g + 4 * q4 + s;
                 const float p = k <= i ? s_pa[i & (NP - 1)][k & (NP - 1)] : 0.0f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < CT; ++c)
                     acc[MT - MO + m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, u[s][c], acc[MT - MO + m][c], 0, 0, 0);
             }
         }
@@ -554,11 +572,13 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
         for (int e = 0; e < 4; ++e) {
             const int i = (NP >= 16 ? 16 * m : -8) + 4 * q4 + e;
             if (i < 0 || i >= N) continue;
-            f32x2 v = {a.scale * acc[MT - MO + m][0][e], a.scale * acc[MT - MO + m][1][e]};
-            if (!(there >> i & 1)) v = f32x2{0.f, 0.f};
+            cols v;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) v[c] = there >> i & 1 ? a.scale * acc[MT - MO + m][c][e] : 0.0f;
             TOUT* p = o + row_of(i) * D + c2;
-            if constexpr (sizeof(TOUT) == 4) *reinterpret_cast<f32x2*>(p) = v;
-            else *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
+            if constexpr (sizeof(TOUT) == 4) *reinterpret_cast<cols*>(p) = v;
+            else if constexpr (CT == 2) *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v[0], v[1]);
+            else st(p, v[0]);
         }
     if (any_bad) {
         // rare: NaN for every write that is not finite and for what lies below it
@@ -567,7 +587,7 @@ __global__ __launch_bounds__(256, kTreeWaves<NP>) void decode_tree_kernel(TreeAr
             uint64_t above = 0;
             for (int j = __builtin_amdgcn_readlane(parent, i); j >= 0; j = __builtin_amdgcn_readlane(parent, j))
                 above |= (uint64_t)1 << j;
-            if (!(there >> i & 1) || half) continue;
+            if (!(there >> i & 1) || lane >= CW) continue;
             if (!(bad & (above | (uint64_t)1 << i))) continue;
             if (a.writes) a.writes[row_of(i) * D + col] = __builtin_nanf("");
             st(o + row_of(i) * D + col, __builtin_nanf(""));
@@ -653,11 +673,11 @@ __global__ __launch_bounds__(CommitMap<TS>::kThreads) void tree_commit_kernel(Tr
 template <typename TIN, typename TOUT, typename TS>
 hipError_t launch_tree_t(const TreeArgs& a, hipStream_t s)
 {
-    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
+    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256), wide(512);
     if (a.N <= 8) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 8>), grid, block, 0, s, a);
     else if (a.N <= 16) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 16>), grid, block, 0, s, a);
     else if (a.N <= 32) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 32>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 64>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 64>), grid, wide, 0, s, a);
     return hipGetLastError();
 }
 template <typename TIN>
