@@ -83,6 +83,10 @@ int check_lower_bound(const char* fn, float lb, bool chunked)
     return KDA_OK;
 }
 
+// A launch holds less than 2^32 threads; the kernels that give a workgroup (of at
+// most 256) to a row, or a few to a tile of rows, take this many.
+constexpr int64_t kMaxRows = (int64_t)1 << 24;
+
 // cu_seqlens on the host: cu[0] = 0, non-decreasing, cu[N] = T.
 int check_cu(const int32_t* cu_dev, const int32_t* cu_host, int num_seqs, int64_t T, int64_t* seq_len)
 {
@@ -509,6 +513,7 @@ static int check_conv_tree(const char* fn, const void* x, int64_t x_ld, const vo
     REQUIRE(x && conv_state, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
     REQUIRE(valid_dtype(dtype), KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
     if (int rc = check_tree(fn, parents, B, num_nodes, 1); rc != KDA_OK) return rc;
+    REQUIRE(B < kMaxRows, KDA_ERR_UNSUPPORTED, "%s: at most 2^24 - 1 sequences (got %d)", fn, B);
     REQUIRE(C >= 128 && C % 128 == 0, KDA_ERR_UNSUPPORTED, "%s: C must be a positive multiple of 128 (got %d)", fn, C);
     REQUIRE(W >= 2 && W <= 8, KDA_ERR_UNSUPPORTED, "%s: W must be in [2, 8] (got %d)", fn, W);
     REQUIRE(x_ld >= C && x_ld % 8 == 0, KDA_ERR_INVALID_ARG, "%s: x_ld must be >= C and a multiple of 8", fn);
@@ -564,6 +569,7 @@ static int add_rmsnorm_impl(const char* fn, const void* x, int64_t x_ld, kda_dty
             KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
     REQUIRE(K % (fp8 ? 128 : 8) == 0, KDA_ERR_UNSUPPORTED, "%s: K must be a multiple of %d (got %lld)", fn,
             fp8 ? 128 : 8, (long long)K);
+    REQUIRE(M < kMaxRows, KDA_ERR_UNSUPPORTED, "%s: at most 2^24 - 1 rows (got %lld)", fn, (long long)M);
     REQUIRE(eps >= 0.0f, KDA_ERR_INVALID_ARG, "%s: eps must be >= 0 (got %g)", fn, (double)eps);
     REQUIRE(residual || !residual_out, KDA_ERR_INVALID_ARG, "%s: residual_out needs a residual", fn);
     if (M == 0) return ok();
@@ -925,6 +931,7 @@ int kda_gemm_epilogue(const void* A, int64_t lda, const void* B, int64_t ldb, co
     REQUIRE(M >= 0 && N >= 1 && K >= 8 && M <= 0x7fffffff && N <= 0x7fffffff && K <= 0x7fffffff, KDA_ERR_INVALID_ARG,
             "%s: bad sizes", fn);
     REQUIRE(K % 8 == 0, KDA_ERR_UNSUPPORTED, "%s: K must be a multiple of 8", fn);
+    REQUIRE(M < kMaxRows && N < kMaxRows, KDA_ERR_UNSUPPORTED, "%s: at most 2^24 - 1 rows and columns", fn);
     if (M == 0) return ok();
     REQUIRE(A && B && C, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
     REQUIRE(lda >= K && ldb >= K && ldc >= N && lda % 8 == 0 && ldb % 8 == 0 && ldc % 4 == 0, KDA_ERR_INVALID_ARG,

@@ -65,10 +65,10 @@ class KDAMixer:
             self._bufs[name] = b
         return b
 
-    def projections(self, x):
+    def projections(self, x, tag=""):
         """P = x W_in^T (bf16): columns q | k | v | f | gate | b."""
         T = x.shape[0]
-        P = self._buf("P", (T, self.W_in.shape[0]), torch.bfloat16)
+        P = self._buf(tag + "P", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm(x, self.W_in, P)
         return P, self._columns(P)
 
@@ -76,13 +76,13 @@ class KDAMixer:
         W = self.W
         return [P[:, i * W:(i + 1) * W] for i in range(5)] + [P[:, 5 * W:5 * W + self.H]]
 
-    def projections_of_norm(self, x, residual, norm_weight, eps):
+    def projections_of_norm(self, x, residual, norm_weight, eps, tag):
         """The columns of RMSNorm(x + residual) norm_weight W_in^T (bf16); the
         residual (or None) is updated in place."""
         T, hidden = x.shape
         y = self._buf("ny", (T, hidden), torch.bfloat16)
         K.kda_add_rmsnorm(x, norm_weight, y, residual=residual, residual_out=residual, eps=eps)
-        P = self._buf("nP", (T, self.W_in.shape[0]), torch.bfloat16)
+        P = self._buf(tag + "nP", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm_epilogue(y, self.W_in, P)
         return self._columns(P)
 
@@ -166,7 +166,7 @@ class KDAMixer:
         Returns out [B, N, hidden] float32 and the DraftTree that commits an
         accepted path (both valid until the next call)."""
         B, N, hidden = x.shape
-        _, cols = self.projections(x.reshape(B * N, hidden))
+        _, cols = self.projections(x.reshape(B * N, hidden), tag="t")  # the commit reads them: not decode's buffer
         o, tree = self._core_tree(cols, parents, state, conv_states)
         out, _ = self.output(o.view(B * N, self.H, D), cols[4], tag="t")
         return out.view(B, N, hidden), tree
@@ -217,16 +217,17 @@ class KDABlock:
     and the next block adds it while it normalises: one pass then updates the
     stream, norms it and quantizes the projections' input. So every method takes
     the delta still to be added (None: nothing) and returns the one it leaves
-    (None: added); `finish` adds a last one."""
+    (None: added; else a buffer of the mixer, valid until that method's next call);
+    `finish` adds a last one."""
 
     def __init__(self, mixer, norm_weight, eps=1e-6):
         self.mixer, self.norm_weight, self.eps = mixer, norm_weight, eps
 
-    def _enter(self, hidden, delta):
+    def _enter(self, hidden, delta, tag=""):
         """hidden += delta in place; the projections of its norm -> their columns."""
         m = self.mixer
         x, residual = (hidden, None) if delta is None else (delta, hidden)
-        return m.projections_of_norm(x, residual, self.norm_weight, self.eps)
+        return m.projections_of_norm(x, residual, self.norm_weight, self.eps, tag)
 
     def forward(self, hidden, delta=None, **states):
         """Prefill: hidden [T, width] rows, states as KDAMixer.forward's arguments."""
@@ -242,7 +243,7 @@ class KDABlock:
 
     def decode_tree(self, hidden, parents, state, conv_states, delta=None):
         """A tree of drafts per sequence: hidden [B * N, width]. Returns (delta, DraftTree)."""
-        cols = self._enter(hidden, delta)
+        cols = self._enter(hidden, delta, tag="t")  # the commit reads them: not decode's buffer
         o, tree = self.mixer._core_tree(cols, parents, state, conv_states)
         return self.mixer.output_into(o.view(hidden.shape[0], self.mixer.H, D), cols[4], hidden, tag="bt"), tree
 
@@ -317,23 +318,23 @@ class KDAMixerFP8(KDAMixer):
                    _dev_bf16(d["conv_q"]), _dev_bf16(d["conv_k"]), _dev_bf16(d["conv_v"]),
                    torch.from_numpy(d["A_log"]).cuda(), torch.from_numpy(d["norm_w"]).cuda(), d["H"])
 
-    def projections(self, x):
+    def projections(self, x, tag=""):
         """x quantized per (token, 128 channels), then P = X W_in^T (bf16)."""
         T, hidden = x.shape
         xq = self._buf("xq", (T, hidden), torch.uint8)
         xs = self._buf("xs", (T, hidden // 128), torch.float32)
         K.kda_quantize_fp8(x, xq, xs)
-        P = self._buf("P", (T, self.W_in.shape[0]), torch.bfloat16)
+        P = self._buf(tag + "P", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm_fp8(xq, xs, self.W_in, self.W_in_s, P)
         return P, self._columns(P)
 
-    def projections_of_norm(self, x, residual, norm_weight, eps):
+    def projections_of_norm(self, x, residual, norm_weight, eps, tag):
         """As KDAMixer's, the norm quantized in the same pass."""
         T, hidden = x.shape
         xq = self._buf("nq", (T, hidden), torch.uint8)
         xs = self._buf("ns", (T, hidden // 128), torch.float32)
         K.kda_add_rmsnorm_fp8(x, norm_weight, xq, xs, residual=residual, residual_out=residual, eps=eps)
-        P = self._buf("nP", (T, self.W_in.shape[0]), torch.bfloat16)
+        P = self._buf(tag + "nP", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm_fp8(xq, xs, self.W_in, self.W_in_s, P)
         return self._columns(P)
 

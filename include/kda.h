@@ -541,7 +541,7 @@ int kda_conv_prefill(const void* x, int64_t x_ld, int64_t num_tokens, int C, int
  *             at x + row * x_ld)
  * conv_state  [B, W-1, C], oldest first, read only
  * y           [B * num_nodes, C], must not overlap another tensor
- * The rest as kda_conv_state_update; 1 <= num_nodes <= 64.
+ * The rest as kda_conv_state_update; 1 <= num_nodes <= 64, B < 2^24.
  * ---------------------------------------------------------------------- */
 int kda_conv_tree(const void* x, int64_t x_ld, const void* conv_state, const int32_t* parents, const void* weight,
                   const void* bias, kda_dtype dtype, int B, int num_nodes, int C, int W, int apply_silu,
@@ -620,8 +620,8 @@ int kda_gemm(const void* A, int64_t lda, const void* B, int64_t ldb, void* C, in
  *               pointer and stride: updated in place).
  * norm_weight   float32 [K].
  * y             [M, K] y_dtype, row stride y_ld.
- * K and the row strides are multiples of 8; M = 0 does nothing; eps >= 0. No
- * output may overlap another tensor, but for the in-place residual.
+ * K and the row strides are multiples of 8; M < 2^24, M = 0 does nothing;
+ * eps >= 0. No output may overlap another tensor, but for the in-place residual.
  * ---------------------------------------------------------------------- */
 int kda_add_rmsnorm(const void* x, int64_t x_ld, kda_dtype x_dtype, const void* residual, int64_t residual_ld,
                     void* residual_out, int64_t residual_out_ld, kda_dtype residual_dtype, const float* norm_weight,
@@ -650,8 +650,9 @@ int kda_add_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const vo
  *
  *   C[M, N] = act(A[M, K] * B[N, K]^T + bias) + residual
  * The product, the bias, the activation and the residual are taken in float32;
- * C is rounded once, when stored. Every M takes one launch that reads B once
- * for few rows (decode), or tiles of the matrix cores.
+ * C is rounded once, when stored. One launch for every shape: tiles whose
+ * wavefronts split K where rows are few (decode, verification), larger ones for
+ * prefill.
  *
  * A, B, C    as kda_gemm (ab_dtype = KDA_BF16; C in c_dtype).
  * bias       float32 [N] or NULL.
@@ -660,7 +661,8 @@ int kda_add_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const vo
  * residual   [M, N] residual_dtype, row stride residual_ld (a multiple of 4),
  *            16-byte aligned, or NULL. It may be C itself (same pointer, stride
  *            and dtype: accumulated in place); any other overlap is rejected.
- * M = 0 does nothing. Sizes, strides and alignment as kda_gemm.
+ * M = 0 does nothing. Sizes, strides and alignment as kda_gemm; M and N below
+ * 2^24, lda + K and ldb + K below 2^22 (else KDA_ERR_UNSUPPORTED).
  * ---------------------------------------------------------------------- */
 typedef enum { KDA_ACT_NONE = 0, KDA_ACT_RELU = 1, KDA_ACT_SILU = 2, KDA_ACT_GELU = 3, KDA_ACT_SIGMOID = 4 } kda_activation;
 

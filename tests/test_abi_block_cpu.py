@@ -26,6 +26,7 @@ def test_add_rmsnorm_validation(fp8):
         assert norm(fp8, **{name: None}) == INVALID, name
     assert norm(fp8, M=-1) == INVALID and norm(fp8, M=1 << 31) == INVALID
     assert norm(fp8, K=0) == INVALID and norm(fp8, K=12) == UNSUPPORTED
+    assert norm(fp8, M=1 << 24) == UNSUPPORTED  # more threads than a launch holds
     for name in ("x_ld", "r_ld", "ro_ld", "y_ld"):
         assert norm(fp8, **{name: 504}) == INVALID, name
         assert norm(fp8, **{name: 516}) == INVALID, name
@@ -65,6 +66,8 @@ def test_gemm_epilogue_validation():
     assert gemm(abd=K.KDA_F32) == UNSUPPORTED and gemm(abd=2) == INVALID and gemm(cd=9) == INVALID and gemm(rd=9) == INVALID
     assert gemm(act=-1) == INVALID and gemm(act=5) == INVALID
     assert gemm(M=-1) == INVALID and gemm(N=0) == INVALID and gemm(K=0) == INVALID and gemm(K=252) == UNSUPPORTED
+    assert gemm(M=1 << 24) == UNSUPPORTED and gemm(N=1 << 24, ldc=1 << 24, ldr=1 << 24, bias=None) == UNSUPPORTED
+    assert gemm(lda=1 << 22) == UNSUPPORTED and gemm(ldb=1 << 22, N=2, ldc=4, ldr=4) == UNSUPPORTED
     assert gemm(lda=248) == INVALID and gemm(ldb=260) == INVALID and gemm(ldc=96) == INVALID and gemm(ldc=102) == INVALID
     assert gemm(ldr=96) == INVALID and gemm(ldr=101) == INVALID
     assert gemm(C=fake(1)) == INVALID and gemm(C=fake(2) + 64) == INVALID and gemm(C=fake(3)) == INVALID

@@ -26,7 +26,7 @@ def test_decode_tree_validation():
     for name in ("B", "N", "H"):
         assert tree(**{name: 0}) == INVALID, name
     assert tree(N=65) == UNSUPPORTED and tree(dk=64) == UNSUPPORTED and tree(dv=256) == UNSUPPORTED
-    assert tree(B=1 << 30, H=4) == INVALID
+    assert tree(B=1 << 30, H=4) == INVALID and tree(B=1, N=64, H=1 << 18) == INVALID
     assert tree(xd=2) == INVALID and tree(sd=-1) == INVALID and tree(od=7) == INVALID
     assert tree(lb=0.5) == INVALID and tree(lb=float("nan")) == INVALID
     for name in ("q", "k", "v", "g", "beta", "s", "par"):
@@ -78,6 +78,7 @@ def test_conv_tree_common_validation(fn):
         assert fn(**{name: None}) == INVALID and fn(**{name: BIG + 2}) == INVALID, name
     for name in ("B", "N"):
         assert fn(**{name: 0}) == INVALID, name
+    assert fn(B=1 << 24, N=1) == UNSUPPORTED
     assert fn(N=65) == UNSUPPORTED and fn(C=0) == UNSUPPORTED and fn(C=192) == UNSUPPORTED
     assert fn(W=1) == UNSUPPORTED and fn(W=9) == UNSUPPORTED and fn(d=4) == INVALID
     assert fn(ld=504) == INVALID and fn(ld=516) == INVALID

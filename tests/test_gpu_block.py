@@ -168,6 +168,58 @@ def test_block_fp8_tree_step():
     assert torch.equal(state, s1) and torch.equal(conv, c1)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_survives_a_decode_before_its_commit(fp8):
+    """Decoding as many rows as the tree has, between its verification and its
+    commit, leaves what the commit needs alone (of the block and of the mixer)."""
+    announce("block tree, decode, commit fp8=%s" % fp8)
+    block, state, conv, drafts, par = prefilled(fp8)
+    acc = torch.tensor([4, 5], dtype=torch.int32, device="cuda")
+    rows = B * N
+    other = torch.zeros((rows, H, 128, 128), device="cuda"), torch.zeros((3, rows, 3, W), dtype=torch.bfloat16, device="cuda")
+    x = torch.randn((rows, 256), generator=torch.Generator().manual_seed(9)).cuda()
+    for verify, decode in (
+            (lambda: block.decode_tree(drafts.reshape(rows, 256).clone(), par, state, conv)[1],
+             lambda: block.decode(x.clone(), *other)),
+            (lambda: block.mixer.decode_tree(drafts.bfloat16(), par, state, conv)[1],
+             lambda: block.mixer.decode(x.bfloat16(), *other))):
+        s1, c1, s2, c2 = state.clone(), conv.clone(), state.clone(), conv.clone()
+        verify().commit(acc, s1, c1)
+        tree = verify()
+        decode()
+        tree.commit(acc, s2, c2)
+        torch.cuda.synchronize()
+        assert torch.equal(s1, s2) and torch.equal(c1, c2) and not torch.equal(s1, state)
+
+
+def test_calls_on_another_stream_and_without_rows():
+    """On a side stream the calls run there (their result waits for that stream's
+    work); no rows are no work."""
+    announce("other stream, no rows")
+    s = torch.cuda.Stream()
+    x = torch.ones((64, 1024), device="cuda")
+    w, y, y2 = torch.ones(1024, device="cuda"), torch.zeros((64, 1024), device="cuda"), torch.zeros((64, 1024), device="cuda")
+    A, Bm = torch.ones((40, 512), device="cuda").bfloat16(), torch.ones((24, 512), device="cuda").bfloat16()
+    C, C2 = torch.zeros((40, 24), device="cuda"), torch.zeros((40, 24), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for _ in range(200):  # a queue of work before the inputs are ready
+            x.mul_(1.0)
+        x.mul_(3.0)
+        A.mul_(2.0)
+        K.kda_add_rmsnorm(x, w, y, residual=x)
+        K.kda_gemm_epilogue(A, Bm, C)
+    K.kda_gemm_epilogue(A, Bm, C2, stream=s)
+    K.kda_add_rmsnorm(x, w, y2, residual=x, stream=s)
+    torch.cuda.synchronize()
+    assert (C == 1024).all() and torch.equal(C, C2) and torch.equal(y, y2)
+    assert relerr(host64(y), np.ones((64, 1024))) < 1e-6
+    K.kda_add_rmsnorm(x[:0], w, y[:0])
+    K.kda_add_rmsnorm_fp8(x[:0], w, torch.empty((0, 1024), dtype=torch.uint8, device="cuda"), torch.empty((0, 8), device="cuda"))
+    K.kda_gemm_epilogue(A[:0], Bm, C[:0], residual=C[:0])
+    torch.cuda.synchronize()
+
+
 def test_mixer_decode_tree_matches_decode():
     """The bare mixer: a one-node tree is a decode step (outputs to the projections'
     rounding), commits to the same states."""
