@@ -465,8 +465,9 @@ def kda_output_norm_gate_fp8(o, gate, norm_weight, y_codes, y_scales, eps=1e-6, 
 
 # --------------------------------------------------------------------------
 # The calls below are made once per token of a decode step, where their host
-# time counts as much as the kernels': one metadata query per fact, the raw
-# stream and the bound function taken directly.
+# time counts as much as the kernels': each tests all that has to hold in one
+# expression and goes through the checks that name the fault only where it does not;
+# the raw stream and the bound function are taken directly.
 _DTYPES = {torch.float32: KDA_F32, torch.bfloat16: KDA_BF16}
 _fns = {}
 
@@ -507,7 +508,7 @@ def _call_on(name, tensors, stream, *args):
     current for the call; without a stream on that device's current one."""
     index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and (t.get_device() != index or index < 0):
+        if t is not None and t.get_device() != index or index < 0:
             raise ValueError("%s: all tensors must be on one GPU device (got %s and %s)" % (name, tensors[0].device, t.device))
     fn = _fns.get(name)
     if fn is None:
@@ -532,12 +533,17 @@ def kda_decode_tree(q, k, v, g, beta, parents, state, o, writes=None, scale=1.0,
         raise ValueError("q must be [B, N, H, 128]")
     B, N, H, dk = shape
     dv = v.shape[-1]
-    vshape = (B, N, H, dv)
-    _tensor("q", q, shape), _tensor("k", k, shape), _tensor("g", g, shape), _tensor("v", v, vshape)
-    _tensor("beta", beta, (B, N, H)), _tensor("parents", parents, (B, N)), _tensor("state", state, (B, H, dk, dv))
-    _tensor("o", o, vshape)
-    xd = q.dtype
-    _type("k", k, xd), _type("g", g, xd), _type("v", v, xd), _type("beta", beta, xd), _type("parents", parents, torch.int32)
+    vshape, xd = (B, N, H, dv), q.dtype
+    if not (k.shape == shape and g.shape == shape and v.shape == vshape and beta.shape == (B, N, H) and
+            parents.shape == (B, N) and state.shape == (B, H, dk, dv) and o.shape == vshape and
+            k.dtype is xd and g.dtype is xd and v.dtype is xd and beta.dtype is xd and parents.dtype is torch.int32 and
+            q.is_contiguous() and k.is_contiguous() and g.is_contiguous() and v.is_contiguous() and
+            beta.is_contiguous() and parents.is_contiguous() and state.is_contiguous() and o.is_contiguous()):
+        _tensor("q", q, shape), _tensor("k", k, shape), _tensor("g", g, shape), _tensor("v", v, vshape)
+        _tensor("beta", beta, (B, N, H)), _tensor("parents", parents, (B, N)), _tensor("state", state, (B, H, dk, dv))
+        _tensor("o", o, vshape)
+        _type("k", k, xd), _type("g", g, xd), _type("v", v, xd), _type("beta", beta, xd)
+        _type("parents", parents, torch.int32)
     if writes is not None:
         _tensor("writes", writes, vshape), _type("writes", writes, torch.float32)
     _call_on("kda_decode_tree", (q, k, v, g, beta, parents, state, o, writes), stream, q.data_ptr(), k.data_ptr(),
@@ -556,10 +562,15 @@ def kda_decode_tree_commit(k, g, writes, parents, accepted, state, lower_bound=-
         raise ValueError("k must be [B, N, H, 128]")
     B, N, H, dk = shape
     dv = writes.shape[-1]
-    _tensor("k", k, shape), _tensor("g", g, shape), _tensor("writes", writes, (B, N, H, dv))
-    _tensor("parents", parents, (B, N)), _tensor("accepted", accepted, (B,)), _tensor("state", state, (B, H, dk, dv))
-    _type("g", g, k.dtype), _type("writes", writes, torch.float32)
-    _type("parents", parents, torch.int32), _type("accepted", accepted, torch.int32)
+    if not (g.shape == shape and writes.shape == (B, N, H, dv) and parents.shape == (B, N) and accepted.shape == (B,) and
+            state.shape == (B, H, dk, dv) and g.dtype is k.dtype and writes.dtype is torch.float32 and
+            parents.dtype is torch.int32 and accepted.dtype is torch.int32 and
+            k.is_contiguous() and g.is_contiguous() and writes.is_contiguous() and parents.is_contiguous() and
+            accepted.is_contiguous() and state.is_contiguous()):
+        _tensor("k", k, shape), _tensor("g", g, shape), _tensor("writes", writes, (B, N, H, dv))
+        _tensor("parents", parents, (B, N)), _tensor("accepted", accepted, (B,)), _tensor("state", state, (B, H, dk, dv))
+        _type("g", g, k.dtype), _type("writes", writes, torch.float32)
+        _type("parents", parents, torch.int32), _type("accepted", accepted, torch.int32)
     _call_on("kda_decode_tree_commit", (k, g, writes, parents, accepted, state), stream, k.data_ptr(), g.data_ptr(),
              _code(k, "k"), writes.data_ptr(), parents.data_ptr(), accepted.data_ptr(), B, N, H, dk, dv, lower_bound,
              state.data_ptr(), _code(state, "state"))
@@ -569,8 +580,10 @@ def kda_decode_tree_commit(k, g, writes, parents, accepted, state, lower_bound=-
 def _conv_tree_sizes(x, conv_state, parents):
     B, N = parents.shape
     b, w1, C = conv_state.shape
-    _tensor("conv_state", conv_state, (B, w1, C)), _tensor("parents", parents, (B, N))
-    _type("conv_state", conv_state, x.dtype), _type("parents", parents, torch.int32)
+    if not (conv_state.dtype is x.dtype and parents.dtype is torch.int32 and conv_state.is_contiguous() and
+            parents.is_contiguous()):
+        _tensor("conv_state", conv_state, (B, w1, C)), _tensor("parents", parents, (B, N))
+        _type("conv_state", conv_state, x.dtype), _type("parents", parents, torch.int32)
     return _mat("x", x, (B * N, C)), B, N, C, w1 + 1
 
 
@@ -580,8 +593,10 @@ def kda_conv_tree(x, conv_state, parents, weight, y, bias=None, apply_silu=True,
     allowed), conv_state [B,W-1,C] (read only), parents int32 [B,N] (as
     kda_decode_tree), weight [C,W], y [B*N,C]."""
     ld, B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
-    _tensor("weight", weight, (C, W)), _tensor("y", y, (B * N, C))
-    _type("weight", weight, x.dtype), _type("y", y, x.dtype)
+    if not (weight.shape == (C, W) and y.shape == (B * N, C) and weight.dtype is x.dtype and y.dtype is x.dtype and
+            weight.is_contiguous() and y.is_contiguous()):
+        _tensor("weight", weight, (C, W)), _tensor("y", y, (B * N, C))
+        _type("weight", weight, x.dtype), _type("y", y, x.dtype)
     if bias is not None:
         _tensor("bias", bias, (C,)), _type("bias", bias, x.dtype)
     _call_on("kda_conv_tree", (x, conv_state, parents, weight, y, bias), stream, x.data_ptr(), ld, conv_state.data_ptr(),
@@ -594,7 +609,8 @@ def kda_conv_tree_commit(x, parents, accepted, conv_state, stream=None):
     """conv_state[b] <- the last W-1 inputs of itself followed by the path to node
     accepted[b] of the tree (x, parents as for kda_conv_tree), in place."""
     ld, B, N, C, W = _conv_tree_sizes(x, conv_state, parents)
-    _tensor("accepted", accepted, (B,)), _type("accepted", accepted, torch.int32)
+    if not (accepted.shape == (B,) and accepted.dtype is torch.int32 and accepted.is_contiguous()):
+        _tensor("accepted", accepted, (B,)), _type("accepted", accepted, torch.int32)
     _call_on("kda_conv_tree_commit", (x, parents, accepted, conv_state), stream, x.data_ptr(), ld, parents.data_ptr(),
              accepted.data_ptr(), _code(x, "x"), B, N, C, W, conv_state.data_ptr())
     return conv_state
@@ -604,18 +620,20 @@ def _add_rmsnorm_args(x, norm_weight, residual, residual_out):
     shape = x.shape
     if len(shape) != 2:
         raise ValueError("x must be [M, K]")
-    if norm_weight.shape != shape[1:] or norm_weight.dtype != torch.float32 or not norm_weight.is_contiguous():
+    if norm_weight.shape != shape[1:] or norm_weight.dtype is not torch.float32 or not norm_weight.is_contiguous():
         raise TypeError("norm_weight must be dense float32 [K]")
-    res = (None, 0, None, 0, KDA_F32)
+    r = ro = None
+    r_ld = ro_ld = 0
+    rd = KDA_F32
     if residual is not None:
-        rd = _code(residual, "residual")
-        res = (residual.data_ptr(), _mat("residual", residual, shape), None, 0, rd)
+        r, r_ld, rd = residual.data_ptr(), _mat("residual", residual, shape), _code(residual, "residual")
         if residual_out is not None:
             _type("residual_out", residual_out, residual.dtype)
-            res = res[:2] + (residual_out.data_ptr(), _mat("residual_out", residual_out, shape), rd)
+            ro, ro_ld = residual_out.data_ptr(), _mat("residual_out", residual_out, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    return (x.data_ptr(), _mat("x", x, shape), _code(x, "x")) + res + (norm_weight.data_ptr(), shape[0], shape[1])
+    return (x.data_ptr(), _mat("x", x, shape), _code(x, "x"), r, r_ld, ro, ro_ld, rd, norm_weight.data_ptr(), shape[0],
+            shape[1])
 
 
 def kda_add_rmsnorm(x, norm_weight, y, residual=None, residual_out=None, eps=1e-6, stream=None):
