@@ -313,6 +313,12 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
     const TIN* pq_ = static_cast<const TIN*>(a.q) + base;
     const TIN* pv = static_cast<const TIN*>(a.v) + base;
     const int c2 = CW * wave + CT * m16;  // this lane's CT value channels
+    // the n-th node this lane's group of 16 walks: later nodes lie deeper, so the
+    // odd rounds deal their nodes the other way about (places past the end as they are)
+    auto walk_node = [&](int n) {
+        const int first = 4 * NW * n, x = 4 * wave + q4, count = min(4 * NW, N - first);
+        return first + (n % 2 && x < count ? count - 1 - x : x);
+    };
     const int parent_in = load_parent(a.parents + (size_t)b * N, N);
     typename R::R4 rk[KR], rg[KR], rq[WR][2];
     typename R::RC rv[MO][4];
@@ -326,7 +332,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
     for (int r = 0; r < WR; ++r)
 #pragma unroll
         for (int p = 0; p < 2; ++p)
-            rq[r][p] = *reinterpret_cast<const typename R::R4*>(pq_ + at(4 * NW * r + 4 * wave + q4) + 64 * p + 4 * m16);
+            rq[r][p] = *reinterpret_cast<const typename R::R4*>(pq_ + at(walk_node(r)) + 64 * p + 4 * m16);
 #pragma unroll
     for (int m = 0; m < MO; ++m)
 #pragma unroll
@@ -379,7 +385,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
     // walk: node i by 16 lanes, lane channels 4 m16 .. and 64 + 4 m16 ..
 #pragma unroll
     for (int n = 0; n < WR; ++n) {
-        const int i = 4 * NW * n + 4 * wave + q4;
+        const int i = walk_node(n);
         if (i >= NP) break;
         int j = there >> i & 1 ? i : -1;
         f32x4 q[2], k[2], decay[2];
