@@ -231,12 +231,12 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 // nodes 158 us = 5.1 TB/s (a copy reaches 5.1), 64 of 8 nodes 55 us = 6.1 TB/s; above,
 // the walk (of 64 trees of 32 nodes it took 73 of 188 us, skipped for the measurement) and the
 // products (54 us).
-// NP: N rounded up to 8, 16, 32 or 64.
-// NW wavefronts: 4, and 8 for NP = 64, where LDS leaves room for one workgroup a
+// NP: N rounded up to 8, 16, 32, 48 or 64.
+// NW wavefronts: 4, and 8 for NP > 32, where LDS leaves room for one workgroup a
 // compute unit and 4 wavefronts left a SIMD with one to cover every latency of
 // the walk and the substitution (32 trees of 64 nodes, 64 heads: 320 | 275 us with 4 | 8;
 // 64 of 32 nodes 178 | 189, so 4 there).
-template <int NP> constexpr int kTreeWaves = NP == 64 ? 8 : 4;
+template <int NP> constexpr int kTreeWaves = NP > 32 ? 8 : 4;
 template <int NP> constexpr int kTreePerSimd = NP <= 16 ? 4 : 2;  // wavefronts per SIMD (by LDS and registers)
 
 // f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
@@ -556,7 +556,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
         for (int s = 0; s < 4; ++s) {
             const int k = 16 * g + 4 * q4 + s;
             u[s] = 0.0f;
-            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const cols*>(&s_row[NP + (k & (NP - 1))][c2]);
+            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const cols*>(&s_row[NP + (NP >= 16 ? k : k & 7)][c2]);
         }
 #pragma unroll
         for (int m = g; m < MO; ++m) {
@@ -564,7 +564,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 const int k = 16 * g + 4 * q4 + s;
-                const float p = k <= i ? s_pa[i & (NP - 1)][k & (NP - 1)] : 0.0f;
+                const float p = k <= i ? s_pa[NP >= 16 ? i : i & 7][NP >= 16 ? k : k & 7] : 0.0f;
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
                     acc[MT - MO + m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(p, u[s][c], acc[MT - MO + m][c], 0, 0, 0);
@@ -683,6 +683,7 @@ hipError_t launch_tree_t(const TreeArgs& a, hipStream_t s)
     if (a.N <= 8) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 8>), grid, block, 0, s, a);
     else if (a.N <= 16) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 16>), grid, block, 0, s, a);
     else if (a.N <= 32) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 32>), grid, block, 0, s, a);
+    else if (a.N <= 48) hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 48>), grid, wide, 0, s, a);
     else hipLaunchKernelGGL((decode_tree_kernel<TIN, TOUT, TS, 64>), grid, wide, 0, s, a);
     return hipGetLastError();
 }

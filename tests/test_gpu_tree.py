@@ -121,6 +121,8 @@ CASES = [
     (3, 64, 1, BF, BF, BF, "random", -5.0, 1.0), (2, 64, 1, F, F, F, "holes", 0.0, 1.0),
     (2, 12, 2, F, F, F, "random", float("-inf"), 1.0), (2, 5, 2, F, F, F, "none", -5.0, 1.0),
     (1, 6, 64, BF, F, F, "random", -5.0, 1.0), (130, 3, 3, BF, F, F, "random", -5.0, 1.0),
+    (2, 24, 2, F, F, F, "holes", -5.0, 1.0), (2, 40, 1, BF, F, F, "random", -5.0, 1.0), (1, 48, 2, F, BF, F, "chain", -5.0, 1.0),
+    (2, 49, 1, BF, BF, BF, "holes", -5.0, 1.0), (2, 57, 2, F, F, F, "binary", -5.0, 1.0),
 ]
 
 
@@ -206,7 +208,7 @@ def test_chain_equals_decode_multi():
         assert relerr(host64(s1), host64(s2)) < TOL_F32
 
 
-@pytest.mark.parametrize("N", [7, 16, 30, 64])
+@pytest.mark.parametrize("N", [7, 16, 30, 45, 64])
 def test_decode_tree_branches_do_not_touch(N):
     """NaN and infinity in one node reach that node and what is below it, and
     nothing else, not even the last bits."""
