@@ -228,16 +228,20 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 //          independent operations); then o += P u by the matrix instruction on
 //          the accumulators that hold (D q) S0.
 // What bounds it (float32 states, 64 heads): up to 16 nodes HBM, 128 trees of 16
-// nodes 158 us = 5.1 TB/s (a copy reaches 5.1), 64 of 8 nodes 55 us = 6.1 TB/s; above,
-// the walk (of 64 trees of 32 nodes it took 73 of 188 us, skipped for the measurement) and the
-// products (54 us).
+// nodes 158-170 us = 4.7-5.1 TB/s (a copy reaches 5.1), 64 of 8 nodes 56 us = 6.0 TB/s;
+// above, the walk (with it skipped, 64 trees of 32 nodes took 115 of 188 us, 32 of 64
+// nodes 166 of 320, before the forms below) and the products. Now 64 of 32 nodes 157 us, 64 of
+// 40 264 us, 32 of 64 263 us. Tried and slower up to 32 nodes: all pairs at once as a
+// matrix product of rows scaled by exp(G + C) and exp(-G - C), C a center per
+// channel (128 of 16 nodes 157 | 180 us; the loads before the state's get more and
+// smaller).
 // NP: N rounded up to 8, 16, 32, 48 or 64.
-// NW wavefronts: 4, and 8 for NP > 32, where LDS leaves room for one workgroup a
-// compute unit and 4 wavefronts left a SIMD with one to cover every latency of
-// the walk and the substitution (32 trees of 64 nodes, 64 heads: 320 | 275 us with 4 | 8;
-// 64 of 32 nodes 178 | 189, so 4 there).
+// NW wavefronts: 4, and 8 for NP > 32, where a compute unit holds one or two
+// workgroups and 4 wavefronts each left a SIMD with too few to cover the latencies of the
+// walk and the substitution (32 trees of 64 nodes 320 | 275 us with 4 | 8; 64 of 32 nodes
+// 178 | 189, so 4 there).
 template <int NP> constexpr int kTreeWaves = NP > 32 ? 8 : 4;
-template <int NP> constexpr int kTreePerSimd = NP <= 16 ? 4 : 2;  // wavefronts per SIMD (by LDS and registers)
+template <int NP> constexpr int kTreePerSimd = NP <= 16 || NP == 48 ? 4 : (NP == 32 ? 3 : 2);  // wavefronts per SIMD (by LDS and registers)
 
 // f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
 // constants from the start (a loop unrolled late left the remainders of the
@@ -283,14 +287,19 @@ template <typename TIN, typename TOUT, typename TS, int NP>
 __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_tree_kernel(TreeArgs a)
 {
     constexpr int NW = kTreeWaves<NP>, CT = 8 / NW, CW = 16 * CT;  // value channels: CT column tiles a wavefront
-    constexpr bool kAhead = NP > 16 || sizeof(TS) == 2;            // (with a float32 state the registers do not suffice)
+    constexpr bool kAhead = NP == 64 || (NP <= 32 && sizeof(TS) == 2);  // (elsewhere the registers do not suffice)
     typedef cols_t<CT> cols;
-    constexpr int LD = D + 4;                  // row of the decayed rows: 16 rows at one column meet distinct banks
     constexpr int LP = NP + 4;
     constexpr int MT = 2 * NP / 16;            // row tiles: D k, then D q (NP = 8: one tile holds both)
     constexpr int MO = NP >= 16 ? NP / 16 : 1;  // row tiles of o, the last MO
-    __shared__ __attribute__((aligned(16))) float s_row[2 * NP][LD];  // D k and D q; then (D k) S0 and the writes u
-    __shared__ __attribute__((aligned(16))) float s_k[NP][D], s_al[NP][D];
+    // k and alpha (rows) while the paths are walked; then the decayed rows D k and D q,
+    // then (D k) S0 and the writes u, with a row's 16-byte quads XORed by its index,
+    // so that 16 rows at one column meet distinct banks. (One region for both, where
+    // they had two: workgroups a compute unit 2 -> 3 for 32 nodes, 1 -> 2 for 48.)
+    __shared__ __attribute__((aligned(16))) float s_buf[2 * NP * D];
+    float(*s_k)[D] = reinterpret_cast<float(*)[D]>(s_buf);
+    float(*s_al)[D] = s_k + NP;
+    auto row = [&](int r, int c) { return &s_buf[r * D + ((((c >> 2) ^ r) & 15) << 2) + (c & 64) + (c & 3)]; };
     // P[i][j] = q_i . D(i,j) k_j at [i][j] (j <= i), A[i][j] = k_i . D(i,j) k_j at [j][i] (j < i)
     __shared__ __attribute__((aligned(16))) float s_pa[NP][LP];
     __shared__ float s_beta[NP];
@@ -368,21 +377,8 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
     for (int e = t; e < NP * LP; e += 64 * NW) (&s_pa[0][0])[e] = 0.0f;
     lds_barrier();
 
-    // the products' accumulators: rows 4 q4 + e of a tile, columns c2 ...
-    // The tiles of (D k) S0 start at -v, so that they end at minus the
-    // substitution's right-hand side.
-    f32x4 acc[MT][CT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            cols v = 0.0f;
-            if (m < MO && (NP >= 16 || q4 < 2)) v = R::fc(rv[m][e]);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) acc[m][c][e] = -v[c];
-        }
-
     // walk: node i by 16 lanes, lane channels 4 m16 .. and 64 + 4 m16 ..
+    f32x4 kd[WR][2], qd[WR][2];  // the decayed rows wait here until everyone has walked
 #pragma unroll
     for (int n = 0; n < WR; ++n) {
         const int i = walk_node(n);
@@ -453,29 +449,54 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
         }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            *reinterpret_cast<f32x4*>(&s_row[i][64 * p + 4 * m16]) = k[p] * decay[p];
-            *reinterpret_cast<f32x4*>(&s_row[NP + i][64 * p + 4 * m16]) = q[p] * decay[p];
+            kd[n][p] = k[p] * decay[p];
+            qd[n][p] = q[p] * decay[p];
         }
     }
     lds_barrier();
+#pragma unroll
+    for (int n = 0; n < WR; ++n) {
+        const int i = walk_node(n);
+        if (i >= NP) break;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            *reinterpret_cast<f32x4*>(row(i, 64 * p + 4 * m16)) = kd[n][p];
+            *reinterpret_cast<f32x4*>(row(NP + i, 64 * p + 4 * m16)) = qd[n][p];
+        }
+    }
+    lds_barrier();
+
+    // the products' accumulators: rows 4 q4 + e of a tile, columns c2 ...
+    // The tiles of (D k) S0 start at -v, so that they end at minus the
+    // substitution's right-hand side.
+    f32x4 acc[MT][CT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            cols v = 0.0f;
+            if (m < MO && (NP >= 16 || q4 < 2)) v = R::fc(rv[m][e]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[m][c][e] = -v[c];
+        }
 
     // read: lane (m16, q4) gives row m16 of a tile, K element 16 g + 4 q4 + s in
     // step (g, s), and takes rows 4 q4 + e of column tile c (columns CT m16 + c)
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-        f32x4 row[MT];
+        f32x4 x[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) row[m] = *reinterpret_cast<const f32x4*>(&s_row[16 * m + m16][16 * g + 4 * q4]);
+        for (int m = 0; m < MT; ++m) x[m] = *reinterpret_cast<const f32x4*>(row(16 * m + m16, 16 * g + 4 * q4));
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const cols st = RS::fc(raw[g][s]);
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int c = 0; c < CT; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(row[m][s], st[c], acc[m][c], 0, 0, 0);
+                for (int c = 0; c < CT; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[m][s], st[c], acc[m][c], 0, 0, 0);
         }
     }
-    lds_barrier();  // s_row is read: its halves now hold (D k) S0 and u, each wavefront its own columns
+    lds_barrier();  // the rows are read: they now take (D k) S0 and u, each wavefront its own columns
     __builtin_amdgcn_sched_barrier(0);
 
     // solve: the 64 / CW lanes of a channel hold the same values
@@ -493,7 +514,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
             for (int s = 0; s < 4; ++s) {
                 const int k = 16 * J + 4 * q4 + s;
                 const float A = s_pa[k][16 * I + m16];
-                const cols u = *reinterpret_cast<const cols*>(&s_row[NP + k][c2]);
+                const cols u = *reinterpret_cast<const cols*>(row(NP + k, c2));
 #pragma unroll
                 for (int c = 0; c < CT; ++c) acc[I][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(A, u[c], acc[I][c], 0, 0, 0);
             }
@@ -504,13 +525,13 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
                 cols v;
 #pragma unroll
                 for (int c = 0; c < CT; ++c) v[c] = acc[I][c][e];
-                *reinterpret_cast<cols*>(&s_row[16 * I + 4 * q4 + e][c2]) = v;
+                *reinterpret_cast<cols*>(row(16 * I + 4 * q4 + e, c2)) = v;
             }
         // within the block
         constexpr int BN_ = NP < 16 ? NP : 16, i0 = 16 * I;
         float r[BN_], beta_[BN_];
         static_for<BN_>([&](auto n) {
-            r[n] = -s_row[i0 + n][col];
+            r[n] = -*row(i0 + n, col);
             beta_[n] = s_beta[i0 + n];
         });
         // row j of A is read while row j - 1 is used
@@ -528,7 +549,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
             const bool fine = fabsf(u) < __builtin_inff();
             const float w = fine ? u : 0.0f;
             if (!fine) bad |= (uint64_t)1 << (i0 + j);
-            s_row[NP + i0 + j][col] = w;
+            *row(NP + i0 + j, col) = w;
             static_for<BN_>([&](auto n) {
                 if constexpr (n > j) r[n] -= A[j % 2][n / 4][n % 4] * w;
             });
@@ -544,7 +565,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
         for (int i0 = 0; i0 < NP; i0 += 64 / kLanes) {
             const int i = i0 + lane / kLanes;
             if (i < N)
-                __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(&s_row[NP + i][cw]),
+                __builtin_nontemporal_store(*reinterpret_cast<const f32x4*>(row(NP + i, cw)),
                                             reinterpret_cast<f32x4*>(a.writes + row_of(i) * D + cw));
         }
     }
@@ -556,7 +577,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
         for (int s = 0; s < 4; ++s) {
             const int k = 16 * g + 4 * q4 + s;
             u[s] = 0.0f;
-            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const cols*>(&s_row[NP + (NP >= 16 ? k : k & 7)][c2]);
+            if (NP >= 16 || k < NP) u[s] = *reinterpret_cast<const cols*>(row(NP + (NP >= 16 ? k : k & 7), c2));
         }
 #pragma unroll
         for (int m = g; m < MO; ++m) {
