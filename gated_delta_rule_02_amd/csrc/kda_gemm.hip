@@ -24,6 +24,7 @@
 // 8-byte (bfloat16) access.
 // The fallback (any K multiple of 8): 128 x 128 tiles, 2 x 2 wavefronts of
 // 64 x 64, K steps of 32 through double-buffered LDS.
+#include <climits>
 #include <cmath>
 
 #include "kda_device.h"
@@ -45,30 +46,6 @@ __device__ __forceinline__ float activate(int act, float y)
         case 4: return sigmoidf_(y);
         default: return y;
     }
-}
-__device__ __forceinline__ float epilogue1(const GemmArgs& a, int64_t row, int64_t col, float v)
-{
-    if (a.bias) v += a.bias[col];
-    v = activate(a.act, v);
-    if (a.res) {
-        const int64_t i = row * a.ldr + col;
-        v += a.r_dtype == F32 ? static_cast<const float*>(a.res)[i] : bf16_to_f32(static_cast<const bf16_t*>(a.res)[i]);
-    }
-    return v;
-}
-// columns col .. col + 3 (col a multiple of 4, all of them inside N)
-__device__ __forceinline__ f32x4 epilogue4(const GemmArgs& a, int64_t row, int64_t col, f32x4 v)
-{
-    if (a.bias) v += *reinterpret_cast<const f32x4*>(a.bias + col);
-    if (a.act) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = activate(a.act, v[e]);
-    }
-    if (a.res) {
-        const int64_t i = row * a.ldr + col;
-        v += a.r_dtype == F32 ? ld4(static_cast<const float*>(a.res) + i) : ld4(static_cast<const bf16_t*>(a.res) + i);
-    }
-    return v;
 }
 
 // Workgroup -> tile of the epilogue entry's tiled kernels. Workgroup ids go round
@@ -114,6 +91,7 @@ __device__ __forceinline__ void tile_epilogue(const GemmArgs& a, const f32x4 (&a
                                               int64_t col0)
 {
     constexpr int kLd = 16 * NJ + 4, kLanes = 4 * NJ, kRows = 64 / kLanes;  // kRows rows a step, NJ steps
+    static_assert(64 % kLanes == 0, "whole rows a step");
     const int lane = threadIdx.x & 63, m16 = lane & 15, q4 = lane >> 4;
     const int r0 = lane / kLanes, c0 = 4 * (lane % kLanes);
     const int64_t col = col0 + c0;
@@ -300,23 +278,33 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // row's K chunk slot ^ ((row / 2) mod 8))
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)&smem[0][0][0];
     const int lrow = lane >> 3, lslot = lane & 7;
-    auto copy = [&](int kt, int st) {
+    // (k_end: in the epilogue entry K is any multiple of 8; a last step that K
+    // does not fill sends its chunks past K outside either descriptor, as zeros)
+    auto copy_to = [&](int kt, int st, int k_end) {
 #pragma unroll
         for (int j = 0; j < kACopy; ++j) {
             const int i = wave * kACopy + j;
             const int row = 8 * i + lrow;
-            const int koff = (kt * TK + (lslot ^ ((row >> 1) & 7)) * 8) * 2;
+            const int k = kt * TK + (lslot ^ ((row >> 1) & 7)) * 8;
+            const int off = k < k_end ? (int)(row * a.lda * 2) + k * 2 : (int)0x80000000;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(uintptr_t)(lds0 + (st * 2 + 0) * kStageBytes + i * 1024),
-                                                     16, (int)(row * a.lda * 2) + koff, 0, 0, 0);
+                                                     16, off, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < kBCopy; ++j) {
             const int i = wave * kBCopy + j;
             const int row = 8 * i + lrow;
-            const int koff = (kt * TK + (lslot ^ ((row >> 1) & 7)) * 8) * 2;
+            const int k = kt * TK + (lslot ^ ((row >> 1) & 7)) * 8;
+            const int off = k < k_end ? (int)(row * a.ldb * 2) + k * 2 : (int)0x80000000;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(uintptr_t)(lds0 + (st * 2 + 1) * kStageBytes + i * 1024),
-                                                     16, (int)(row * a.ldb * 2) + koff, 0, 0, 0);
+                                                     16, off, 0, 0, 0);
         }
+    };
+    const int nk = (int)((a.K + TK - 1) / TK);
+    const bool ragged = EPI && a.K % TK != 0;
+    auto copy = [&](int kt, int st) {
+        if (ragged && kt == nk - 1) copy_to(kt, st, (int)a.K);
+        else copy_to(kt, st, INT_MAX);
     };
 
     f32x4 acc[8][NJ];
@@ -331,7 +319,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // MFMAs run. At its end every wavefront waits for its copy (the compiler
     // does not track these copies: the wait is explicit) and the barrier
     // hands the stage over.
-    const int nk = (int)(a.K / TK);
     u32x4_t fa[8], fb[NJ];
     auto read_a = [&](int st, int h, int i) {
         fa[i] = *reinterpret_cast<const u32x4_t*>(&smem[st][0][0] + swz(wm + 16 * i + m16, 4 * h + q4));
@@ -763,39 +750,48 @@ hipError_t launch_ring(const GemmArgs& a, hipStream_t s)
     return hipGetLastError();
 }
 
-// The form with the least cost: rounds of tiles over the 256 compute units, times the
-// rows of A and B that a tile takes in (K values each), times what a row costs in that form
-// relative to the K-split tiles. Those are bound by taking their rows in, so any
-// tile costs about its rows (measured at K = 8192, us per row and round: 64 x 64
-// 0.28, 96 x 64 0.245, 64 x 32 0.28, 32 x 32 0.33); the 128 x 128 tiles cost 0.30 a
-// row; the 256 x 256 tiles 0.42 (bound by the matrix instructions instead, and the
-// only ones that reach 1.3 PFLOP/s). 4096 columns, K = 8192, us, this choice | the
-// next tile up: 16 rows 14.5 | 15.2, 64 rows 21.0 | 27.6, 96 rows 23.2 | 32.2, 192
-// rows 32.5 | 36.0, 333 rows 38.8 | 72, 1024 rows 79 | 203, 4096 rows 220 | 302.
+// The form with the least cost: rounds of tiles over the 256 compute units, times what a
+// tile costs: the rows of A and B that it takes in, K values each, at a rate relative to
+// the K-split tiles', plus what starts and ends it (the first loads' latency, the
+// epilogue) in the same unit (60,000 is about 2 us). Both numbers are fitted to the
+// times of every form at 365 sizes (1 to 8,192 rows, 36 to 41,024 columns, K 136 to
+// 8,192), where this choice is 0.9 per cent (geometric mean) above the best form. The
+// tiles that are bound by taking their rows in cost about their rows; the 256 x 256
+// ones are bound by the matrix instructions instead, are the only ones that reach 1.3
+// PFLOP/s, and pay most at their ends (one wavefront a SIMD). Left out of the list, a
+// form costs over all sizes: 16 x 16 4 per cent, 32 x 32, 64 x 64, 128 x 128 and
+// 192 x 128 1 each, the others 0.2 to 0.7; 32 x 16, 32 x 64, 128 x 64 and 128 x 256 tiles
+// gave less than 0.1 and are not built. 4096 columns, K = 8192, us, this choice | the
+// next best of the list: 1 row 13.8 | 14.9, 64 rows 19.9 | 26.4, 96 rows 22.6 | 30.9, 192 rows
+// 31.9 | 34.6, 333 rows 39.3 | 58.2, 1024 rows 77.0 | 94.6, 2048 rows 139 | 157, 3000
+// rows 202 | 216, 4096 rows 227 | 261.
 template <typename TC>
 hipError_t launch_epilogue(const GemmArgs& a, hipStream_t s)
 {
     struct Form {
         int tm, tn;
-        float row;
+        float row, ends;
         hipError_t (*launch)(const GemmArgs&, hipStream_t);
     };
     static const Form forms[] = {
-        {16, 16, 1.0f, launch_ring<TC, 1, 1, 8, 4>},   {16, 32, 1.0f, launch_ring<TC, 1, 2, 4, 6>},
-        {32, 16, 1.0f, launch_ring<TC, 2, 1, 4, 6>},   {32, 32, 1.0f, launch_ring<TC, 2, 2, 4, 4>},
-        {64, 32, 1.0f, launch_ring<TC, 4, 2, 4, 3>},   {32, 64, 1.0f, launch_ring<TC, 2, 4, 4, 3>},
-        {48, 64, 1.0f, launch_ring<TC, 3, 4, 4, 2>},   {64, 64, 1.0f, launch_ring<TC, 4, 4, 4, 2>},
-        {96, 64, 1.0f, launch_ring<TC, 6, 4, 4, 2>},   {128, 64, 1.2f, launch_ring<TC, 8, 4, 3, 2>},
-        {128, 128, 1.05f, launch_tile<TC, 128, 128, 4, 2, 4>},
-        {256, 256, 1.45f, launch_256<TC>},  // last: K a multiple of 64 only
+        {16, 16, 1.0f, 60e3f, launch_ring<TC, 1, 1, 8, 4>},
+        {16, 32, 1.0f, 60e3f, launch_ring<TC, 1, 2, 4, 6>},
+        {32, 32, 1.0f, 60e3f, launch_ring<TC, 2, 2, 4, 4>},
+        {64, 32, 1.0f, 60e3f, launch_ring<TC, 4, 2, 4, 3>},
+        {48, 64, 1.0f, 60e3f, launch_ring<TC, 3, 4, 4, 2>},
+        {64, 64, 1.0f, 60e3f, launch_ring<TC, 4, 4, 4, 2>},
+        {96, 64, 1.05f, 120e3f, launch_ring<TC, 6, 4, 4, 2>},
+        {128, 128, 1.1f, 100e3f, launch_tile<TC, 128, 128, 4, 2, 4>},
+        {192, 128, 1.15f, 140e3f, launch_tile<TC, 192, 128, 4, 2, 3>},
+        {256, 128, 1.15f, 240e3f, launch_tile<TC, 256, 128, 4, 2, 3>},
+        {256, 256, 1.4f, 660e3f, launch_256<TC>},
     };
-    constexpr int n = sizeof(forms) / sizeof(forms[0]);
     const Form* best = nullptr;
     double least = 0.0;
-    for (int f = 0; f < (a.K % 64 == 0 ? n : n - 1); ++f) {
-        const double tiles = (double)((a.M + forms[f].tm - 1) / forms[f].tm) * (double)((a.N + forms[f].tn - 1) / forms[f].tn);
-        const double cost = std::ceil(tiles / 256.0) * (forms[f].tm + forms[f].tn) * forms[f].row;
-        if (!best || cost < least) best = &forms[f], least = cost;
+    for (const Form& f : forms) {
+        const double tiles = (double)((a.M + f.tm - 1) / f.tm) * (double)((a.N + f.tn - 1) / f.tn);
+        const double cost = std::ceil(tiles / 256.0) * ((f.tm + f.tn) * f.row * (double)a.K + f.ends);
+        if (!best || cost < least) best = &f, least = cost;
     }
     return best->launch(a, s);
 }

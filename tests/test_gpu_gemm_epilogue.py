@@ -173,3 +173,25 @@ def test_gemm_epilogue_wide(M, N, k):
     ref, tol = expected(A, B, b, "silu", r)
     assert check(C[:, :N], ref, tol)
     assert torch.isnan(C[:, N:]).all()
+
+
+@pytest.mark.parametrize("M,N,k", [
+    (1000, 8190, 200), (2890, 2084, 72), (1500, 4104, 264), (4090, 4090, 1096), (3900, 4070, 1608), (1480, 3333, 264),
+    (700, 8190, 136), (1900, 4100, 520), (60, 2050, 1032), (150, 4100, 72),
+    (1500, 4100, 520), (2990, 2050, 520), (2050, 500, 264), (60, 1100, 72),
+])
+def test_gemm_epilogue_tall_tiles(M, N, k):
+    """The tall and the 256 x 256 tiles (and the small ones of long K) with every edge
+    ragged, K not a multiple of their step: what follows a row's last value is NaN, so a
+    chunk read past K would show in every column."""
+    announce("gemm_epilogue tall tiles M=%d N=%d K=%d" % (M, N, k))
+    pad = (24, 16, -N % 4)
+    A, B, b, res = make(M, N, k, M + N, pad)
+    for x in (A, B):
+        x.as_strided((x.shape[0], x.stride(0)), (x.stride(0), 1))[:, k:] = float("nan")
+    C = torch.full((M, N + pad[2]), float("nan"), dtype=BF if M % 200 else F, device="cuda")
+    K.kda_gemm_epilogue(A, B, C[:, :N], bias=b, activation="relu", residual=res[:, :N])
+    torch.cuda.synchronize()
+    ref, tol = expected(A, B, b, "relu", res[:, :N])
+    assert check(C[:, :N], ref, tol)
+    assert torch.isnan(C[:, N:]).all()
