@@ -281,25 +281,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // row's K chunk slot ^ ((row / 2) mod 8))
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)&smem[0][0][0];
     const int lrow = lane >> 3, lslot = lane & 7;
+    auto copy1 = [&](int kt, int st, int c) {  // copy c of the wavefront's kACopy + kBCopy
+        const bool isa = c < kACopy;
+        const int i = isa ? wave * kACopy + c : wave * kBCopy + c - kACopy;
+        const int row = 8 * i + lrow;
+        const int k = kt * TK + (lslot ^ ((row >> 1) & 7)) * 8;
+        const int off = TAIL && k >= a.K ? (int)0x80000000 : (int)(row * (isa ? a.lda : a.ldb) * 2) + k * 2;
+        lds_void* dst = (lds_void*)(uintptr_t)(lds0 + (st * 2 + (isa ? 0 : 1)) * kStageBytes + i * 1024);
+        if (isa) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, off, 0, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, off, 0, 0, 0);
+    };
     auto copy = [&](int kt, int st) {
 #pragma unroll
-        for (int j = 0; j < kACopy; ++j) {
-            const int i = wave * kACopy + j;
-            const int row = 8 * i + lrow;
-            const int k = kt * TK + (lslot ^ ((row >> 1) & 7)) * 8;
-            const int off = TAIL && k >= a.K ? (int)0x80000000 : (int)(row * a.lda * 2) + k * 2;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(uintptr_t)(lds0 + (st * 2 + 0) * kStageBytes + i * 1024),
-                                                     16, off, 0, 0, 0);
-        }
-#pragma unroll
-        for (int j = 0; j < kBCopy; ++j) {
-            const int i = wave * kBCopy + j;
-            const int row = 8 * i + lrow;
-            const int k = kt * TK + (lslot ^ ((row >> 1) & 7)) * 8;
-            const int off = TAIL && k >= a.K ? (int)0x80000000 : (int)(row * a.ldb * 2) + k * 2;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(uintptr_t)(lds0 + (st * 2 + 1) * kStageBytes + i * 1024),
-                                                     16, off, 0, 0, 0);
-        }
+        for (int c = 0; c < kACopy + kBCopy; ++c) copy1(kt, st, c);
     };
     const int nk = (int)((a.K + TK - 1) / TK);
 
@@ -315,6 +309,55 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // MFMAs run. At its end every wavefront waits for its copy (the compiler
     // does not track these copies: the wait is explicit) and the barrier
     // hands the stage over.
+    if constexpr (EPI) {
+        // The reads of one half run under the products of the other: the second half's
+        // of step kt under the first's products, the first half's of step kt + 1 under
+        // the second's. Between the two, once everyone has read all of stage kt and
+        // its copy of step kt + 1 has landed, the stage is refilled with step kt + 2.
+        u32x4_t fa[2][8], fb[2][NJ];
+        auto read = [&](int st, int h, int c) {  // fragment c: the NJ of B, then the 8 of A
+            if (c < NJ) fb[h][c] = *reinterpret_cast<const u32x4_t*>(&smem[st][1][0] + swz(wn + 16 * c + m16, 4 * h + q4));
+            else fa[h][c - NJ] = *reinterpret_cast<const u32x4_t*>(&smem[st][0][0] + swz(wm + 16 * (c - NJ) + m16, 4 * h + q4));
+        };
+        constexpr int kRead = (8 + NJ + 5) / 6;           // reads beside each of the first six rows of products
+        constexpr int kCopy = (kACopy + kBCopy + 7) / 8;  // copies beside each row
+        copy(0, 0);
+        if (nk > 1) copy(1, 1);
+        if (nk > 1) __builtin_amdgcn_s_waitcnt(0x0f70 | ((kACopy + kBCopy) & 15) | (((kACopy + kBCopy) >> 4) << 14));
+        else __builtin_amdgcn_s_waitcnt(0x0f70);
+        lds_barrier();
+#pragma unroll
+        for (int c = 0; c < NJ + 8; ++c) read(0, 0, c);
+        for (int kt = 0; kt < nk; ++kt) {
+            const int st = kt & 1;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fb[h][j]),
+                                                                            __builtin_bit_cast(bf16x8, fa[h][i]),
+                                                                            acc[i][j], 0, 0, 0);
+                    // (the last step's read of a step that is not there is not used)
+#pragma unroll
+                    for (int c = kRead * i; c < min(kRead * (i + 1), NJ + 8); ++c) read(h ? st ^ 1 : st, h ^ 1, c);
+                    if (h == 1 && kt + 2 < nk) {
+#pragma unroll
+                        for (int c = kCopy * i; c < min(kCopy * (i + 1), kACopy + kBCopy); ++c) copy1(kt + 2, st, c);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (h == 0) {
+                    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+                    lds_barrier();
+                }
+            }
+        }
+        tile_epilogue<TC, 8, NJ>(a, acc, reinterpret_cast<float*>(&smem[0][0][0]) + wave * kEpiFloats<NJ>, m0 + wm,
+                                 n0 + wn);
+        return;
+    }
     u32x4_t fa[8], fb[NJ];
     auto read_a = [&](int st, int h, int i) {
         fa[i] = *reinterpret_cast<const u32x4_t*>(&smem[st][0][0] + swz(wm + 16 * i + m16, 4 * h + q4));
@@ -354,11 +397,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 
     // acc[i][j] holds C^T of tile (i, j): lane (m16, q4) element e is
     // C[row 16i + m16][column 16j + 4q4 + e]
-    if constexpr (EPI) {
-        tile_epilogue<TC, 8, NJ>(a, acc, reinterpret_cast<float*>(&smem[0][0][0]) + wave * kEpiFloats<NJ>, m0 + wm,
-                                 n0 + wn);
-        return;
-    }
     TC* Cp = static_cast<TC*>(a.C);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
