@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             if (c < NJ) fb[h][c] = *reinterpret_cast<const u32x4_t*>(&smem[st][1][0] + swz(wn + 16 * c + m16, 4 * h + q4));
             else fa[h][c - NJ] = *reinterpret_cast<const u32x4_t*>(&smem[st][0][0] + swz(wm + 16 * (c - NJ) + m16, 4 * h + q4));
         };
-        constexpr int kRead = (8 + NJ + 5) / 6;           // reads beside each of the first six rows of products
+        constexpr int kRead = (8 + NJ + 7) / 8;           // reads beside each row of products (bunched 3 or 4: 1 to 2 per cent slower)
         constexpr int kCopy = (kACopy + kBCopy + 7) / 8;  // copies beside each row
         copy(0, 0);
         if (nk > 1) copy(1, 1);
@@ -790,16 +790,17 @@ hipError_t launch_ring(const GemmArgs& a, hipStream_t s)
 // the K-split tiles', plus what starts and ends it (the first loads' latency, the
 // epilogue) in the same unit (60,000 is about 2 us). Both numbers are fitted to the
 // times of every form at 365 sizes (1 to 8,192 rows, 36 to 41,024 columns, K 136 to
-// 8,192), where this choice is 0.9 per cent (geometric mean) above the best form. The
+// 8,192), where this choice is 0.9 per cent (geometric mean) above the best form, and
+// 1.8 at 365 others. The
 // tiles that are bound by taking their rows in cost about their rows; the 256 x 256
-// ones are bound by the matrix instructions instead, are the only ones that reach 1.3
-// PFLOP/s, and pay most at their ends (one wavefront a SIMD). Left out of the list, a
+// ones are bound by the matrix instructions instead, are the only ones past 1.1
+// PFLOP/s (1.35 at 8192 rows), and pay most at their ends (one wavefront a SIMD). Left out of the list, a
 // form costs over all sizes: 16 x 16 4 per cent, 32 x 32, 64 x 64, 128 x 128 and
 // 192 x 128 1 each, the others 0.2 to 0.7; 32 x 16, 32 x 64, 128 x 64 and 128 x 256 tiles
 // gave less than 0.1 and are not built. 4096 columns, K = 8192, us, this choice | the
 // next best of the list: 1 row 13.8 | 14.9, 64 rows 19.9 | 26.4, 96 rows 22.6 | 30.9, 192 rows
-// 31.9 | 34.6, 333 rows 39.3 | 58.2, 1024 rows 77.0 | 94.6, 2048 rows 139 | 157, 3000
-// rows 202 | 216, 4096 rows 227 | 261.
+// 31.9 | 34.6, 333 rows 39.3 | 58.2, 1024 rows 77.0 | 94.6, 2048 rows 129 | 150, 3000
+// rows 182 | 204, 4096 rows 208 | 261.
 template <typename TC>
 hipError_t launch_epilogue(const GemmArgs& a, hipStream_t s)
 {
@@ -819,7 +820,7 @@ hipError_t launch_epilogue(const GemmArgs& a, hipStream_t s)
         {128, 128, 1.1f, 100e3f, launch_tile<TC, 128, 128, 4, 2, 4>},
         {192, 128, 1.15f, 140e3f, launch_tile<TC, 192, 128, 4, 2, 3>},
         {256, 128, 1.15f, 240e3f, launch_tile<TC, 256, 128, 4, 2, 3>},
-        {256, 256, 1.4f, 660e3f, launch_256<TC>},
+        {256, 256, 1.3f, 600e3f, launch_256<TC>},
     };
     const Form* best = nullptr;
     double least = 0.0;
