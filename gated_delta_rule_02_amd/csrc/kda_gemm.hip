@@ -7,7 +7,8 @@
 // 16x16x32 bf16 MFMA consumes: each lane takes 8 consecutive K values of one
 // row of A and one row of B.
 //
-// Two kernels. The main one (K a multiple of 64): a 256 x 256 tile of C per
+// Two kernels of the plain product (the epilogue entry's forms stand below, with
+// the rule that picks them). The main one (K a multiple of 64): a 256 x 256 tile of C per
 // workgroup of 4 wavefronts, each owning 128 x 128 (8 x 8 MFMA tiles, 256
 // accumulator registers: one wavefront per SIMD), K steps of 64 in two LDS
 // stages filled by buffer-to-LDS copies of whole 128-byte operand rows (the

@@ -26,7 +26,6 @@ namespace kda {
 namespace {
 
 constexpr int D = 128;
-constexpr int kMaxNodes = 64;  // one lane of a wavefront per node
 
 // The parent of this lane's node: -1 (the state), a node, or -2 (absent, itself
 // or through a node above it). Every lane of the wavefront takes part.
