@@ -580,7 +580,7 @@ def kda_decode_tree_commit(k, g, writes, parents, accepted, state, lower_bound=-
 def _conv_tree_sizes(x, conv_state, parents):
     B, N = parents.shape
     b, w1, C = conv_state.shape
-    if not (conv_state.dtype is x.dtype and parents.dtype is torch.int32 and conv_state.is_contiguous() and
+    if not (b == B and conv_state.dtype is x.dtype and parents.dtype is torch.int32 and conv_state.is_contiguous() and
             parents.is_contiguous()):
         _tensor("conv_state", conv_state, (B, w1, C)), _tensor("parents", parents, (B, N))
         _type("conv_state", conv_state, x.dtype), _type("parents", parents, torch.int32)

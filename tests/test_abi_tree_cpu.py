@@ -128,3 +128,17 @@ def test_tree_binding_refuses():
         K.kda_conv_tree(torch.zeros(B * N, 256), hist, par, w[:, :3], y)
     with pytest.raises(ValueError, match="GPU"):
         K.kda_conv_tree_commit(torch.zeros(B * N, 256), par, acc, hist)
+
+
+@pytest.mark.parametrize("b", [1, 3])
+def test_conv_tree_binding_refuses_histories_of_another_batch(b):
+    """conv_state of fewer (or more) sequences than the trees, dense and of the
+    right type: the C entries take B from parents and would run past it."""
+    B, N, C = 2, 5, 256
+    x, y, w = torch.zeros(B * N, C), torch.zeros(B * N, C), torch.zeros(C, 4)
+    par, acc = torch.zeros(B, N, dtype=torch.int32), torch.zeros(B, dtype=torch.int32)
+    hist = torch.zeros(b, 3, C)
+    with pytest.raises(ValueError, match="conv_state must have shape"):
+        K.kda_conv_tree(x, hist, par, w, y)
+    with pytest.raises(ValueError, match="conv_state must have shape"):
+        K.kda_conv_tree_commit(x, par, acc, hist)
