@@ -30,6 +30,10 @@ def _dev_bf16(t):
 
 
 class KDAMixer:
+    """The mixer with bfloat16 weights. Outputs (and a DraftTree) are buffers of the
+    mixer, valid until the method's next call on the same stream, or, if the call
+    was captured, until the graph's next replay."""
+
     def __init__(self, W_in, conv_q, conv_k, conv_v, A_log, norm_w, Wo, H, scale=1.0,
                  lower_bound=-5.0, l2_eps=1e-6, rms_eps=1e-6):
         self.W_in, self.Wo = W_in, Wo
@@ -59,6 +63,15 @@ class KDAMixer:
         return 2 * (rows * self.W_in.shape[1] + self.Wo.shape[0] * self.Wo.shape[1]) + core * self.H // 64
 
     def _buf(self, name, shape, dtype):
+        """Scratch of this name, kept for the next call. Every stream has its own, so
+        that calls on two streams share none; a captured call's belongs to its graph
+        (the capture's memory pool): a later call of another size replaces a kept
+        buffer and would free what the replays use."""
+        stream = torch._C._cuda_getCurrentRawStream(self.W_in.get_device())
+        if stream:  # (nothing can be captured on the default stream, 0)
+            if torch.cuda.is_current_stream_capturing():
+                return torch.empty(shape, dtype=dtype, device="cuda")
+            name = (name, stream)
         b = self._bufs.get(name)
         if b is None or tuple(b.shape) != tuple(shape) or b.dtype != dtype:
             b = torch.empty(shape, dtype=dtype, device="cuda")
@@ -164,7 +177,7 @@ class KDAMixer:
         parents int32 [B, N] (as kda_decode_tree), state [B, H, 128, 128]
         (float32 or bfloat16) and conv_states bf16 [3, B, 3, H*128] only read.
         Returns out [B, N, hidden] float32 and the DraftTree that commits an
-        accepted path (both valid until the next call)."""
+        accepted path (both valid until the next call on this stream)."""
         B, N, hidden = x.shape
         _, cols = self.projections(x.reshape(B * N, hidden), tag="t")  # the commit reads them: not decode's buffer
         o, tree = self._core_tree(cols, parents, state, conv_states)
@@ -194,7 +207,7 @@ class KDAMixer:
 
 class DraftTree:
     """What a mixer's verification of a tree leaves for its commit (buffers of
-    the mixer: valid until its next verification)."""
+    the mixer: valid until its next verification on the same stream)."""
 
     def __init__(self, mixer, parents, inputs, k, g, writes):
         self.mixer, self.parents, self.inputs, self.k, self.g, self.writes = mixer, parents, inputs, k, g, writes
@@ -217,8 +230,8 @@ class KDABlock:
     and the next block adds it while it normalises: one pass then updates the
     stream, norms it and quantizes the projections' input. So every method takes
     the delta still to be added (None: nothing) and returns the one it leaves
-    (None: added; else a buffer of the mixer, valid until that method's next call);
-    `finish` adds a last one."""
+    (None: added; else a buffer of the mixer, valid until that method's next call on
+    the same stream); `finish` adds a last one."""
 
     def __init__(self, mixer, norm_weight, eps=1e-6):
         self.mixer, self.norm_weight, self.eps = mixer, norm_weight, eps
@@ -260,15 +273,14 @@ class DecodeGraph:
     projection) are replayed without a host launch each, which at a few
     sequences is a large part of the step. The graph reads x from, and writes
     out to, its own buffers and updates the given state and conv states in
-    place, so each replay advances those sequences by one token. Every call
-    it makes allocates nothing and enqueues no memset (the library never
-    does), and the mixer's buffers are allocated by an eager step before the
-    capture."""
+    place, so each replay advances those sequences by one token. The calls
+    enqueue no memset (the library never does), and the step's buffers are the
+    graph's own, so other calls of the mixer may run between replays."""
 
     def __init__(self, mixer, B, state, conv_states):
         self.x = torch.zeros((B, mixer.hidden), dtype=torch.bfloat16, device="cuda")
         self.state, self.conv_states = state, conv_states
-        # an eager step on copies allocates every buffer the step uses
+        # an eager step on copies: every kernel is loaded before the capture
         mixer.decode(self.x, state.clone(), conv_states.clone())
         torch.cuda.synchronize()
         self.graph = torch.cuda.CUDAGraph()
