@@ -139,9 +139,16 @@ def _cu(cu_seqlens, cu_seqlens_host):
 _workspaces = {}
 
 
-def _workspace(device, nbytes):
-    """A cached device buffer of at least nbytes (one per device; grows on demand)."""
-    key = torch.device(device).index
+def _workspace(device, nbytes, stream=None):
+    """A device buffer of at least nbytes for a call on this stream (None: the
+    current one): one kept per device and stream (grows on demand); in a captured
+    call the graph's own (a kept one would be freed under its replays when it grows)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):  # the allocator reuses a buffer in this stream's order
+            return _workspace(device, nbytes)
+    key = (torch.device(device).index, torch.cuda.current_stream().cuda_stream)
+    if key[1] and torch.cuda.is_current_stream_capturing():  # (nothing is captured on the default stream, 0)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -155,10 +162,10 @@ def kda_prefill(q, k, v, g, beta, o, cu_seqlens=None, cu_seqlens_host=None, num_
     """KDA core over packed sequences. q,k,g [T,H,128], v [T,H,128], beta [T,H]
     (one dtype), o [T,H,128] (float32 or bfloat16), states float32 [N,H,128,128].
 
-    workspace: "auto" (a cached buffer of kda_prefill_workspace_bytes bytes, so
-    bfloat16 inputs take the two-pass form), None (no workspace: single-pass
-    form), or a caller-owned uint8 device tensor. Calls sharing the cached
-    buffer must be ordered on one stream.
+    workspace: "auto" (a buffer of at least kda_prefill_workspace_bytes bytes, kept
+    per stream, so bfloat16 inputs take the two-pass form), None (no workspace:
+    single-pass form), or a caller-owned uint8 device tensor (calls that share it
+    must be ordered on one stream).
 
     snapshots: float32 [N, slots, H, 128, 128] with snapshot_interval (a
     multiple of 64): calls kda_prefill_snapshots, which also stores the state
@@ -175,7 +182,7 @@ def kda_prefill(q, k, v, g, beta, o, cu_seqlens=None, cu_seqlens_host=None, num_
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a tensor")
         need = lib().kda_prefill_workspace_bytes(T, num_seqs, H, dk, dv, _dt(q))
-        workspace = _workspace(q.device, need) if need else None
+        workspace = _workspace(q.device, need, stream) if need else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if snapshots is None:
         _call("kda_prefill", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), T, H, dk, dv,
@@ -212,7 +219,7 @@ def kda_prefill_gated(q, k, v, f, b, A_log, o, cu_seqlens=None, cu_seqlens_host=
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
         need = lib().kda_prefill_workspace_bytes(T, num_seqs, H, dk, dv, _dt(q))
-        workspace = _workspace(q.device, need) if need else None
+        workspace = _workspace(q.device, need, stream) if need else None
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _call("kda_prefill_gated", _ptr(q), _ptr(k), _ptr(v), _ptr(f), f.stride(0), _ptr(b), b.stride(0),
           _ptr(A_log), _dt(q), T, H, dk, dv, cu_dev, cu_host, num_seqs, scale, lower_bound,
@@ -261,7 +268,8 @@ def kda_prefill_segment_maps(k, v, g, beta, M_out, N_out, cu_seqlens=None, cu_se
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
-        workspace = _workspace(k.device, max(lib().kda_prefill_workspace_bytes(max(T, 1), num_seqs, H, dk, dv, _dt(k)), 16))
+        need = lib().kda_prefill_workspace_bytes(max(T, 1), num_seqs, H, dk, dv, _dt(k))
+        workspace = _workspace(k.device, max(need, 16), stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     _call("kda_prefill_segment_maps", _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(k), T, H, dk, dv,
           cu_dev, cu_host, num_seqs, lower_bound, _ptr(M_out), _ptr(N_out), _ptr(workspace), ws_bytes,

@@ -1,10 +1,12 @@
 """The block's and the mixer's scratch: a captured call keeps its own whatever
 sizes are called between its replays, and calls on two streams share none."""
+import numpy as np
 import pytest
 import torch
 
+from gated_delta_rule_02_amd import kda as K
 from gated_delta_rule_02_amd import layer, synth
-from tests.gpu_util import announce
+from tests.gpu_util import announce, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -152,3 +154,74 @@ def test_two_streams_share_no_scratch(fp8):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
     first, second = both[0][1][-1], both[1][1][-1]
     assert first.writes.data_ptr() != second.writes.data_ptr() and first.k.data_ptr() != second.k.data_ptr()
+
+
+def prefill_case(block, T, seed):
+    hidden = torch.randn((T, 256), generator=torch.Generator().manual_seed(seed)).cuda()
+    return hidden, torch.zeros((1, H, 128, 128), device="cuda"), torch.zeros((3, 1, 3, W), device="cuda").bfloat16()
+
+
+def test_captured_prefill_keeps_its_workspace():
+    """A captured prefill of the block; between the replays a longer one grows the
+    binding's workspace. Every replay equals the eager call bit for bit."""
+    announce("captured prefill")
+    block = build(False)
+    hidden, state, conv = prefill_case(block, 200, 1)
+    h, s1, c1 = hidden.clone(), state.clone(), conv.clone()
+    block.forward(h, final_state=s1, conv_state_out=c1)
+    torch.cuda.synchronize()
+    kept = dict(K._workspaces)
+    buf = hidden.clone()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            block.forward(buf, final_state=state, conv_state_out=conv)
+    torch.cuda.synchronize()
+    assert K._workspaces.keys() == kept.keys() and all(K._workspaces[n] is kept[n] for n in kept)
+    for r in range(4):
+        block.forward(torch.ones((1000 + 700 * r, 256), device="cuda"))
+        junk = other_calls(block)
+        buf.copy_(hidden)
+        state.zero_(), conv.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf, h) and torch.equal(state, s1) and torch.equal(conv, c1), r
+        del junk
+
+
+@pytest.mark.parametrize("how", ["current", "argument"])
+def test_prefills_on_two_streams_share_no_workspace(how):
+    """The same prefill on two streams at once, by the current stream or by the
+    stream argument: the results are those of the call alone."""
+    announce("prefill on two streams: " + how)
+    T, Hc = 700, 4
+    cases = []
+    for seed in (5, 6):
+        d = synth.core_inputs(np.random.default_rng(seed), T, Hc, bf16=True)
+        cases.append([dev(d[n]) for n in ("q", "k", "v", "g", "beta")])
+    def out():
+        return torch.zeros((T, Hc, 128), device="cuda"), torch.zeros((1, Hc, 128, 128), device="cuda")
+    alone = []
+    for c in cases:
+        o, st = out()
+        K.kda_prefill(*c, o, final_state=st)
+        torch.cuda.synchronize()
+        alone.append((o, st))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[out() for _ in range(5)] for _ in cases]
+    torch.cuda.synchronize()
+    for r in range(5):
+        for c, s, g in zip(cases, streams, got):
+            if how == "argument":
+                K.kda_prefill(*c, g[r][0], final_state=g[r][1], stream=s)
+            else:
+                with torch.cuda.stream(s):
+                    K.kda_prefill(*c, g[r][0], final_state=g[r][1])
+    torch.cuda.synchronize()
+    for a, g in zip(alone, got):
+        for o, st in g:
+            assert torch.equal(o, a[0]) and torch.equal(st, a[1])
+    index = torch.cuda.current_device()
+    bufs = [K._workspaces[index, x.cuda_stream] for x in streams]
+    assert bufs[0].data_ptr() != bufs[1].data_ptr()
