@@ -112,6 +112,17 @@ __device__ __forceinline__ void lds_barrier()
     asm volatile("" ::: "memory");
 }
 
+// Between an LDS store by one lane and a load of it by another lane of the same
+// wavefront (or a load and a store over it). A wavefront's LDS accesses execute in
+// order, so this waits for nothing and emits no instruction: it keeps the compiler from
+// reordering the two, which it may where it proves one lane's addresses distinct.
+__device__ __forceinline__ void wave_lds_order()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 // The activations use the hardware exp2, log2 and reciprocal (about one ulp
 // each): the memory-bound kernels that apply them per element would otherwise

@@ -111,8 +111,10 @@ __device__ __forceinline__ void tile_epilogue(const GemmArgs& a, const f32x4 (&a
     if (a.res) load_res(0, res[0]);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
+        wave_lds_order();  // the 16 rows before are read
 #pragma unroll
         for (int j = 0; j < NJ; ++j) *reinterpret_cast<f32x4*>(lds + m16 * kLd + 16 * j + 4 * q4) = acc[i][j];
+        wave_lds_order();
         if (a.res && i + 1 < NI) load_res(i + 1, res[(i + 1) & 1]);
         if (a.act) {
 #pragma unroll 1

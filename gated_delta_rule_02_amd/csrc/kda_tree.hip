@@ -526,6 +526,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
                 for (int c = 0; c < CT; ++c) v[c] = acc[I][c][e];
                 *reinterpret_cast<cols*>(row(16 * I + 4 * q4 + e, c2)) = v;
             }
+        wave_lds_order();  // (the wavefront's own columns: its other lanes' rows)
         // within the block
         constexpr int BN_ = NP < 16 ? NP : 16, i0 = 16 * I;
         float r[BN_], beta_[BN_];
@@ -554,6 +555,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
             });
             __builtin_amdgcn_sched_barrier(0);  // keep the reads ahead, and no further
         });
+        wave_lds_order();  // u of the block, for the blocks after, the writes and o
         __builtin_amdgcn_sched_barrier(0);
     });
     const bool any_bad = __any(bad != 0);
@@ -608,7 +610,9 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
         }
     if (any_bad) {
         // rare: NaN for every write that is not finite and for what lies below it
-        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): over the stores above
+        asm volatile("" ::: "memory");  // over the stores above, which other lanes made:
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        asm volatile("" ::: "memory");
         for (int i = 0; i < N; ++i) {
             uint64_t above = 0;
             for (int j = __builtin_amdgcn_readlane(parent, i); j >= 0; j = __builtin_amdgcn_readlane(parent, j))
