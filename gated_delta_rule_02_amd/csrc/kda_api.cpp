@@ -452,6 +452,15 @@ static int check_tree(const char* fn, const int32_t* parents, int B, int num_nod
     return KDA_OK;
 }
 
+// The tree kernels give every (sequence, head) a workgroup of this many threads.
+static int check_tree_launch(const char* fn, int B, int H, int threads)
+{
+    const int64_t most = ((int64_t)1 << 32) / threads;  // a launch holds less than 2^32 threads
+    REQUIRE((int64_t)B * H < most, KDA_ERR_UNSUPPORTED, "%s: B*H must be below %lld here (got %lld)", fn, (long long)most,
+            (long long)B * H);
+    return KDA_OK;
+}
+
 int kda_decode_tree(const void* q, const void* k, const void* v, const void* g, const void* beta, kda_dtype in_dtype,
                     const int32_t* parents, int B, int num_nodes, int H, int dk, int dv, float scale,
                     float lower_bound, const void* state, kda_dtype state_dtype, void* o, kda_dtype out_dtype,
@@ -463,6 +472,7 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* g, 
             "%s: bad dtype", fn);
     REQUIRE(dk == 128 && dv == 128, KDA_ERR_UNSUPPORTED, "%s: only dk = dv = 128 is supported (got %d, %d)", fn, dk, dv);
     if (int rc = check_tree(fn, parents, B, num_nodes, H); rc != KDA_OK) return rc;
+    if (int rc = check_tree_launch(fn, B, H, tree_threads(num_nodes)); rc != KDA_OK) return rc;
     if (int rc = check_lower_bound(fn, lower_bound, false); rc != KDA_OK) return rc;
     for (const void* p : {q, k, v, g, beta, state, (const void*)o, (const void*)writes})
         REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
@@ -490,6 +500,7 @@ int kda_decode_tree_commit(const void* k, const void* g, kda_dtype in_dtype, con
     REQUIRE(valid_dtype(in_dtype) && valid_dtype(state_dtype), KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
     REQUIRE(dk == 128 && dv == 128, KDA_ERR_UNSUPPORTED, "%s: only dk = dv = 128 is supported (got %d, %d)", fn, dk, dv);
     if (int rc = check_tree(fn, parents, B, num_nodes, H); rc != KDA_OK) return rc;
+    if (int rc = check_tree_launch(fn, B, H, tree_commit_threads((DType)state_dtype)); rc != KDA_OK) return rc;
     if (int rc = check_lower_bound(fn, lower_bound, false); rc != KDA_OK) return rc;
     for (const void* p : {k, g, (const void*)writes, (const void*)state})
         REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);

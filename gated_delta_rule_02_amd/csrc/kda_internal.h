@@ -180,6 +180,9 @@ struct TreeArgs {
     float scale, lower_bound;
     DType in_dtype, out_dtype, state_dtype;
 };
+// threads of the workgroup that each (sequence, head) gets
+constexpr int tree_threads(int num_nodes) { return num_nodes <= 32 ? 256 : 512; }
+constexpr int tree_commit_threads(DType state_dtype) { return state_dtype == F32 ? 1024 : 256; }
 hipError_t launch_decode_tree(const TreeArgs& a, hipStream_t s);
 hipError_t launch_tree_commit(const TreeArgs& a, hipStream_t s);
 

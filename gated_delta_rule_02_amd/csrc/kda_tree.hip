@@ -239,7 +239,7 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 // workgroups and 4 wavefronts each left a SIMD with too few to cover the latencies of the
 // walk and the substitution (32 trees of 64 nodes 320 | 275 us with 4 | 8; 64 of 32 nodes
 // 178 | 189, so 4 there).
-template <int NP> constexpr int kTreeWaves = NP > 32 ? 8 : 4;
+template <int NP> constexpr int kTreeWaves = tree_threads(NP) / 64;
 template <int NP> constexpr int kTreePerSimd = NP <= 16 || NP == 48 ? 4 : (NP == 32 ? 3 : 2);  // wavefronts per SIMD (by LDS and registers)
 
 // f(0), ..., f(N - 1) with compile-time arguments: indexes of register arrays are
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(64 * kTreeWaves<NP>, kTreePerSimd<NP>) void decode_
 // nodes at a time, from the accepted node up.
 template <typename TS> struct CommitMap {
     static constexpr int kCols = 16 / (int)sizeof(TS);
-    static constexpr int kThreads = sizeof(TS) == 4 ? 1024 : 256;
+    static constexpr int kThreads = tree_commit_threads(sizeof(TS) == 4 ? F32 : BF16);
     static constexpr int kLanesPerRow = D / kCols;
     static constexpr int kRowGroups = kThreads / kLanesPerRow;
     static constexpr int kRows = D / kRowGroups;

@@ -346,7 +346,8 @@ int kda_decode_commit(const void* token_states, const int32_t* accepted, int B, 
  * writes  float32 [B, num_nodes, H, dv] or NULL (verification only).
  * Everything is computed in float32 (o rounded once, when stored). lower_bound as
  * for kda_decode_step. Neither output may overlap another tensor.
- * Supported: dk = dv = 128, B, H >= 1, 1 <= num_nodes <= 64.
+ * Supported: dk = dv = 128, B, H >= 1, 1 <= num_nodes <= 64; B*H < 2^24, and
+ * < 2^23 for more than 32 nodes (else KDA_ERR_UNSUPPORTED: one launch).
  * ---------------------------------------------------------------------- */
 int kda_decode_tree(const void* q, const void* k, const void* v, const void* g, const void* beta, kda_dtype in_dtype,
                     const int32_t* parents, int B, int num_nodes, int H, int dk, int dv, float scale,
@@ -364,6 +365,7 @@ int kda_decode_tree(const void* q, const void* k, const void* v, const void* g, 
  *           node, leaves state[b] as it is.
  * state     [B, H, dk, dv] in state_dtype, updated in place (float32 arithmetic,
  *           bfloat16 rounded to nearest even when stored).
+ * B*H < 2^22 for float32 states, < 2^24 for bfloat16 (else KDA_ERR_UNSUPPORTED).
  * The rest as kda_decode_tree.
  * ---------------------------------------------------------------------- */
 int kda_decode_tree_commit(const void* k, const void* g, kda_dtype in_dtype, const float* writes,

@@ -130,6 +130,25 @@ def test_tree_binding_refuses():
         K.kda_conv_tree_commit(torch.zeros(B * N, 256), par, acc, hist)
 
 
+def far(i):
+    """Addresses that do not overlap whatever these sizes take."""
+    return i << 50
+
+
+def test_tree_counts_beyond_a_launch():
+    """A launch holds less than 2^32 threads: a workgroup of 256 (512 above 32
+    nodes; 1,024 for the commit of a float32 state) for every sequence and head."""
+    a = dict(q=far(1), k=far(2), v=far(3), g=far(4), beta=far(5), par=far(6), s=far(7), o=far(8), w=far(9), H=64)
+    for N, most in ((1, 1 << 24), (32, 1 << 24), (33, 1 << 23), (64, 1 << 23)):
+        assert tree(B=most // 64, N=N, **a) == UNSUPPORTED, N
+        # one sequence fewer passes this check (the next, of the alignment of o, refuses it)
+        assert tree(B=most // 64 - 1, N=N, **dict(a, o=far(8) + 8)) == INVALID, N
+    a = dict(k=far(2), g=far(4), w=far(9), par=far(6), acc=far(10), s=far(7), H=64)
+    for sd, most in ((K.KDA_F32, 1 << 22), (K.KDA_BF16, 1 << 24)):
+        assert commit(B=most // 64, N=1, sd=sd, **a) == UNSUPPORTED, sd
+        assert commit(B=most // 64 - 1, N=1, sd=sd, **dict(a, s=far(7) + 8)) == INVALID, sd
+
+
 @pytest.mark.parametrize("b", [1, 3])
 def test_conv_tree_binding_refuses_histories_of_another_batch(b):
     """conv_state of fewer (or more) sequences than the trees, dense and of the
