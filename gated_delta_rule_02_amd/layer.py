@@ -179,6 +179,8 @@ class KDAMixer:
         Returns out [B, N, hidden] float32 and the DraftTree that commits an
         accepted path (both valid until the next call on this stream)."""
         B, N, hidden = x.shape
+        if parents.shape != (B, N):
+            raise ValueError("parents must be [%d, %d] as x (got %s)" % (B, N, tuple(parents.shape)))
         _, cols = self.projections(x.reshape(B * N, hidden), tag="t")  # the commit reads them: not decode's buffer
         o, tree = self._core_tree(cols, parents, state, conv_states)
         out, _ = self.output(o.view(B * N, self.H, D), cols[4], tag="t")
