@@ -217,6 +217,8 @@ class DraftTree:
     def commit(self, accepted, state, conv_states):
         """state and conv_states (those that were verified against) advance in place
         along the path to node accepted[b] (int32 [B]; any other value: unchanged)."""
+        if len(conv_states) != len(self.inputs):
+            raise ValueError("conv_states must hold the q, k and v histories (got %d)" % len(conv_states))
         K.kda_decode_tree_commit(self.k, self.g, self.writes, self.parents, accepted, state,
                                  lower_bound=self.mixer.lower_bound)
         for x, cs in zip(self.inputs, conv_states):

@@ -21,3 +21,36 @@ def test_mixer_tree_of_another_shape_is_refused():
     for shape in ((3, 4), (6, 2), (2, 5), (12,)):
         with pytest.raises(ValueError, match="parents must be"):
             mixer().decode_tree(x, torch.zeros(shape, dtype=torch.int32), None, None)
+
+
+def recorded(monkeypatch):
+    """The library's calls as a list of names (nothing is computed), and the
+    mixer's buffers on the CPU."""
+    calls = []
+    for name in ("kda_gemm", "kda_gemm_epilogue", "kda_add_rmsnorm", "kda_conv_tree", "kda_gate_prologue", "kda_decode_tree",
+                 "kda_output_norm_gate", "kda_decode_tree_commit", "kda_conv_tree_commit"):
+        def call(*a, _name=name, **kw):
+            calls.append(_name)
+            return a[4] if _name == "kda_conv_tree" else None
+        monkeypatch.setattr(K, name, call)
+
+    def buf(self, name, shape, dtype):
+        key = (name, tuple(shape), dtype)
+        if key not in self._bufs:
+            self._bufs[key] = torch.empty(shape, dtype=dtype)
+        return self._bufs[key]
+    monkeypatch.setattr(layer.KDAMixer, "_buf", buf)
+    return calls
+
+
+def test_commit_takes_three_histories(monkeypatch):
+    """Fewer histories than streams would leave the others where they were."""
+    calls = recorded(monkeypatch)
+    m = mixer()
+    tree = m.decode_tree(torch.zeros((2, 6, 256), dtype=torch.bfloat16), torch.zeros((2, 6), dtype=torch.int32), None,
+                         [None] * 3)[1]
+    calls.clear()
+    for n in (0, 2, 4):
+        with pytest.raises(ValueError, match="conv_states"):
+            tree.commit(None, None, [None] * n)
+    assert not calls
