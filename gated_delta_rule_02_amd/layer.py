@@ -201,22 +201,29 @@ class KDAMixer:
         K.kda_gate_prologue(fp, bp, self.A_log, g, beta, H, D, lower_bound=self.lower_bound)
         o = self._buf("to", (B, N, H, D), torch.float32)
         writes = self._buf("tw", (B, N, H, D), torch.float32)
-        g = g.view(B, N, H, D)
-        K.kda_decode_tree(qkv[0], qkv[1], qkv[2], g, beta.view(B, N, H), parents, state, o, writes, scale=self.scale,
+        tree = DraftTree(self, parents, (qp, kp, vp), qkv[1], g.view(B, N, H, D), writes, g)
+        K.kda_decode_tree(qkv[0], qkv[1], qkv[2], tree.g, beta.view(B, N, H), parents, state, o, writes, scale=self.scale,
                           lower_bound=self.lower_bound)
-        return o, DraftTree(self, parents, (qp, kp, vp), qkv[1], g, writes)
+        return o, tree
 
 
 class DraftTree:
     """What a mixer's verification of a tree leaves for its commit (buffers of
-    the mixer: valid until its next verification on the same stream)."""
+    the mixer: valid until its next verification on the same stream; once another
+    has overwritten them it refuses to commit)."""
 
-    def __init__(self, mixer, parents, inputs, k, g, writes):
+    def __init__(self, mixer, parents, inputs, k, g, writes, buffer):
         self.mixer, self.parents, self.inputs, self.k, self.g, self.writes = mixer, parents, inputs, k, g, writes
+        # `buffer`, a buffer of the verification that every next one with as many
+        # rows overwrites, names the tree that it holds
+        self.buffer, self.token = buffer, object()
+        buffer.tree = self.token
 
     def commit(self, accepted, state, conv_states):
         """state and conv_states (those that were verified against) advance in place
         along the path to node accepted[b] (int32 [B]; any other value: unchanged)."""
+        if self.buffer.tree is not self.token:
+            raise RuntimeError("the mixer has verified another tree since: this one's buffers are overwritten")
         if len(conv_states) != len(self.inputs):
             raise ValueError("conv_states must hold the q, k and v histories (got %d)" % len(conv_states))
         K.kda_decode_tree_commit(self.k, self.g, self.writes, self.parents, accepted, state,

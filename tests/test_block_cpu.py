@@ -43,6 +43,35 @@ def recorded(monkeypatch):
     return calls
 
 
+@pytest.mark.parametrize("entry", ["block", "mixer"])
+def test_overwritten_tree_refuses_to_commit(monkeypatch, entry):
+    """After another verification of as many rows (also in trees of another
+    shape) a tree's buffers hold that one's; committing it would write the wrong
+    path into the states. Its last tree commits, and one of other rows as well."""
+    calls = recorded(monkeypatch)
+    m = mixer()
+    block = layer.KDABlock(m, torch.ones(256))
+
+    def verify(B, N):
+        par = torch.zeros((B, N), dtype=torch.int32)
+        if entry == "block":
+            return block.decode_tree(torch.zeros((B * N, 256)), par, None, [None] * 3)[1]
+        return m.decode_tree(torch.zeros((B, N, 256), dtype=torch.bfloat16), par, None, [None] * 3)[1]
+
+    for again in ((2, 6), (3, 4)):
+        first = verify(2, 6)
+        second = verify(*again)
+        calls.clear()
+        with pytest.raises(RuntimeError, match="overwritten"):
+            first.commit(None, None, [None] * 3)
+        assert not calls
+        second.commit(None, None, [None] * 3)
+        assert calls == ["kda_decode_tree_commit"] + ["kda_conv_tree_commit"] * 3
+    first = verify(2, 6)
+    verify(1, 6)  # buffers of its own
+    first.commit(None, None, [None] * 3)
+
+
 def test_commit_takes_three_histories(monkeypatch):
     """Fewer histories than streams would leave the others where they were."""
     calls = recorded(monkeypatch)
