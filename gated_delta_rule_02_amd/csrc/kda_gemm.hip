@@ -797,7 +797,7 @@ hipError_t launch_ring(const GemmArgs& a, hipStream_t s)
 // 1.8 at 365 others. The
 // tiles that are bound by taking their rows in cost about their rows; the 256 x 256
 // ones are bound by the matrix instructions instead, are the only ones past 1.1
-// PFLOP/s (1.35 at 8192 rows), and pay most at their ends (one wavefront a SIMD). Left out of the list, a
+// PFLOP/s (1.3 at 8192 rows), and pay most at their ends (one wavefront a SIMD). Left out of the list, a
 // form costs over all sizes: 16 x 16 4 per cent, 32 x 32, 64 x 64, 128 x 128 and
 // 192 x 128 1 each, the others 0.2 to 0.7; 32 x 16, 32 x 64, 128 x 64 and 128 x 256 tiles
 // gave less than 0.1 and are not built. 4096 columns, K = 8192, us, this choice | the

@@ -138,7 +138,8 @@ __global__ __launch_bounds__(256) void add_norm_kernel(AddNormArgs a)
 }
 
 // Rows too wide for the registers: the row is read again (from the caches) for
-// the second half.
+// the second half. 2048 rows of 16,384 (bfloat16) 73 us, with E4M3 output 70 us (one
+// read of everything at a copy's rate: 53 and 47).
 template <typename TX, typename TR, typename TY, bool RES>
 __global__ __launch_bounds__(256) void add_norm_wide_kernel(AddNormArgs a)
 {

@@ -227,13 +227,14 @@ __global__ __launch_bounds__(256) void conv_commit_kernel(ConvTreeArgs a)
 //          independent operations); then o += P u by the matrix instruction on
 //          the accumulators that hold (D q) S0.
 // What bounds it (float32 states, 64 heads): up to 16 nodes HBM, 128 trees of 16
-// nodes 158-170 us = 4.7-5.1 TB/s (a copy reaches 5.1), 64 of 8 nodes 56 us = 6.0 TB/s;
+// nodes 151 us = 5.3 TB/s (a copy reaches 5.1), 64 of 8 nodes 54 us = 6.1 TB/s;
 // above, the walk (with it skipped, 64 trees of 32 nodes took 115 of 188 us, 32 of 64
-// nodes 166 of 320, before the forms below) and the products. Now 64 of 32 nodes 157 us, 64 of
-// 40 264 us, 32 of 64 263 us. Tried and slower up to 32 nodes: all pairs at once as a
-// matrix product of rows scaled by exp(G + C) and exp(-G - C), C a center per
-// channel (128 of 16 nodes 157 | 180 us; the loads before the state's get more and
-// smaller).
+// nodes 166 of 320, before the forms below) and the products. Now 64 of 32 nodes 148 us, 64 of
+// 40 258 us, 32 of 64 263 us. bfloat16 states take about the same: 128 of 16 nodes 145 us,
+// 64 of 32 145 us, 64 of 40 258 us, 32 of 64 261 us. Tried and slower up to 32 nodes:
+// all pairs at once as a matrix product of rows scaled by exp(G + C) and exp(-G - C),
+// C a center per channel (128 of 16 nodes 157 | 180 us; the loads before the state's
+// get more and smaller).
 // NP: N rounded up to 8, 16, 32, 48 or 64.
 // NW wavefronts: 4, and 8 for NP > 32, where a compute unit holds one or two
 // workgroups and 4 wavefronts each left a SIMD with too few to cover the latencies of the

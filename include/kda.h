@@ -344,7 +344,9 @@ int kda_decode_commit(const void* token_states, const int32_t* accepted, int B, 
  * state   [B, H, dk, dv] in state_dtype, read only.
  * o       [B, num_nodes, H, dv] out_dtype.
  * writes  float32 [B, num_nodes, H, dv] or NULL (verification only).
- * Everything is computed in float32 (o rounded once, when stored). lower_bound as
+ * Everything is computed in float32 (o rounded once, when stored). A write that
+ * overflows or is NaN becomes NaN, as do o and writes of its node and of the nodes
+ * below it, in its value channel; no other value depends on it. lower_bound as
  * for kda_decode_step. Neither output may overlap another tensor.
  * Supported: dk = dv = 128, B, H >= 1, 1 <= num_nodes <= 64; B*H < 2^24, and
  * < 2^23 for more than 32 nodes (else KDA_ERR_UNSUPPORTED: one launch).
