@@ -117,6 +117,15 @@ def _dense(t, name):
     return t
 
 
+def _holds(name, t, dtype, n):
+    """t (None: not given) is of this dtype and holds what the call reads or writes."""
+    if t is not None:
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
+        if t.numel() < n:
+            raise ValueError("%s holds %d elements, the call takes %d" % (name, t.numel(), n))
+
+
 def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -296,6 +305,7 @@ def kda_decode_step(q, k, v, g, beta, state, o, scale=1.0, lower_bound=-5.0, str
         _dense(t_, n_)
     B, H, dk = q.shape
     dv = v.shape[2]
+    _holds("state", state, torch.float32, B * H * dk * dv)
     _call("kda_decode_step", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), B, H, dk, dv,
           scale, lower_bound, _ptr(state), _ptr(o), _dt(o), _stream(stream))
     return o
@@ -354,6 +364,7 @@ def kda_conv_state_update(x, conv_state, weight, y, bias=None, apply_silu=True, 
         raise ValueError("x rows must be contiguous")
     B = x.shape[0]
     C, W = weight.shape
+    _holds("conv_state", conv_state, x.dtype, B * (W - 1) * C)
     _call("kda_conv_state_update", _ptr(x), x.stride(0), _ptr(conv_state), _ptr(weight), _ptr(bias), _dt(x), B, C, W,
           int(bool(apply_silu)), l2norm_group, l2norm_eps, _ptr(y), _stream(stream))
     return y

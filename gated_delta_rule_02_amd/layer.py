@@ -260,13 +260,15 @@ class KDABlock:
         return self.mixer.output_into(o, cols[4], hidden, tag="b")
 
     def decode(self, hidden, state, conv_states, delta=None):
-        """One token per sequence: hidden [B, width], states updated in place."""
+        """One token per sequence: hidden [B, width], states (as KDAMixer.decode's,
+        float32) updated in place."""
         cols = self._enter(hidden, delta)
         o = self.mixer._core_decode(cols, state, conv_states)
         return self.mixer.output_into(o, cols[4], hidden, tag="bd")
 
     def decode_tree(self, hidden, parents, state, conv_states, delta=None):
-        """A tree of drafts per sequence: hidden [B * N, width]. Returns (delta, DraftTree)."""
+        """A tree of drafts per sequence: hidden [B * N, width], states as
+        KDAMixer.decode_tree's. Returns (delta, DraftTree)."""
         cols = self._enter(hidden, delta, tag="t")  # the commit reads them: not decode's buffer
         o, tree = self.mixer._core_tree(cols, parents, state, conv_states)
         return self.mixer.output_into(o.view(hidden.shape[0], self.mixer.H, D), cols[4], hidden, tag="bt"), tree
