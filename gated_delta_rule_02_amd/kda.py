@@ -187,6 +187,8 @@ def kda_prefill(q, k, v, g, beta, o, cu_seqlens=None, cu_seqlens_host=None, num_
     cu_dev, cu_host, keep = _cu(cu_seqlens, cu_seqlens_host)
     if num_seqs is None:
         num_seqs = (keep.numel() - 1) if keep is not None else 1
+    _holds("initial_state", initial_state, torch.float32, num_seqs * H * dk * dv)
+    _holds("final_state", final_state, torch.float32, num_seqs * H * dk * dv)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a tensor")
@@ -224,6 +226,8 @@ def kda_prefill_gated(q, k, v, f, b, A_log, o, cu_seqlens=None, cu_seqlens_host=
     cu_dev, cu_host, keep = _cu(cu_seqlens, cu_seqlens_host)
     if num_seqs is None:
         num_seqs = (keep.numel() - 1) if keep is not None else 1
+    _holds("initial_state", initial_state, torch.float32, num_seqs * H * dk * dv)
+    _holds("final_state", final_state, torch.float32, num_seqs * H * dk * dv)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
@@ -248,6 +252,8 @@ def kda_prefill_noalloc(q, k, v, g, beta, o, cu_seqlens=None, cu_seqlens_host=No
     cu_dev, cu_host, keep = _cu(cu_seqlens, cu_seqlens_host)
     if num_seqs is None:
         num_seqs = (keep.numel() - 1) if keep is not None else 1
+    _holds("initial_state", initial_state, torch.float32, num_seqs * H * dk * dv)
+    _holds("final_state", final_state, torch.float32, num_seqs * H * dk * dv)
     _call("kda_prefill_noalloc", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), T, H, dk, dv,
           cu_dev, cu_host, num_seqs, scale, lower_bound, _ptr(initial_state), _ptr(final_state),
           _ptr(o), _dt(o), _stream(stream))
@@ -384,6 +390,8 @@ def kda_conv_prefill(x, weight, y, cu_seqlens=None, cu_seqlens_host=None, num_se
     cu_dev, cu_host, keep = _cu(cu_seqlens, cu_seqlens_host)
     if num_seqs is None:
         num_seqs = (keep.numel() - 1) if keep is not None else 1
+    _holds("conv_state_in", conv_state_in, x.dtype, num_seqs * (W - 1) * C)
+    _holds("conv_state_out", conv_state_out, x.dtype, num_seqs * (W - 1) * C)
     _call("kda_conv_prefill", _ptr(x), x.stride(0), T, C, W, cu_dev, cu_host, num_seqs, _ptr(weight),
           _ptr(bias), _ptr(conv_state_in), _ptr(conv_state_out), int(bool(apply_silu)), l2norm_group,
           l2norm_eps, _ptr(y), y.stride(0), _dt(x), _stream(stream))

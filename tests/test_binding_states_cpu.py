@@ -32,3 +32,36 @@ def test_conv_state_update_state(state, error):
         K.kda_conv_state_update(x, state, w, y)
     with pytest.raises(ValueError, match="GPU"):
         K.kda_conv_state_update(x, torch.zeros(B, W - 1, C), w, y)
+
+
+def prefill(fn, **states):
+    T, Hp = 5, 2
+    q, beta, o = torch.zeros(T, Hp, 128), torch.zeros(T, Hp), torch.zeros(T, Hp, 128)
+    if fn is K.kda_prefill_gated:
+        return fn(q, q, q, torch.zeros(T, Hp * 128), beta, torch.zeros(Hp), o, workspace=torch.zeros(16), **states)
+    return fn(q, q, q, q, beta, o, **states)
+
+
+@pytest.mark.parametrize("fn", [K.kda_prefill, K.kda_prefill_gated, K.kda_prefill_noalloc])
+@pytest.mark.parametrize("name", ["initial_state", "final_state"])
+def test_prefill_states(fn, name):
+    with pytest.raises(ValueError, match=name):
+        prefill(fn, **{name: torch.zeros(1, 1, 128, 128)})
+    with pytest.raises(TypeError, match=name):
+        prefill(fn, **{name: torch.zeros(1, 2, 128, 128, dtype=torch.bfloat16)})
+    with pytest.raises(ValueError, match=name):
+        prefill(fn, **{name: torch.zeros(2, 2, 128, 128)}, num_seqs=5)
+    with pytest.raises(ValueError, match="GPU"):
+        prefill(fn, **{name: torch.zeros(1, 2, 128, 128)})
+
+
+@pytest.mark.parametrize("name", ["conv_state_in", "conv_state_out"])
+def test_conv_prefill_states(name):
+    x, w, y = torch.zeros(5, C), torch.zeros(C, W), torch.zeros(5, C)
+    for n, shape in ((1, (1, W - 2, C)), (5, (4, W - 1, C))):
+        with pytest.raises(ValueError, match=name):
+            K.kda_conv_prefill(x, w, y, num_seqs=n, **{name: torch.zeros(shape)})
+    with pytest.raises(TypeError, match=name):
+        K.kda_conv_prefill(x, w, y, **{name: torch.zeros(1, W - 1, C, dtype=torch.bfloat16)})
+    with pytest.raises(ValueError, match="GPU"):
+        K.kda_conv_prefill(x, w, y, **{name: torch.zeros(1, W - 1, C)})
