@@ -307,11 +307,14 @@ def kda_affine_apply(M, X, Y, N=None, stream=None):
 def kda_decode_step(q, k, v, g, beta, state, o, scale=1.0, lower_bound=-5.0, stream=None):
     """One token per sequence. q,k,g,v [B,H,128], beta [B,H]; state float32
     [B,H,128,128] updated in place; o [B,H,128]."""
-    for n_, t_ in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state), ("o", o)):
-        _dense(t_, n_)
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and
+            beta.is_contiguous() and state.is_contiguous() and o.is_contiguous()):
+        for n_, t_ in (("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("state", state), ("o", o)):
+            _dense(t_, n_)
     B, H, dk = q.shape
     dv = v.shape[2]
-    _holds("state", state, torch.float32, B * H * dk * dv)
+    if state.dtype is not torch.float32 or state.numel() < B * H * dk * dv:
+        _holds("state", state, torch.float32, B * H * dk * dv)
     _call("kda_decode_step", _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _dt(q), B, H, dk, dv,
           scale, lower_bound, _ptr(state), _ptr(o), _dt(o), _stream(stream))
     return o
@@ -364,13 +367,15 @@ def kda_conv_state_update(x, conv_state, weight, y, bias=None, apply_silu=True, 
                           l2norm_eps=1e-6, stream=None):
     """x rows [B, >=C] (row stride x.stride(0)), conv_state [B,W-1,C] (in place),
     weight [C,W], y [B,C]."""
-    for n_, t_ in (("conv_state", conv_state), ("weight", weight), ("y", y), ("bias", bias)):
-        _dense(t_, n_)
+    if not (conv_state.is_contiguous() and weight.is_contiguous() and y.is_contiguous()) or bias is not None:
+        for n_, t_ in (("conv_state", conv_state), ("weight", weight), ("y", y), ("bias", bias)):
+            _dense(t_, n_)
     if x.stride(1) != 1:
         raise ValueError("x rows must be contiguous")
     B = x.shape[0]
     C, W = weight.shape
-    _holds("conv_state", conv_state, x.dtype, B * (W - 1) * C)
+    if conv_state.dtype is not x.dtype or conv_state.numel() < B * (W - 1) * C:
+        _holds("conv_state", conv_state, x.dtype, B * (W - 1) * C)
     _call("kda_conv_state_update", _ptr(x), x.stride(0), _ptr(conv_state), _ptr(weight), _ptr(bias), _dt(x), B, C, W,
           int(bool(apply_silu)), l2norm_group, l2norm_eps, _ptr(y), _stream(stream))
     return y

@@ -44,6 +44,7 @@ class KDAMixer:
         self.hidden = Wo.shape[0]
         self.scale, self.lower_bound, self.l2_eps, self.rms_eps = scale, lower_bound, l2_eps, rms_eps
         self._bufs = {}
+        self._device = W_in.get_device()
 
     @classmethod
     def from_host(cls, d):
@@ -67,13 +68,13 @@ class KDAMixer:
         that calls on two streams share none; a captured call's belongs to its graph
         (the capture's memory pool): a later call of another size replaces a kept
         buffer and would free what the replays use."""
-        stream = torch._C._cuda_getCurrentRawStream(self.W_in.get_device())
+        stream = torch._C._cuda_getCurrentRawStream(self._device)
         if stream:  # (nothing can be captured on the default stream, 0)
             if torch.cuda.is_current_stream_capturing():
                 return torch.empty(shape, dtype=dtype, device="cuda")
             name = (name, stream)
         b = self._bufs.get(name)
-        if b is None or tuple(b.shape) != tuple(shape) or b.dtype != dtype:
+        if b is None or b.shape != shape or b.dtype is not dtype:
             b = torch.empty(shape, dtype=dtype, device="cuda")
             self._bufs[name] = b
         return b
