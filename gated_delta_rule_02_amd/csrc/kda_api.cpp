@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 #include <string>
 #include <vector>
 
@@ -626,6 +627,274 @@ int kda_add_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const vo
     return add_rmsnorm_impl("kda_add_rmsnorm_fp8", x, x_ld, x_dtype, residual, residual_ld, residual_out,
                             residual_out_ld, residual_dtype, norm_weight, M, K, eps, codes, ldc, KDA_F32, scales,
                             ld_scale, true, hip_stream);
+}
+
+// ---------------------------------------------------------------- norms around a block
+static int sandwich_impl(const char* fn, const void* x, int64_t x_ld, kda_dtype x_dtype, const float* post_weight,
+                         float post_eps, const void* gate, int64_t gate_ld, kda_dtype gate_dtype,
+                         kda_activation gate_activation, const void* residual, int64_t residual_ld,
+                         void* residual_out, int64_t residual_out_ld, kda_dtype residual_dtype, float residual_scale,
+                         float branch_scale, const float* norm_weight, int64_t M, int64_t K, float eps, void* y,
+                         int64_t y_ld, kda_dtype y_dtype, float* scales, int64_t scale_ld, bool fp8, void* hip_stream)
+{
+    REQUIRE(M >= 0 && M <= 0x7fffffff && K >= 8, KDA_ERR_INVALID_ARG, "%s: M in [0, 2^31) and K >= 8 required", fn);
+    REQUIRE(valid_dtype(x_dtype) && valid_dtype(y_dtype) && valid_dtype(residual_dtype) && (!gate || valid_dtype(gate_dtype)),
+            KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    REQUIRE(gate_activation == KDA_ACT_NONE || gate_activation == KDA_ACT_SIGMOID, KDA_ERR_INVALID_ARG,
+            "%s: the gate's activation must be KDA_ACT_NONE or KDA_ACT_SIGMOID (got %d)", fn, (int)gate_activation);
+    REQUIRE(K % (fp8 ? 128 : 8) == 0, KDA_ERR_UNSUPPORTED, "%s: K must be a multiple of %d (got %lld)", fn,
+            fp8 ? 128 : 8, (long long)K);
+    REQUIRE(M < kMaxRows, KDA_ERR_UNSUPPORTED, "%s: at most 2^24 - 1 rows (got %lld)", fn, (long long)M);
+    REQUIRE(eps >= 0.0f && post_eps >= 0.0f, KDA_ERR_INVALID_ARG, "%s: eps must be >= 0 (got %g, %g)", fn,
+            (double)post_eps, (double)eps);
+    REQUIRE(std::isfinite(residual_scale) && std::isfinite(branch_scale), KDA_ERR_INVALID_ARG,
+            "%s: the scales must be finite (got %g, %g)", fn, (double)residual_scale, (double)branch_scale);
+    if (M == 0) return ok();
+    REQUIRE(x && post_weight && residual && norm_weight && y && (!fp8 || scales), KDA_ERR_INVALID_ARG,
+            "%s: null pointer", fn);
+    for (int64_t ld : {x_ld, residual_ld, residual_out ? residual_out_ld : K, y_ld, gate && gate_ld != 0 ? gate_ld : K})
+        REQUIRE(ld >= K && ld % 8 == 0, KDA_ERR_INVALID_ARG, "%s: row strides must be >= K and multiples of 8", fn);
+    REQUIRE(!fp8 || scale_ld >= K / 128, KDA_ERR_INVALID_ARG, "%s: the scales' row stride must be >= K/128", fn);
+    for (const void* p : {x, residual, (const void*)residual_out, gate, (const void*)post_weight, (const void*)norm_weight,
+                          fp8 ? nullptr : (const void*)y})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    REQUIRE(!fp8 || ((uintptr_t)y % 8 == 0 && (uintptr_t)scales % 4 == 0), KDA_ERR_INVALID_ARG,
+            "%s: codes must be 8-byte aligned", fn);
+    const size_t r = (size_t)(M - 1), er = esize(residual_dtype);
+    const Range rr = rng(residual, (r * residual_ld + K) * er);
+    const Range ro = rng(residual_out, residual_out ? (r * residual_out_ld + K) * er : 0);
+    const Range ry = rng(y, (r * y_ld + K) * (fp8 ? 1 : esize(y_dtype)));
+    const Range rs = rng(scales, fp8 ? (r * scale_ld + K / 128) * 4 : 0);
+    const Range rx = rng(x, (r * x_ld + K) * esize(x_dtype)), rw = rng(norm_weight, (size_t)K * 4);
+    const Range rp = rng(post_weight, (size_t)K * 4), rg = rng(gate, gate ? (r * gate_ld + K) * esize(gate_dtype) : 0);
+    for (Range out : {ro, ry, rs})
+        REQUIRE(!overlap(out, rx) && !overlap(out, rw) && !overlap(out, rp) && !overlap(out, rg), KDA_ERR_INVALID_ARG,
+                "%s: an output overlaps x, the gate or a weight", fn);
+    REQUIRE(!overlap(ry, rr) && !overlap(rs, rr) && !overlap(ry, ro) && !overlap(rs, ro) && !overlap(ry, rs),
+            KDA_ERR_INVALID_ARG, "%s: outputs overlap each other or the residual", fn);
+    REQUIRE(!overlap(ro, rr) || (residual == residual_out && residual_ld == residual_out_ld), KDA_ERR_INVALID_ARG,
+            "%s: residual and residual_out overlap without being the same rows", fn);
+    SandwichArgs a{x, x_ld, (DType)x_dtype, post_weight, gate, gate_ld, (DType)gate_dtype,
+                   gate_activation == KDA_ACT_SIGMOID, residual_scale, branch_scale, post_eps, residual, residual_ld,
+                   residual_out, residual_out_ld, (DType)residual_dtype, norm_weight, M, K, eps, y, y_ld,
+                   (DType)y_dtype, fp8 ? scales : nullptr, scale_ld};
+    return hip_status(launch_sandwich(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_sandwich_rmsnorm(const void* x, int64_t x_ld, kda_dtype x_dtype, const float* post_weight, float post_eps,
+                         const void* gate, int64_t gate_ld, kda_dtype gate_dtype, kda_activation gate_activation,
+                         const void* residual, int64_t residual_ld, void* residual_out, int64_t residual_out_ld,
+                         kda_dtype residual_dtype, float residual_scale, float branch_scale, const float* norm_weight,
+                         int64_t M, int64_t K, float eps, void* y, int64_t y_ld, kda_dtype y_dtype, void* hip_stream)
+{
+    return sandwich_impl("kda_sandwich_rmsnorm", x, x_ld, x_dtype, post_weight, post_eps, gate, gate_ld, gate_dtype,
+                         gate_activation, residual, residual_ld, residual_out, residual_out_ld, residual_dtype,
+                         residual_scale, branch_scale, norm_weight, M, K, eps, y, y_ld, y_dtype, nullptr, 0, false,
+                         hip_stream);
+}
+
+int kda_sandwich_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const float* post_weight, float post_eps,
+                             const void* gate, int64_t gate_ld, kda_dtype gate_dtype, kda_activation gate_activation,
+                             const void* residual, int64_t residual_ld, void* residual_out, int64_t residual_out_ld,
+                             kda_dtype residual_dtype, float residual_scale, float branch_scale,
+                             const float* norm_weight, int64_t M, int64_t K, float eps, uint8_t* codes, int64_t ldc,
+                             float* scales, int64_t ld_scale, void* hip_stream)
+{
+    return sandwich_impl("kda_sandwich_rmsnorm_fp8", x, x_ld, x_dtype, post_weight, post_eps, gate, gate_ld, gate_dtype,
+                         gate_activation, residual, residual_ld, residual_out, residual_out_ld, residual_dtype,
+                         residual_scale, branch_scale, norm_weight, M, K, eps, codes, ldc, KDA_F32, scales, ld_scale,
+                         true, hip_stream);
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+namespace {
+bool w4_sizes(int64_t N, int64_t K, int group)
+{
+    return (group == 32 || group == 64 || group == 128) && N >= 1 && N < kMaxRows && K >= group && K % group == 0 &&
+           K < ((int64_t)1 << 20);
+}
+int check_w4(const char* fn, int64_t N, int64_t K, int group, kda_dtype scale_dtype)
+{
+    REQUIRE(valid_dtype(scale_dtype), KDA_ERR_INVALID_ARG, "%s: bad scale dtype", fn);
+    REQUIRE(N >= 1 && K >= 1 && group >= 1, KDA_ERR_INVALID_ARG, "%s: bad sizes", fn);
+    REQUIRE(w4_sizes(N, K, group), KDA_ERR_UNSUPPORTED,
+            "%s: groups of 32, 64 or 128 columns, K a multiple of the group below 2^20 and N below 2^24 (got N = %lld, K = "
+            "%lld, group %d)", fn, (long long)N, (long long)K, group);
+    return KDA_OK;
+}
+}  // namespace
+
+size_t kda_w4_packed_bytes(int64_t N, int64_t K, int group, kda_dtype scale_dtype, int has_zeros)
+{
+    if (!w4_sizes(N, K, group) || !valid_dtype(scale_dtype)) return 0;
+    return w4_packed_bytes(N, K, group, (DType)scale_dtype, has_zeros != 0);
+}
+
+int kda_w4_pack(const uint8_t* codes, int64_t ldc, const void* scales, int64_t lds, kda_dtype scale_dtype,
+                const uint8_t* zeros, int64_t ldz, int64_t N, int64_t K, int group, void* packed, size_t packed_bytes,
+                void* hip_stream)
+{
+    const char* fn = "kda_w4_pack";
+    if (int rc = check_w4(fn, N, K, group, scale_dtype); rc != KDA_OK) return rc;
+    REQUIRE(codes && scales && packed, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    const int64_t groups = K / group;
+    REQUIRE(ldc >= K / 2 && ldc % 4 == 0 && lds >= groups && (!zeros || ldz >= groups), KDA_ERR_INVALID_ARG,
+            "%s: ldc >= K/2 (a multiple of 4), lds and ldz >= K/group", fn);
+    for (const void* p : {(const void*)codes, scales, (const void*)packed})
+        REQUIRE(aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t need = w4_packed_bytes(N, K, group, (DType)scale_dtype, zeros != nullptr), r = (size_t)(N - 1);
+    REQUIRE(packed_bytes >= need, KDA_ERR_WORKSPACE, "%s: packed must hold %zu bytes (got %zu)", fn, need, packed_bytes);
+    const Range rp = rng(packed, need);
+    REQUIRE(!overlap(rp, rng(codes, r * ldc + K / 2)) && !overlap(rp, rng(scales, (r * lds + groups) * esize(scale_dtype))) &&
+                !overlap(rp, rng(zeros, zeros ? r * ldz + groups : 0)),
+            KDA_ERR_INVALID_ARG, "%s: packed overlaps an input", fn);
+    W4PackArgs a{codes, ldc, scales, lds, (DType)scale_dtype, zeros, ldz, N, K, group, static_cast<uint8_t*>(packed)};
+    return hip_status(launch_w4_pack(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_w4_expand(const void* packed, int64_t N, int64_t K, int group, kda_dtype scale_dtype, int has_zeros, void* W,
+                  int64_t ldw, void* hip_stream)
+{
+    const char* fn = "kda_w4_expand";
+    if (int rc = check_w4(fn, N, K, group, scale_dtype); rc != KDA_OK) return rc;
+    REQUIRE(packed && W, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(ldw >= K && ldw % 8 == 0, KDA_ERR_INVALID_ARG, "%s: ldw >= K, a multiple of 8", fn);
+    REQUIRE(aligned16(packed) && aligned16(W), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    REQUIRE(!overlap(rng(packed, w4_packed_bytes(N, K, group, (DType)scale_dtype, has_zeros != 0)),
+                     rng(W, ((size_t)(N - 1) * ldw + K) * 2)),
+            KDA_ERR_INVALID_ARG, "%s: W overlaps packed", fn);
+    W4ExpandArgs a{static_cast<const uint8_t*>(packed), N, K, group, (DType)scale_dtype, has_zeros != 0,
+                   static_cast<uint16_t*>(W), ldw};
+    return hip_status(launch_w4_expand(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_gemm_w4(const void* x, int64_t ldx, kda_dtype x_dtype, const void* packed, int group, kda_dtype scale_dtype,
+                int has_zeros, const void* residual, int64_t residual_ld, kda_dtype residual_dtype, void* y,
+                int64_t ldy, kda_dtype y_dtype, int64_t M, int64_t N, int64_t K, void* hip_stream)
+{
+    const char* fn = "kda_gemm_w4";
+    REQUIRE(valid_dtype(x_dtype) && valid_dtype(y_dtype) && (!residual || valid_dtype(residual_dtype)),
+            KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    REQUIRE(x_dtype == KDA_BF16, KDA_ERR_UNSUPPORTED, "%s: only bfloat16 x is supported", fn);
+    if (int rc = check_w4(fn, N, K, group, scale_dtype); rc != KDA_OK) return rc;
+    REQUIRE(M >= 0, KDA_ERR_INVALID_ARG, "%s: M must be >= 0", fn);
+    REQUIRE(M < ((int64_t)1 << 20), KDA_ERR_UNSUPPORTED, "%s: at most 2^20 - 1 rows (got %lld)", fn, (long long)M);
+    if (M == 0) return ok();
+    REQUIRE(x && packed && y, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    // (the kernel addresses up to 64 rows of x through 32-bit offsets)
+    REQUIRE(ldx >= K && ldx % 8 == 0 && ldx < ((int64_t)1 << 22), KDA_ERR_INVALID_ARG,
+            "%s: ldx must be a multiple of 8 in [K, 2^22) (got %lld)", fn, (long long)ldx);
+    REQUIRE(ldy >= N && (!residual || residual_ld >= N), KDA_ERR_INVALID_ARG, "%s: ldy and residual_ld >= N", fn);
+    for (const void* p : {x, packed, (const void*)y, residual})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t r = (size_t)(M - 1);
+    const Range ry = rng(y, (r * ldy + N) * esize(y_dtype));
+    const Range rr = rng(residual, residual ? (r * residual_ld + N) * esize(residual_dtype) : 0);
+    REQUIRE(!overlap(ry, rng(x, (r * ldx + K) * 2)) &&
+                !overlap(ry, rng(packed, w4_packed_bytes(N, K, group, (DType)scale_dtype, has_zeros != 0))),
+            KDA_ERR_INVALID_ARG, "%s: y overlaps x or packed", fn);
+    REQUIRE(!overlap(ry, rr) || (residual == y && residual_ld == ldy && residual_dtype == y_dtype), KDA_ERR_INVALID_ARG,
+            "%s: y and the residual overlap without being the same matrix", fn);
+    W4GemmArgs a{x, ldx, static_cast<const uint8_t*>(packed), group, (DType)scale_dtype, has_zeros != 0, residual,
+                 residual_ld, (DType)residual_dtype, y, ldy, (DType)y_dtype, M, N, K};
+    return hip_status(launch_w4_gemm(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+// ---------------------------------------------------------------- beam search
+namespace {
+constexpr int kMaxBeams = 32;
+struct BeamParts {
+    int parts, len;
+    size_t sums, tops, keys, tokens, bytes;  // offsets in the workspace, total
+};
+BeamParts beam_parts(int64_t B, int W, int64_t V)
+{
+    BeamParts p;
+    p.parts = beam_part_count(B * W, V, &p.len);
+    const size_t units = (size_t)(B * W) * p.parts;
+    auto up = [](size_t n) { return (n + 15) & ~(size_t)15; };
+    p.sums = 0;
+    p.tops = up(units * 8);
+    p.keys = p.tops + up(units * 4);
+    p.tokens = p.keys + up(units * W * 4);
+    p.bytes = p.tokens + up(units * W * 4);
+    return p;
+}
+bool beam_sizes(int64_t B, int64_t W, int64_t V)
+{
+    return B >= 0 && W >= 1 && W <= kMaxBeams && V >= 1 && V <= ((int64_t)1 << 30) && B * W < ((int64_t)1 << 20);
+}
+}  // namespace
+
+size_t kda_beam_select_workspace_bytes(int B, int W, int64_t V)
+{
+    if (B < 1 || !beam_sizes(B, W, V)) return 0;
+    return beam_parts(B, W, V).bytes;
+}
+
+int kda_beam_select(const void* logits, int64_t ld, kda_dtype dtype, const float* scores, const uint8_t* finished,
+                    int B, int W, int64_t V, int64_t eos, float* next_scores, int32_t* parents, int32_t* tokens,
+                    uint8_t* next_finished, void* workspace, size_t workspace_bytes, void* hip_stream)
+{
+    const char* fn = "kda_beam_select";
+    REQUIRE(valid_dtype(dtype), KDA_ERR_INVALID_ARG, "%s: bad dtype", fn);
+    REQUIRE(B >= 0 && W >= 1 && V >= 1, KDA_ERR_INVALID_ARG, "%s: bad sizes", fn);
+    REQUIRE(beam_sizes(B, W, V), KDA_ERR_UNSUPPORTED,
+            "%s: at most %d beams, 2^30 tokens and 2^20 - 1 rows (got B = %d, W = %d, V = %lld)", fn, kMaxBeams, B, W,
+            (long long)V);
+    REQUIRE(!finished || (eos >= 0 && eos < V), KDA_ERR_INVALID_ARG,
+            "%s: with finished beams eos must be a token (got %lld)", fn, (long long)eos);
+    if (B == 0) return ok();
+    REQUIRE(logits && scores && next_scores && parents && tokens, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    REQUIRE(ld >= V, KDA_ERR_INVALID_ARG, "%s: ld must be >= V", fn);
+    REQUIRE((uintptr_t)logits % esize(dtype) == 0, KDA_ERR_INVALID_ARG, "%s: logits misaligned", fn);
+    for (const void* p : {(const void*)scores, (const void*)next_scores, (const void*)parents, (const void*)tokens})
+        REQUIRE((uintptr_t)p % 4 == 0, KDA_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    const BeamParts p = beam_parts(B, W, V);
+    REQUIRE(workspace && workspace_bytes >= p.bytes, KDA_ERR_WORKSPACE, "%s: workspace of %zu bytes required (got %zu)",
+            fn, p.bytes, workspace ? workspace_bytes : 0);
+    REQUIRE(aligned16(workspace), KDA_ERR_INVALID_ARG, "%s: the workspace must be 16-byte aligned", fn);
+    const size_t n = (size_t)B * W;
+    const Range ins[] = {rng(logits, ((n - 1) * ld + V) * esize(dtype)), rng(scores, n * 4), rng(finished, finished ? n : 0)};
+    const Range outs[] = {rng(next_scores, n * 4), rng(parents, n * 4), rng(tokens, n * 4),
+                          rng(next_finished, next_finished ? n : 0), rng(workspace, p.bytes)};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < 3; ++j)
+            REQUIRE(!overlap(outs[i], ins[j]) || (i == 0 && next_scores == scores && j == 1) ||
+                        (i == 3 && next_finished == finished && j == 2),
+                    KDA_ERR_INVALID_ARG, "%s: an output or the workspace overlaps an input", fn);
+        for (int j = 0; j < i; ++j)
+            REQUIRE(!overlap(outs[i], outs[j]), KDA_ERR_INVALID_ARG, "%s: outputs or the workspace overlap", fn);
+    }
+    char* ws = static_cast<char*>(workspace);
+    BeamSelectArgs a{logits, ld, (DType)dtype, scores, finished, B, W, (int)V,
+                     eos >= 0 && eos < V ? (int)eos : -1, p.parts, p.len, next_scores, parents, tokens, next_finished,
+                     reinterpret_cast<double*>(ws + p.sums), reinterpret_cast<float*>(ws + p.tops),
+                     reinterpret_cast<uint32_t*>(ws + p.keys), reinterpret_cast<uint32_t*>(ws + p.tokens)};
+    return hip_status(launch_beam_select(a, static_cast<hipStream_t>(hip_stream)), fn);
+}
+
+int kda_beam_reorder(const int32_t* parents, int B, int W, void* state, size_t state_bytes, void* conv_states,
+                     int streams, size_t conv_bytes, void* hip_stream)
+{
+    const char* fn = "kda_beam_reorder";
+    REQUIRE(B >= 0 && W >= 1 && streams >= 0, KDA_ERR_INVALID_ARG, "%s: bad sizes", fn);
+    REQUIRE(W <= kMaxBeams && (int64_t)B * W < ((int64_t)1 << 30) && streams < (1 << 16), KDA_ERR_UNSUPPORTED,
+            "%s: at most %d beams, 2^30 - 1 rows and 2^16 - 1 streams (got B = %d, W = %d, %d streams)", fn, kMaxBeams, B,
+            W, streams);
+    const size_t sb = state ? state_bytes : 0, cb = conv_states && streams ? conv_bytes : 0;
+    REQUIRE(sb % 16 == 0 && cb % 16 == 0, KDA_ERR_INVALID_ARG, "%s: row sizes must be multiples of 16 bytes", fn);
+    REQUIRE(sb < ((size_t)1 << 40) && cb < ((size_t)1 << 40), KDA_ERR_INVALID_ARG, "%s: row sizes too large", fn);
+    if (B == 0 || sb + cb == 0) return ok();
+    REQUIRE(parents && (uintptr_t)parents % 4 == 0, KDA_ERR_INVALID_ARG, "%s: parents null or misaligned", fn);
+    for (const void* p : {(const void*)state, (const void*)conv_states})
+        REQUIRE(!p || aligned16(p), KDA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", fn);
+    const size_t n = (size_t)B * W;
+    const Range rs = rng(state, n * sb), rc = rng(conv_states, n * streams * cb), rp = rng(parents, n * 4);
+    REQUIRE(!overlap(rs, rc) && !overlap(rs, rp) && !overlap(rc, rp), KDA_ERR_INVALID_ARG,
+            "%s: parents, state and conv_states overlap", fn);
+    BeamReorderArgs a{parents, B, W, state, (int64_t)(sb / 16), conv_states, cb ? streams : 0, (int64_t)(cb / 16)};
+    return hip_status(launch_beam_reorder(a, static_cast<hipStream_t>(hip_stream)), fn);
 }
 
 // ---------------------------------------------------------------- prefill

@@ -223,6 +223,111 @@ struct AddNormArgs {
 };
 hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t s);
 
+// h = residual_scale res + branch_scale act(gate) RMSNorm(x) w_post; res_out = h;
+// y = RMSNorm(h) w, stored as in AddNormArgs
+struct SandwichArgs {
+    const void* x;
+    int64_t x_ld;
+    DType x_dtype;
+    const float* w_post;
+    const void* gate;  // rows of stride gate_ld (0: one row for all), or null
+    int64_t gate_ld;
+    DType gate_dtype;
+    bool sigmoid;
+    float residual_scale, branch_scale, post_eps;
+    const void* res;
+    int64_t res_ld;
+    void* res_out;
+    int64_t res_out_ld;
+    DType res_dtype;
+    const float* w;
+    int64_t M, K;
+    float eps;
+    void* y;
+    int64_t y_ld;
+    DType y_dtype;
+    float* scales;
+    int64_t scale_ld;
+};
+hipError_t launch_sandwich(const SandwichArgs& a, hipStream_t s);
+
+// 4-bit weights: W[n, k] = scales[n, k/group] (code - zeros[n, k/group]); zeros null: 8
+struct W4PackArgs {
+    const uint8_t* codes;  // [N, K/2], the even column in the low four bits
+    int64_t codes_ld;
+    const void* scales;  // [N, K/group]
+    int64_t scales_ld;
+    DType scale_dtype;
+    const uint8_t* zeros;  // [N, K/group] or null
+    int64_t zeros_ld, N, K;
+    int group;
+    uint8_t* packed;
+};
+size_t w4_packed_bytes(int64_t N, int64_t K, int group, DType scale_dtype, bool has_zeros);
+hipError_t launch_w4_pack(const W4PackArgs& a, hipStream_t s);
+
+struct W4ExpandArgs {
+    const uint8_t* packed;
+    int64_t N, K;
+    int group;
+    DType scale_dtype;
+    bool has_zeros;
+    uint16_t* out;  // bfloat16 [N, K], row stride out_ld
+    int64_t out_ld;
+};
+hipError_t launch_w4_expand(const W4ExpandArgs& a, hipStream_t s);
+
+// y[M, N] = x[M, K] W^T (+ res)
+struct W4GemmArgs {
+    const void* x;  // bfloat16
+    int64_t x_ld;
+    const uint8_t* packed;
+    int group;
+    DType scale_dtype;
+    bool has_zeros;
+    const void* res;  // [M, N] or null; may be y itself
+    int64_t res_ld;
+    DType res_dtype;
+    void* y;
+    int64_t y_ld;
+    DType y_dtype;
+    int64_t M, N, K;
+};
+hipError_t launch_w4_gemm(const W4GemmArgs& a, hipStream_t s);
+
+// the W best of every sequence's W x V continuations; each row of logits in `parts`
+// parts of part_len tokens
+struct BeamSelectArgs {
+    const void* logits;  // [B * W, V], row stride ld
+    int64_t ld;
+    DType dtype;
+    const float* scores;      // [B, W]
+    const uint8_t* finished;  // [B, W] or null
+    int B, W, V, eos, parts, part_len;
+    float* next_scores;
+    int32_t *parents, *tokens;
+    uint8_t* next_finished;  // or null
+    // workspace, [B * W * parts] each, the last two with W entries each
+    double* part_sum;
+    float* part_top;
+    uint32_t *part_key, *part_token;
+};
+// parts (at most 64) into which a row of V logits is cut, and their length
+int beam_part_count(int64_t rows, int64_t V, int* len);
+hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s);
+
+// state[b, w] <- state[b, parents[b, w]] in place, in units of 16 bytes
+struct BeamReorderArgs {
+    const int32_t* parents;  // [B, W]
+    int B, W;
+    void* state;  // [B, W, state_vecs]
+    int64_t state_vecs;
+    void* conv;  // [streams, B, W, conv_vecs]
+    int streams;
+    int64_t conv_vecs;
+};
+hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t s);
+
 struct GemmArgs {
     const void *A, *B;
     void* C;

@@ -1,5 +1,6 @@
 // kda_norm.hip -- residual addition + RMSNorm in front of a block's projections,
-// its output in float32, bfloat16 or block FP8 (gfx950).
+// also with a norm of the block's output before it is added, its output in
+// float32, bfloat16 or block FP8 (gfx950).
 //
 // Per row: h = x + residual, residual_out = round(h), and
 //   y = h / sqrt(mean(h^2) + eps) * w,
@@ -61,8 +62,8 @@ __device__ __forceinline__ float row_sum(float v, float* part)
 }
 
 // 8 normalised values of columns c .. c + 7 of row m -> memory
-template <typename TY>
-__device__ __forceinline__ void emit8(const AddNormArgs& a, int64_t m, int64_t c, const float* y)
+template <typename TY, typename Args>
+__device__ __forceinline__ void emit8(const Args& a, int64_t m, int64_t c, const float* y)
 {
     if constexpr (!__is_same(TY, Fp8Out)) {
         store8(static_cast<TY*>(a.y) + m * a.y_ld + c, y);
@@ -204,12 +205,168 @@ hipError_t launch_out(const AddNormArgs& a, hipStream_t s)
     return a.y_dtype == F32 ? launch_res<TX, float>(a, s) : launch_res<TX, bf16_t>(a, s);
 }
 
+// ---------------------------------------------------------------- a norm after the block, too
+//   h = residual_scale residual + branch_scale act(gate) x / sqrt(mean(x^2) + post_eps) w_post
+//   residual_out = round(h),  y = h / sqrt(mean(h^2) + eps) w
+// One pass as above, with two sums over the row; the row, its residual and gate are in
+// registers before the first (all loads go out together). Everything is float32 until stored.
+enum Gate : int { kNoGate = 0, kGate = 1, kSigmoid = 2 };
+
+// the 8 columns of h from those of x (normalised by rn), residual r and gate g
+template <int GATE>
+__device__ __forceinline__ void combine8(const SandwichArgs& a, int64_t c, float rn, const float* r, const float* g, float* h)
+{
+    float w[8];
+    load8(a.w_post + c, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float n = h[i] * rn * w[i];
+        if constexpr (GATE == kGate) n *= g[i];
+        if constexpr (GATE == kSigmoid) n *= sigmoidf_(g[i]);
+        h[i] = fmaf(a.branch_scale, n, a.residual_scale * r[i]);
+    }
+}
+
+template <typename TX, typename TR, typename TG, typename TY, int GATE, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_kernel(SandwichArgs a)
+{
+    constexpr int THREADS = TPR > 256 ? TPR : 256;
+    __shared__ float part[2][TPR / 64];
+    const int t = threadIdx.x % TPR;
+    const int64_t m = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+    if (m >= a.M) return;  // whole wavefronts (TPR = 64) leave; otherwise a workgroup has one row
+    const TX* x = static_cast<const TX*>(a.x) + m * a.x_ld;
+    float h[NV][8], r[NV][8], g[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int64_t c = (int64_t)(v * TPR + t) * 8;
+        if (c < a.K) {
+            load8(x + c, h[v]);
+            load8(static_cast<const TR*>(a.res) + m * a.res_ld + c, r[v]);
+            if constexpr (GATE != kNoGate) load8(static_cast<const TG*>(a.gate) + m * a.gate_ld + c, g[v]);
+        }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+        if ((int64_t)(v * TPR + t) * 8 < a.K)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += h[v][i] * h[v][i];
+    const float rx = 1.0f / sqrtf(row_sum<TPR>(ss, part[0]) / (float)a.K + a.post_eps);
+    ss = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int64_t c = (int64_t)(v * TPR + t) * 8;
+        if (c >= a.K) continue;
+        combine8<GATE>(a, c, rx, r[v], g[v], h[v]);
+        if (a.res_out) store8(static_cast<TR*>(a.res_out) + m * a.res_out_ld + c, h[v]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += h[v][i] * h[v][i];
+    }
+    const float rh = 1.0f / sqrtf(row_sum<TPR>(ss, part[1]) / (float)a.K + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int64_t c = (int64_t)(v * TPR + t) * 8;
+        if (c >= a.K) continue;  // K is a multiple of 128 for FP8: whole 16-lane groups leave
+        float y[8], w[8];
+        load8(a.w + c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = h[v][i] * rh * w[i];
+        emit8<TY>(a, m, c, y);
+    }
+}
+
+// Rows too wide for the registers: x is read again for h, and h formed again (from the
+// caches) for y. residual_out is written in the last sweep.
+template <typename TX, typename TR, typename TG, typename TY, int GATE>
+__global__ __launch_bounds__(1024) void sandwich_wide_kernel(SandwichArgs a)
+{
+    __shared__ float part[2][16];
+    const int64_t m = blockIdx.x;
+    const TX* x = static_cast<const TX*>(a.x) + m * a.x_ld;
+    float ss = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < a.K; c += 8192) {
+        float h[8];
+        load8(x + c, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += h[i] * h[i];
+    }
+    const float rx = 1.0f / sqrtf(row_sum<1024>(ss, part[0]) / (float)a.K + a.post_eps);
+    auto row8 = [&](int64_t c, float* h) {
+        float r[8], g[8];
+        load8(x + c, h);
+        load8(static_cast<const TR*>(a.res) + m * a.res_ld + c, r);
+        if constexpr (GATE != kNoGate) load8(static_cast<const TG*>(a.gate) + m * a.gate_ld + c, g);
+        combine8<GATE>(a, c, rx, r, g, h);
+    };
+    ss = 0.0f;
+    for (int64_t c = threadIdx.x * 8; c < a.K; c += 8192) {
+        float h[8];
+        row8(c, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += h[i] * h[i];
+    }
+    const float rh = 1.0f / sqrtf(row_sum<1024>(ss, part[1]) / (float)a.K + a.eps);
+    for (int64_t c = threadIdx.x * 8; c < a.K; c += 8192) {
+        float h[8], w[8];
+        row8(c, h);  // before this thread's own store: residual_out may be residual
+        if (a.res_out) store8(static_cast<TR*>(a.res_out) + m * a.res_out_ld + c, h);
+        load8(a.w + c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = h[i] * rh * w[i];
+        emit8<TY>(a, m, c, h);
+    }
+}
+
+template <typename TX, typename TR, typename TG, typename TY, int GATE>
+hipError_t sandwich_rows(const SandwichArgs& a, hipStream_t s)
+{
+    const dim3 rows((unsigned)a.M);
+    if (a.K <= 1024)
+        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, 64, 2>), dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, s, a);
+    else if (a.K <= 4096)
+        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, 256, 2>), rows, dim3(256), 0, s, a);
+    else if (a.K <= 8192)
+        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, 256, 4>), rows, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((sandwich_wide_kernel<TX, TR, TG, TY, GATE>), rows, dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename TX, typename TR, typename TY>
+hipError_t sandwich_gate(const SandwichArgs& a, hipStream_t s)
+{
+    if (!a.gate) return sandwich_rows<TX, TR, float, TY, kNoGate>(a, s);
+    if (a.gate_dtype == F32)
+        return a.sigmoid ? sandwich_rows<TX, TR, float, TY, kSigmoid>(a, s) : sandwich_rows<TX, TR, float, TY, kGate>(a, s);
+    return a.sigmoid ? sandwich_rows<TX, TR, bf16_t, TY, kSigmoid>(a, s) : sandwich_rows<TX, TR, bf16_t, TY, kGate>(a, s);
+}
+
+template <typename TX, typename TR>
+hipError_t sandwich_out(const SandwichArgs& a, hipStream_t s)
+{
+    if (a.scales) return sandwich_gate<TX, TR, Fp8Out>(a, s);
+    return a.y_dtype == F32 ? sandwich_gate<TX, TR, float>(a, s) : sandwich_gate<TX, TR, bf16_t>(a, s);
+}
+
+template <typename TX>
+hipError_t sandwich_res(const SandwichArgs& a, hipStream_t s)
+{
+    return a.res_dtype == F32 ? sandwich_out<TX, float>(a, s) : sandwich_out<TX, bf16_t>(a, s);
+}
+
 }  // namespace
 
 hipError_t launch_add_norm(const AddNormArgs& a, hipStream_t s)
 {
     if (a.M == 0) return hipSuccess;
     return a.x_dtype == F32 ? launch_out<float>(a, s) : launch_out<bf16_t>(a, s);
+}
+
+hipError_t launch_sandwich(const SandwichArgs& a, hipStream_t s)
+{
+    if (a.M == 0) return hipSuccess;
+    return a.x_dtype == F32 ? sandwich_res<float>(a, s) : sandwich_res<bf16_t>(a, s);
 }
 
 }  // namespace kda

@@ -57,6 +57,17 @@ _SIGS = {
     "kda_add_rmsnorm": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _I64, _I, _P]),
     "kda_add_rmsnorm_fp8": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _I, _P, _I64, _I64, _F, _P, _I64, _P, _I64, _P]),
     "kda_gemm_epilogue": (_I, [_P, _I64, _P, _I64, _P, _I, _P, _I64, _I, _P, _I64, _I64, _I64, _I64, _I, _I, _P]),
+    "kda_sandwich_rmsnorm": (_I, [_P, _I64, _I, _P, _F, _P, _I64, _I, _I, _P, _I64, _P, _I64, _I, _F, _F, _P, _I64, _I64,
+                                  _F, _P, _I64, _I, _P]),
+    "kda_sandwich_rmsnorm_fp8": (_I, [_P, _I64, _I, _P, _F, _P, _I64, _I, _I, _P, _I64, _P, _I64, _I, _F, _F, _P, _I64,
+                                      _I64, _F, _P, _I64, _P, _I64, _P]),
+    "kda_w4_packed_bytes": (_SZ, [_I64, _I64, _I, _I, _I]),
+    "kda_w4_pack": (_I, [_P, _I64, _P, _I64, _I, _P, _I64, _I64, _I64, _I, _P, _SZ, _P]),
+    "kda_w4_expand": (_I, [_P, _I64, _I64, _I, _I, _I, _P, _I64, _P]),
+    "kda_gemm_w4": (_I, [_P, _I64, _I, _P, _I, _I, _I, _P, _I64, _I, _P, _I64, _I, _I64, _I64, _I64, _P]),
+    "kda_beam_select_workspace_bytes": (_SZ, [_I, _I, _I64]),
+    "kda_beam_select": (_I, [_P, _I64, _I, _P, _P, _I, _I, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "kda_beam_reorder": (_I, [_P, _I, _I, _P, _SZ, _P, _I, _SZ, _P]),
     "kda_state_bytes": (_SZ, [_I, _I, _I, _I]),
     "kda_conv_state_bytes": (_SZ, [_I, _I, _I, _I]),
     "kda_last_error": (ctypes.c_char_p, []),
@@ -163,6 +174,20 @@ def _workspace(device, nbytes, stream=None):
         buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
         _workspaces[key] = buf
     return buf
+
+
+def _workspace_on(t, nbytes, stream):
+    """_workspace on t's device (made current for it), for the calls through _call_on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensor must be on a GPU device")
+    if stream is None and index == torch._C._cuda_getDevice():
+        raw = torch._C._cuda_getCurrentRawStream(index)
+        buf = _workspaces.get((index, raw))
+        if buf is not None and buf.numel() >= nbytes and not (raw and torch.cuda.is_current_stream_capturing()):
+            return buf
+    with torch.cuda.device(index):
+        return _workspace(t.device, nbytes, stream)
 
 
 def kda_prefill(q, k, v, g, beta, o, cu_seqlens=None, cu_seqlens_host=None, num_seqs=None,
@@ -714,6 +739,213 @@ def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stre
              _mat("B", B, bshape), pb, act, pr, ldr, rd, C.data_ptr(), _mat("C", C, shape), M, N, K, _code(A, "A"),
              _code(C, "C"))
     return C
+
+
+def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
+                   branch_scale, post_eps, eps):
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError("x must be [M, K]")
+    for name, w in (("post_weight", post_weight), ("norm_weight", norm_weight)):
+        if w.shape != shape[1:] or w.dtype is not torch.float32 or not w.is_contiguous():
+            raise TypeError("%s must be dense float32 [K]" % name)
+    act = ACTIVATIONS.get(gate_activation)
+    if gate_activation not in ("none", "sigmoid"):
+        raise ValueError("gate_activation must be 'none' or 'sigmoid' (got %r)" % (gate_activation,))
+    pg, g_ld, gd = None, 0, KDA_F32
+    if gate is not None:
+        pg, gd = gate.data_ptr(), _code(gate, "gate")
+        if gate.dim() == 1:
+            _tensor("gate", gate, shape[1:])
+        else:
+            g_ld = _mat("gate", gate, shape)
+    ro, ro_ld = None, 0
+    if residual_out is not None:
+        _type("residual_out", residual_out, residual.dtype)
+        ro, ro_ld = residual_out.data_ptr(), _mat("residual_out", residual_out, shape)
+    return (x.data_ptr(), _mat("x", x, shape), _code(x, "x"), post_weight.data_ptr(), post_eps, pg, g_ld, gd, act,
+            residual.data_ptr(), _mat("residual", residual, shape), ro, ro_ld, _code(residual, "residual"), residual_scale,
+            branch_scale, norm_weight.data_ptr(), shape[0], shape[1], eps)
+
+
+def kda_sandwich_rmsnorm(x, post_weight, residual, residual_out, norm_weight, y, gate=None, gate_activation="none",
+                         residual_scale=1.0, branch_scale=1.0, post_eps=1e-6, eps=1e-6, stream=None):
+    """h = residual_scale * residual + branch_scale * act(gate) * RMSNorm(x) * post_weight,
+    residual_out = h, y = RMSNorm(h) * norm_weight. x, residual, y [M, K] (row strides
+    allowed; float32 or bfloat16 each), the weights float32 [K]; gate [M, K] rows or
+    one [K] for all (float32 or bfloat16), through 'none' or 'sigmoid'; residual_out
+    (the residual's dtype, or None) may be residual itself."""
+    args = _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
+                          branch_scale, post_eps, eps)
+    _call_on("kda_sandwich_rmsnorm", (x, post_weight, residual, residual_out, norm_weight, y, gate), stream, *args,
+             y.data_ptr(), _mat("y", y, x.shape), _code(y, "y"))
+    return y
+
+
+def kda_sandwich_rmsnorm_fp8(x, post_weight, residual, residual_out, norm_weight, codes, scales, gate=None,
+                             gate_activation="none", residual_scale=1.0, branch_scale=1.0, post_eps=1e-6, eps=1e-6,
+                             stream=None):
+    """kda_sandwich_rmsnorm with y quantized as kda_quantize_fp8 does: codes uint8
+    [M, K] (E4M3), scales float32 [M, K/128]; K a multiple of 128."""
+    args = _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
+                          branch_scale, post_eps, eps)
+    _type("codes", codes, torch.uint8), _type("scales", scales, torch.float32)
+    M, K = x.shape
+    _call_on("kda_sandwich_rmsnorm_fp8", (x, post_weight, residual, residual_out, norm_weight, codes, scales, gate), stream,
+             *args, codes.data_ptr(), _mat("codes", codes, x.shape), scales.data_ptr(),
+             _mat("scales", scales, (M, K // 128)))
+    return codes, scales
+
+
+class W4Weight:
+    """A packed 4-bit weight [N, K] (kda_w4_pack): one uint8 buffer with its codes,
+    scales and zero points, in the layout that kda_gemm_w4 streams."""
+
+    __slots__ = ("packed", "N", "K", "group", "scale_code", "has_zeros")
+
+    def __init__(self, packed, N, K, group, scale_code, has_zeros):
+        self.packed, self.N, self.K, self.group = packed, N, K, group
+        self.scale_code, self.has_zeros = scale_code, has_zeros
+
+    @property
+    def shape(self):
+        return torch.Size((self.N, self.K))
+
+
+def kda_w4_packed_bytes(N, K, group, scale_dtype=KDA_F32, has_zeros=False):
+    return lib().kda_w4_packed_bytes(N, K, group, scale_dtype, int(bool(has_zeros)))
+
+
+def kda_w4_pack(codes, scales, zeros=None, stream=None):
+    """W[n,k] = scales[n, k/group] * (code[n,k] - zeros[n, k/group]) laid out for kda_gemm_w4
+    -> W4Weight. codes uint8 [N, K/2] (the even column in the low four bits),
+    scales [N, K/group] float32 or bfloat16, zeros uint8 [N, K/group] (None: 8). Once per
+    weight; the inputs are not kept. Row strides allowed."""
+    if codes.dim() != 2 or scales.dim() != 2 or scales.shape[0] != codes.shape[0] or scales.shape[1] < 1:
+        raise ValueError("codes must be [N, K/2] and scales [N, K/group] (got %s, %s)" %
+                         (tuple(codes.shape), tuple(scales.shape)))
+    _type("codes", codes, torch.uint8)
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    group, rest = divmod(K, scales.shape[1])
+    if rest:
+        raise ValueError("%d scales a row do not divide %d columns" % (scales.shape[1], K))
+    code = _code(scales, "scales")
+    pz, ldz = None, 0
+    if zeros is not None:
+        _type("zeros", zeros, torch.uint8)
+        pz, ldz = zeros.data_ptr(), _mat("zeros", zeros, scales.shape)
+    if not codes.is_cuda:
+        raise ValueError("tensor must be on a GPU device")
+    nbytes = kda_w4_packed_bytes(N, K, group, code, zeros is not None)
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(codes.device):
+        packed = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    _call_on("kda_w4_pack", (codes, scales, zeros, packed), stream, codes.data_ptr(), _mat("codes", codes, codes.shape),
+             scales.data_ptr(), _mat("scales", scales, scales.shape), code, pz, ldz, N, K, group, packed.data_ptr(), nbytes)
+    return W4Weight(packed, N, K, group, code, zeros is not None)
+
+
+def kda_w4_expand(weight, out, stream=None):
+    """out [N, K] <- the packed weight's values in bfloat16 (row strides allowed)."""
+    _type("out", out, torch.bfloat16)
+    _call_on("kda_w4_expand", (out, weight.packed), stream, weight.packed.data_ptr(), weight.N, weight.K, weight.group,
+             weight.scale_code, int(weight.has_zeros), out.data_ptr(), _mat("out", out, (weight.N, weight.K)))
+    return out
+
+
+def kda_gemm_w4(x, weight, y, residual=None, stream=None):
+    """y[M,N] = x[M,K] W^T (+ residual) from a W4Weight (bfloat16 x; y and the residual
+    float32 or bfloat16; rows may be strided). residual may be y itself."""
+    M, K = x.shape
+    if K != weight.K:
+        raise ValueError("x must be [M, %d] (got %s)" % (weight.K, tuple(x.shape)))
+    shape = (M, weight.N)
+    pr, ldr, rd = None, 0, KDA_F32
+    if residual is not None:
+        pr, ldr, rd = residual.data_ptr(), _mat("residual", residual, shape), _code(residual, "residual")
+    packed = weight.packed
+    _call_on("kda_gemm_w4", (x, packed, y, residual), stream, x.data_ptr(), _mat("x", x, (M, K)), _code(x, "x"),
+             packed.data_ptr(), weight.group, weight.scale_code, 1 if weight.has_zeros else 0, pr, ldr, rd, y.data_ptr(),
+             _mat("y", y, shape), _code(y, "y"), M, weight.N, K)
+    return y
+
+
+def kda_beam_select_workspace_bytes(B, W, V):
+    return lib().kda_beam_select_workspace_bytes(B, W, V)
+
+
+_beam_bytes = {}
+
+
+def kda_beam_select(logits, scores, next_scores, parents, tokens, finished=None, next_finished=None, eos=-1,
+                    workspace="auto", stream=None):
+    """The W best of every sequence's W beams x V tokens by scores + log softmax(logits),
+    best first, ties to the lower beam, then token. logits [B*W, V] (float32 or
+    bfloat16, rows may be strided), scores and next_scores float32 [B, W] (may be one
+    tensor), parents (the beam followed) and tokens int32 [B, W]; finished and
+    next_finished bool [B, W] or None: a beam that has ended goes on with token eos
+    at its score. workspace: "auto" (kept per stream) or a uint8 tensor of
+    kda_beam_select_workspace_bytes bytes."""
+    if scores.dim() != 2:
+        raise ValueError("scores must be [B, W]")
+    shape = scores.shape
+    B, W = shape
+    n, V = logits.shape
+    if n != B * W:
+        raise ValueError("logits must be [%d, V] for scores [%d, %d] (got %s)" % (B * W, B, W, tuple(logits.shape)))
+    if not (next_scores.shape == shape and parents.shape == shape and tokens.shape == shape and
+            scores.dtype is torch.float32 and next_scores.dtype is torch.float32 and parents.dtype is torch.int32 and
+            tokens.dtype is torch.int32 and scores.is_contiguous() and next_scores.is_contiguous() and
+            parents.is_contiguous() and tokens.is_contiguous()):
+        for name, t, dtype in (("scores", scores, torch.float32), ("next_scores", next_scores, torch.float32),
+                               ("parents", parents, torch.int32), ("tokens", tokens, torch.int32)):
+            _tensor(name, t, shape), _type(name, t, dtype)
+    pf = pn = None
+    if finished is not None:
+        _tensor("finished", finished, shape), _type("finished", finished, torch.bool)
+        pf = finished.data_ptr()
+    if next_finished is not None:
+        _tensor("next_finished", next_finished, shape), _type("next_finished", next_finished, torch.bool)
+        pn = next_finished.data_ptr()
+    ld = logits.stride(0) if n > 1 else V
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("logits rows must be contiguous")
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto' or a tensor")
+        need = _beam_bytes.get((B, W, V))
+        if need is None:
+            need = _beam_bytes[(B, W, V)] = lib().kda_beam_select_workspace_bytes(B, W, V)
+        workspace = _workspace_on(logits, need, stream)
+    pw, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call_on("kda_beam_select", (logits, scores, next_scores, parents, tokens, finished, next_finished, workspace), stream,
+             logits.data_ptr(), ld, _code(logits, "logits"), scores.data_ptr(), pf, B, W, V, eos, next_scores.data_ptr(),
+             parents.data_ptr(), tokens.data_ptr(), pn, pw, wbytes)
+    return next_scores, parents, tokens, next_finished
+
+
+def kda_beam_reorder(parents, state, conv_states=None, stream=None):
+    """state[b, w] <- state[b, parents[b, w]] in place, and likewise every stream of
+    conv_states. parents int32 [B, W]; state [B*W, ...] and conv_states [streams, B*W,
+    ...] dense, of any dtype. A parent that is no beam leaves its row as it is."""
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, W]")
+    B, W = parents.shape
+    _tensor("parents", parents, (B, W)), _type("parents", parents, torch.int32)
+    rows = B * W
+    if state.dim() < 1 or state.shape[0] != rows or not state.is_contiguous():
+        raise ValueError("state must be dense [%d, ...] for parents [%d, %d] (got %s)" % (rows, B, W, tuple(state.shape)))
+    nbytes = state.numel() * state.element_size()
+    pc, streams, cbytes = None, 0, 0
+    if conv_states is not None:
+        if conv_states.dim() < 2 or conv_states.shape[1] != rows or not conv_states.is_contiguous():
+            raise ValueError("conv_states must be dense [streams, %d, ...] (got %s)" % (rows, tuple(conv_states.shape)))
+        pc, streams = conv_states.data_ptr(), conv_states.shape[0]
+        cbytes = conv_states.numel() * conv_states.element_size()
+    if rows == 0:
+        return state
+    _call_on("kda_beam_reorder", (parents, state, conv_states), stream, parents.data_ptr(), B, W, state.data_ptr(),
+             nbytes // rows, pc, streams, cbytes // (rows * max(streams, 1)))
+    return state
 
 
 def kda_state_bytes(H, dk=128, dv=128, dtype=KDA_F32):

@@ -676,6 +676,133 @@ int kda_gemm_epilogue(const void* A, int64_t lda, const void* B, int64_t ldb, co
                       kda_dtype ab_dtype, kda_dtype c_dtype, void* hip_stream);
 
 /* ------------------------------------------------------------------------
+ * kda_sandwich_rmsnorm -- the norm after a block, its gate and residual scale, and
+ * the norm before the next block.
+ *
+ *   n = x / sqrt(mean(x^2) + post_eps) * post_weight
+ *   h = residual_scale * residual + branch_scale * act(gate) * n
+ *   residual_out = h,  y = h / sqrt(mean(h^2) + eps) * norm_weight
+ * per row of K columns: kda_add_rmsnorm for blocks whose output is normalised (and
+ * gated) before it is added. Everything is float32; every output is rounded
+ * once, when stored.
+ *
+ * x             [M, K] x_dtype, row stride x_ld: the block's output.
+ * post_weight, norm_weight  float32 [K].
+ * gate          gate_dtype, or NULL (no factor): rows of K, row stride gate_ld (a
+ *               multiple of 8, at least K), or, with gate_ld = 0, one row of K for all.
+ * gate_activation  KDA_ACT_NONE or KDA_ACT_SIGMOID.
+ * residual, residual_out, y  as for kda_add_rmsnorm, but the residual is required.
+ * Sizes, strides, alignment and overlaps as for kda_add_rmsnorm; both eps >= 0, the
+ * scales finite.
+ * ---------------------------------------------------------------------- */
+int kda_sandwich_rmsnorm(const void* x, int64_t x_ld, kda_dtype x_dtype, const float* post_weight, float post_eps,
+                         const void* gate, int64_t gate_ld, kda_dtype gate_dtype, kda_activation gate_activation,
+                         const void* residual, int64_t residual_ld, void* residual_out, int64_t residual_out_ld,
+                         kda_dtype residual_dtype, float residual_scale, float branch_scale, const float* norm_weight,
+                         int64_t M, int64_t K, float eps, void* y, int64_t y_ld, kda_dtype y_dtype, void* hip_stream);
+
+/* kda_sandwich_rmsnorm with y quantized as by kda_add_rmsnorm_fp8 (codes, ldc, scales,
+ * ld_scale and K as there). */
+int kda_sandwich_rmsnorm_fp8(const void* x, int64_t x_ld, kda_dtype x_dtype, const float* post_weight, float post_eps,
+                             const void* gate, int64_t gate_ld, kda_dtype gate_dtype, kda_activation gate_activation,
+                             const void* residual, int64_t residual_ld, void* residual_out, int64_t residual_out_ld,
+                             kda_dtype residual_dtype, float residual_scale, float branch_scale,
+                             const float* norm_weight, int64_t M, int64_t K, float eps, uint8_t* codes, int64_t ldc,
+                             float* scales, int64_t ld_scale, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_w4_pack -- 4-bit weights laid out for kda_gemm_w4 (once per weight).
+ *
+ *   W[n, k] = scales[n, k / group] * (code[n, k] - zeros[n, k / group])
+ * codes   uint8 [N, K/2], row stride ldc (a multiple of 4): columns 2 i and 2 i + 1 in the
+ *         low and the high four bits of byte i, each 0..15.
+ * scales  [N, K/group] scale_dtype, row stride lds.
+ * zeros   uint8 [N, K/group], row stride ldz, values 0..15 (the low four bits count);
+ *         or NULL: 8 throughout.
+ * packed  kda_w4_packed_bytes(N, K, group, scale_dtype, zeros != NULL) bytes, complete with
+ *         scales and zero points; must not overlap an input.
+ * group is 32, 64 or 128, K a multiple of it; N < 2^24, K < 2^20.
+ * kda_w4_packed_bytes returns 0 for sizes that are not supported.
+ * ---------------------------------------------------------------------- */
+size_t kda_w4_packed_bytes(int64_t N, int64_t K, int group, kda_dtype scale_dtype, int has_zeros);
+int kda_w4_pack(const uint8_t* codes, int64_t ldc, const void* scales, int64_t lds, kda_dtype scale_dtype,
+                const uint8_t* zeros, int64_t ldz, int64_t N, int64_t K, int group, void* packed, size_t packed_bytes,
+                void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_gemm_w4 -- y[M, N] = x[M, K] * W[N, K]^T (+ residual) from a packed 4-bit W.
+ *
+ * For decoding: W's four bits are read once for up to 64 rows of x and are exact
+ * in the products (x is bfloat16, the sums float32, a group's scale is applied
+ * in float32 to the group's sum). Any M works; for hundreds of rows and more expand W
+ * (kda_w4_expand) and use kda_gemm_epilogue.
+ *
+ * x         rows of K at x + m * ldx (x_dtype = KDA_BF16; ldx a multiple of 8, < 2^22).
+ *           A value that is not finite makes its row of y NaN; a row whose values exceed
+ *           2^100 may overflow.
+ * packed, group, scale_dtype, has_zeros  as given to kda_w4_pack for this N and K.
+ * residual  [M, N] residual_dtype, row stride residual_ld, or NULL. It may be y itself
+ *           (same pointer, stride and dtype); any other overlap is rejected.
+ * y         rows of N at y + m * ldy (y_dtype; any ldy >= N).
+ * M < 2^20, M = 0 does nothing.
+ * ---------------------------------------------------------------------- */
+int kda_gemm_w4(const void* x, int64_t ldx, kda_dtype x_dtype, const void* packed, int group, kda_dtype scale_dtype,
+                int has_zeros, const void* residual, int64_t residual_ld, kda_dtype residual_dtype, void* y,
+                int64_t ldy, kda_dtype y_dtype, int64_t M, int64_t N, int64_t K, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_w4_expand -- W of a packed 4-bit weight in bfloat16 (rounded to nearest), for
+ * products of many rows. W rows of K at W + n * ldw, ldw a multiple of 8.
+ * ---------------------------------------------------------------------- */
+int kda_w4_expand(const void* packed, int64_t N, int64_t K, int group, kda_dtype scale_dtype, int has_zeros, void* W,
+                  int64_t ldw, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_beam_select -- the best continuations of every sequence's beams.
+ *
+ * A beam w of sequence b offers every token v at
+ *   c[w, v] = scores[b, w] + logits[b, w, v] - log(sum_u exp(logits[b, w, u])).
+ * A beam that has ended (finished) offers its end token alone, at scores[b, w]: all
+ * others at -inf. The W best of the W * V offers become the new beams, best first;
+ * equal ones in the order of beam, then token. Offers are compared in 64 bits.
+ *   next_scores[b, i], parents[b, i] (the beam followed), tokens[b, i],
+ *   next_finished[b, i] = the followed beam had ended, or the token is eos.
+ * Logits of -inf are tokens that are not offered: like all offers of -inf they come
+ * last. A beam is dead (all its offers are -inf) if its score is not finite, or
+ * none of its logits is, or one of them is +inf or NaN. At a first step give the
+ * beams but one a score of -inf.
+ *
+ * logits     [B * W, V] dtype, row stride ld (any, >= V), aligned to its type.
+ * scores     float32 [B, W]; next_scores may be scores itself.
+ * finished   uint8 [B, W] (0 or 1) or NULL (none has ended; next_finished may be
+ *            finished itself); with it 0 <= eos < V. Without, eos may be any value.
+ * next_finished  uint8 [B, W] or NULL.
+ * parents, tokens  int32 [B, W].
+ * workspace  kda_beam_select_workspace_bytes(B, W, V) bytes, 16-byte aligned: calls that
+ *            share it must be ordered.
+ * 1 <= W <= 32, 1 <= V <= 2^30, B * W < 2^20; B = 0 does nothing.
+ * ---------------------------------------------------------------------- */
+size_t kda_beam_select_workspace_bytes(int B, int W, int64_t V);
+int kda_beam_select(const void* logits, int64_t ld, kda_dtype dtype, const float* scores, const uint8_t* finished,
+                    int B, int W, int64_t V, int64_t eos, float* next_scores, int32_t* parents, int32_t* tokens,
+                    uint8_t* next_finished, void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* ------------------------------------------------------------------------
+ * kda_beam_reorder -- recurrent states and histories follow the chosen beams.
+ *
+ *   state[b, w] <- state[b, parents[b, w]],  conv_states[s, b, w] <- conv_states[s, b, parents[b, w]]
+ * in place (bit copies; a beam may be followed by any number of others). A parent that
+ * is no beam (not in 0..W-1) leaves its row as it is.
+ *
+ * parents      int32 [B, W].
+ * state        [B, W] rows of state_bytes each, or NULL.
+ * conv_states  [streams, B, W] rows of conv_bytes each, or NULL.
+ * Row sizes are multiples of 16 bytes; 1 <= W <= 32, 0 <= streams < 2^16; B = 0 does nothing.
+ * ---------------------------------------------------------------------- */
+int kda_beam_reorder(const int32_t* parents, int B, int W, void* state, size_t state_bytes, void* conv_states,
+                     int streams, size_t conv_bytes, void* hip_stream);
+
+/* ------------------------------------------------------------------------
  * Size helpers. kda_state_bytes(64, 128, 128, KDA_F32) = 4,194,304: one
  * [64,128,128] FP32 matrix per layer, 252 MiB over 63 layers (flozi.net page,
  * section "KDA replaces a token list with a recurrent matrix").

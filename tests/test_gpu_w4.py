@@ -1,0 +1,147 @@
+"""Products with 4-bit weights on the GPU against the formula in 64 bits.
+
+Exact cases: x and the scales are small integers and powers of two, so that every
+product and partial sum is an integer multiple of a power of two below 2^24 of
+them: the float32 result has no rounding and must be equal bit for bit.
+
+Other cases: u = 2^-24. The kernel sums x (16 + c) and x over a group (G terms each, a
+matrix instruction may truncate: 2u a step), subtracts (16 + z) times the second,
+scales, and adds K / G groups, at most 8 wavefronts' sums and the residual: an
+error below 2 u (G + K / G + 16) sum_k |s| |x| (32 + c + z), and a stored
+bfloat16's half step."""
+import pytest
+import torch
+
+from gated_delta_rule_02_amd import kda as K
+from tests.gpu_util import announce
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F = torch.bfloat16, torch.float32
+
+
+def weight(N, k, G, sd, zeros, seed, whole=False):
+    """codes [N, k/2], scales, zeros (or None) on the GPU with padded rows, and W, |s| (32 + c + z) in 64 bits."""
+    g = torch.Generator().manual_seed(seed)
+    codes = torch.randint(0, 256, (N, k // 2 + 4), generator=g, dtype=torch.uint8)
+    if whole:
+        scales = 2.0 ** torch.randint(-1, 2, (N, k // G + 1), generator=g).float()
+    else:
+        scales = (torch.rand((N, k // G + 1), generator=g) + 0.5) * 0.02
+    scales = scales.to(sd)
+    z = torch.randint(0, 16, (N, k // G + 3), generator=g, dtype=torch.uint8) if zeros else None
+    c = torch.stack([codes[:, :k // 2] % 16, codes[:, :k // 2] // 16], -1).reshape(N, k).double()
+    s = scales[:, :k // G].double().repeat_interleave(G, 1)
+    zz = z[:, :k // G].double().repeat_interleave(G, 1) if zeros else torch.full_like(c, 8)
+    dev = (codes.cuda()[:, :k // 2], scales.cuda()[:, :k // G], z.cuda()[:, :k // G] if zeros else None)
+    return dev, s * (c - zz), s.abs() * (32 + c + zz)
+
+
+def packed(dev):
+    codes, scales, zeros = dev
+    # a padded scales row has as many columns as groups: the group follows from the shapes
+    return K.kda_w4_pack(codes, scales, zeros)
+
+
+# (M, N, K, group, scale type, zero points, y, residual, padding of x's rows)
+CASES = [
+    (1, 16, 128, 128, BF, False, F, None, 0), (1, 1, 32, 32, F, True, F, None, 0), (1, 4096, 8192, 128, BF, False, BF, BF, 0),
+    (2, 17, 96, 32, BF, True, BF, F, 8), (5, 4999, 4128, 32, F, True, F, None, 0), (15, 33, 192, 64, F, False, F, F, 16),
+    (16, 130, 1024, 64, BF, True, F, BF, 0), (17, 257, 4160, 64, BF, True, BF, None, 8), (31, 48, 256, 128, F, True, F, None, 0),
+    (32, 1001, 2048, 128, BF, False, F, F, 0), (33, 64, 160, 32, BF, False, BF, BF, 24), (63, 515, 8160, 32, F, True, F, None, 0),
+    (64, 100, 384, 128, BF, True, F, F, 8), (65, 31, 640, 128, F, False, F, None, 0), (200, 79, 448, 64, BF, True, BF, F, 0),
+]
+
+
+@pytest.mark.parametrize("whole", [True, False])
+@pytest.mark.parametrize("M,N,k,G,sd,zeros,yd,rd,pad", CASES)
+def test_gemm_w4(M, N, k, G, sd, zeros, yd, rd, pad, whole):
+    announce("gemm_w4 %s" % ((M, N, k, G, sd, zeros, yd, rd, pad, whole),))
+    dev, W, bound = weight(N, k, G, sd, zeros, M + N + k, whole)
+    g = torch.Generator().manual_seed(M * 7 + k)
+    if whole:  # at most 8192 * 2 * 31 * 2 / (1 / 2) < 2^21
+        x = torch.randint(-2, 3, (M, k + pad), generator=g).to(BF)
+        res = torch.randint(-9, 10, (M, N + 5), generator=g).to(rd) if rd else None
+    else:
+        x = torch.randn((M, k + pad), generator=g).to(BF)
+        res = torch.randn((M, N + 5), generator=g).to(rd) if rd else None
+    xc = x.cuda()[:, :k]
+    w = packed(dev)
+    assert (w.N, w.K, w.group) == (N, k, G)
+    y = torch.full((M, N + 3), float("nan"), dtype=yd, device="cuda")
+    rc = None if res is None else res.cuda()[:, :N]
+    out = K.kda_gemm_w4(xc, w, y[:, :N], residual=rc)
+    torch.cuda.synchronize()
+    assert out.data_ptr() == y.data_ptr() and torch.isnan(y[:, N:]).all()
+    xr = x[:, :k].double()
+    ref = xr @ W.t() + (0 if res is None else res[:, :N].double())
+    got = y[:, :N].double().cpu()
+    if whole:
+        assert torch.equal(got, ref.to(yd).double())
+    else:
+        tol = 2 * U * (G + k / G + 16) * (xr.abs() @ bound.t()) + (ref.abs() * 2.0 ** -8 if yd == BF else 0)
+        print("  worst %.2e of the bound" % float(((got - ref).abs() / tol).max()), flush=True)
+        assert ((got - ref).abs() <= tol).all()
+    if rd is not None:  # in place: the same bits as from a residual of y's type
+        a = rc.to(yd).clone()
+        b = torch.empty((M, N), dtype=yd, device="cuda")
+        K.kda_gemm_w4(xc, w, b, residual=a)
+        K.kda_gemm_w4(xc, w, a, residual=a)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N,k,G,sd,zeros", [(16, 128, 128, F, False), (5, 32, 32, BF, True), (130, 4160, 64, F, True),
+                                            (1000, 224, 32, BF, False)])
+def test_expand(N, k, G, sd, zeros):
+    """Two roundings: the product to float32, then to bfloat16 (2^-8 and 2^-24 of the value)."""
+    announce("w4_expand %s" % ((N, k, G, sd, zeros),))
+    dev, W, _ = weight(N, k, G, sd, zeros, N + k)
+    out = torch.full((N, k + 8), float("nan"), dtype=BF, device="cuda")
+    K.kda_w4_expand(packed(dev), out[:, :k])
+    torch.cuda.synchronize()
+    assert torch.isnan(out[:, k:]).all()
+    got = out[:, :k].double().cpu()
+    assert ((got - W).abs() <= W.abs() * (2.0 ** -8 + 2.0 ** -23)).all()
+
+
+def test_more_rows_than_a_slab_agree_with_single_rows():
+    """The rows of a large call equal those of calls of one row, but for the order of the sums."""
+    dev, W, bound = weight(300, 1024, 64, BF, True, 5)
+    w = packed(dev)
+    x = torch.randn((150, 1024), generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    y = torch.empty((150, 300), device="cuda")
+    K.kda_gemm_w4(x, w, y)
+    one = torch.empty((1, 300), device="cuda")
+    for m in (0, 15, 16, 63, 64, 149):
+        K.kda_gemm_w4(x[m:m + 1], w, one)
+        tol = 4 * U * (64 + 16 + 16) * (x[m:m + 1].double().cpu().abs() @ bound.t())
+        assert ((one.double() - y[m:m + 1].double()).abs().cpu() <= tol).all(), m
+
+
+def test_non_finite_rows_stay_in_their_rows():
+    dev, W, _ = weight(50, 256, 128, F, False, 9)
+    w = packed(dev)
+    x = torch.randn((20, 256), generator=torch.Generator().manual_seed(2)).to(BF).cuda()
+    clean = torch.empty((20, 50), device="cuda")
+    K.kda_gemm_w4(x, w, clean)
+    x[3, 7] = float("nan")
+    x[18, 200] = float("inf")
+    y = torch.empty((20, 50), device="cuda")
+    K.kda_gemm_w4(x, w, y)
+    bad = torch.tensor([3, 18], device="cuda")
+    keep = torch.tensor([m for m in range(20) if m not in (3, 18)], device="cuda")
+    assert torch.isnan(y[bad]).all() and torch.equal(y[keep], clean[keep])
+
+
+def test_empty_and_repeated():
+    dev, _, _ = weight(40, 128, 64, F, True, 4)
+    w = packed(dev)
+    y = torch.full((0, 40), 1.0, device="cuda")
+    K.kda_gemm_w4(torch.empty((0, 128), dtype=BF, device="cuda"), w, y)
+    x = torch.randn((9, 128), generator=torch.Generator().manual_seed(3)).to(BF).cuda()
+    a, b = torch.empty((9, 40), device="cuda"), torch.empty((9, 40), device="cuda")
+    K.kda_gemm_w4(x, w, a)
+    K.kda_gemm_w4(x, w, b)
+    assert torch.equal(a, b)
