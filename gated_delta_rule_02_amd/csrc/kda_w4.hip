@@ -11,15 +11,14 @@
 // which is lane l's operand of a 16x16x32 matrix instruction. So a wavefront's
 // load is one contiguous KiB whatever G is. The codes of an even j sit in nibble
 // j / 2, of an odd one in nibble 4 + j / 2: shifted and masked, each pair falls into
-// the two halves of a register as two bfloat16 numbers.
+// the two halves of a register as two bfloat16 numbers. Scales and zero points are
+// dealt per tile too, [row][group of the tile].
 //
 // A code becomes the number 16 + c, exact in bfloat16 with c in the upper
 // four bits of its mantissa: one shift and one and-or for two weights, and no
-// conversion. The group's sum is then put right in float32,
-//   sum_k x (c - z) = sum_k x (16 + c) - (16 + z) sum_k x,
-// with sum_k x from the same instruction with ones in place of the weights, in
-// the layout of the accumulator. The terms are at most three times as large as
-// x (c - z)'s own, so the float32 sums lose less than two bits to it.
+// conversion. Adding -(16 + z) x, another product on the matrix instruction, into
+// the same float32 accumulators leaves the group's sum of x (c - z). The terms are at
+// most three times as large as x (c - z)'s own, so the sums lose less than two bits.
 //
 // Bound by HBM: N K / 2 bytes of codes for up to about a hundred rows of x.
 #include "kda_device.h"
@@ -32,17 +31,16 @@ constexpr int kTileRows = 16, kTileCols = 128;
 
 // where the parts of a packed weight lie
 struct W4Layout {
-    int64_t row_tiles, col_tiles, groups;  // groups of one row, the padding's included
-    int64_t scales, zeros, bytes;          // offsets (the codes are at 0), total
+    int64_t row_tiles, col_tiles;
+    int64_t scales, zeros, bytes;  // offsets (the codes are at 0), total
 };
 __host__ __device__ inline W4Layout w4_layout(int64_t N, int64_t K, int G, DType scale_dtype, bool has_zeros)
 {
     W4Layout l;
     l.row_tiles = (N + kTileRows - 1) / kTileRows;
     l.col_tiles = (K + kTileCols - 1) / kTileCols;
-    l.groups = l.col_tiles * (kTileCols / G);
     l.scales = l.row_tiles * l.col_tiles * 1024;
-    const int64_t n = l.row_tiles * l.groups * kTileRows;
+    const int64_t n = l.row_tiles * l.col_tiles * (kTileRows * kTileCols / G);
     l.zeros = l.scales + n * (scale_dtype == F32 ? 4 : 2);
     l.bytes = has_zeros ? l.zeros + n : l.zeros;
     return l;
@@ -64,7 +62,8 @@ __device__ __forceinline__ bf16x8 w4_operand(uint32_t w)
 __global__ __launch_bounds__(256) void w4_pack_kernel(W4PackArgs a, W4Layout l)
 {
     const int64_t words = l.row_tiles * l.col_tiles * 256;
-    const int64_t n_scales = l.row_tiles * l.groups * kTileRows;
+    const int gpt = kTileCols / a.group;
+    const int64_t n_scales = l.row_tiles * l.col_tiles * kTileRows * gpt;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) {
         const int step = i & 3, lane = (i >> 2) & 63;
         const int64_t tile = i >> 8, n = tile / l.col_tiles * kTileRows + lane % 16;
@@ -78,7 +77,8 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(W4PackArgs a, W4Layout l)
         reinterpret_cast<uint32_t*>(a.packed)[i] = w;
     }
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_scales; i += (int64_t)gridDim.x * 256) {
-        const int64_t tg = i / kTileRows, n = tg / l.groups * kTileRows + i % kTileRows, g = tg % l.groups;
+        const int64_t tile = i / (kTileRows * gpt), n = tile / l.col_tiles * kTileRows + i / gpt % kTileRows;
+        const int64_t g = tile % l.col_tiles * gpt + i % gpt;
         const bool in = n < a.N && g < a.K / a.group;
         if (a.scale_dtype == F32)
             reinterpret_cast<float*>(a.packed + l.scales)[i] = in ? static_cast<const float*>(a.scales)[n * a.scales_ld + g] : 0.0f;
@@ -103,7 +103,7 @@ __global__ __launch_bounds__(256) void w4_expand_kernel(W4ExpandArgs a, W4Layout
         for (int i = 0; i < 4; ++i) {
             const int64_t k = kc * kTileCols + i * 32 + lane / 16 * 8;
             if (k >= a.K) break;
-            const int64_t at = (nt * l.groups + k / a.group) * kTileRows + lane % 16;
+            const int64_t at = (tile * kTileRows + lane % 16) * (kTileCols / a.group) + i * 32 / a.group;
             const float s = ld(reinterpret_cast<const TS*>(a.packed + l.scales) + at);
             const float z = ZEROS ? (float)a.packed[l.zeros + at] : 8.0f;
             float w[8];
@@ -115,74 +115,122 @@ __global__ __launch_bounds__(256) void w4_expand_kernel(W4ExpandArgs a, W4Layout
 }
 
 // ---------------------------------------------------------------- product
-// A workgroup takes NT row tiles of W and MT tiles of 16 rows of x; its
-// wavefronts deal the column tiles among themselves and their sums are joined in
-// LDS in a fixed order.
-template <int MT, int NT, int G, typename TS, bool ZEROS>
+// -(16 + z) twice, as bfloat16
+__device__ __forceinline__ uint32_t w4_zero_pair(uint32_t z) { return z * 0x00080008u + 0xc180c180u; }
+
+// What a lane reads of the scales or zero points of a tile: ROWS rows of GPT groups
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(rsrc_t r, uint32_t off, uint32_t* w)
+{
+    if constexpr (BYTES == 1) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0);
+    } else if constexpr (BYTES == 2) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    } else if constexpr (BYTES == 4) {
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0);
+    } else if constexpr (BYTES == 8) {
+        typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+        const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i) {
+            const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, off + i * 16, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i * 4 + j] = v[j];
+        }
+    }
+}
+template <typename TS>
+__device__ __forceinline__ float scale_at(const uint32_t* w, int i)
+{
+    if constexpr (sizeof(TS) == 4) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+}
+
+constexpr uint32_t kNowhere = 0x40000000u;  // an offset beyond every buffer here: reads zero
+
+// A workgroup takes NT row tiles of W and MT tiles of 16 rows of x; its wavefronts
+// deal the column tiles among themselves in runs of DEPTH, whose loads all go out
+// before the first is used, and their sums are joined in LDS in a fixed order.
+// Tiles beyond the last read as zero codes with zero scales.
+template <int MT, int NT, int DEPTH, int G, typename TS, bool ZEROS>
 __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
 {
     extern __shared__ f32x4 part[];  // [wavefront][NT * MT][lane]
     constexpr int STEPS = G / 32;    // matrix instructions per group
     constexpr int GPT = kTileCols / G;
+    constexpr int SB = 4 * GPT * sizeof(TS);  // a lane's scales: the four rows of its results
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int col = lane % 16, quad = lane / 16;
     const int64_t nt0 = (int64_t)blockIdx.x * NT, m0 = (int64_t)blockIdx.y * (MT * 16);
-    const uint8_t* w = a.packed + lane * 16;
+    const int K = (int)a.K, col_tiles = (int)l.col_tiles;
     const rsrc_t xr = make_rsrc(static_cast<const bf16_t*>(a.x) + m0 * a.x_ld,
                                 ((min(a.M - m0, (int64_t)MT * 16) - 1) * a.x_ld + a.K) * 2);
+    rsrc_t wr[NT], sr[NT], zr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int64_t at = min(nt0 + n, l.row_tiles - 1) * l.col_tiles;
+        wr[n] = make_rsrc(a.packed + at * 1024, l.col_tiles * 1024);
+        sr[n] = make_rsrc(a.packed + l.scales + at * (16 * GPT * sizeof(TS)), l.col_tiles * (16 * GPT * sizeof(TS)));
+        if constexpr (ZEROS) zr[n] = make_rsrc(a.packed + l.zeros + at * (16 * GPT), l.col_tiles * (16 * GPT));
+    }
     uint32_t xoff[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-        xoff[t] = m0 + t * 16 + col < a.M ? (uint32_t)(((t * 16 + col) * a.x_ld + quad * 8) * 2) : 0x80000000u;
-    const u32x4_t one4 = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-    const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
+        xoff[t] = m0 + t * 16 + col < a.M ? (uint32_t)(((t * 16 + col) * a.x_ld + quad * 8) * 2) : kNowhere;
 
     f32x4 tot[NT][MT] = {};
-    for (int64_t kc = wave; kc < l.col_tiles; kc += waves) {
-        u32x4_t c[NT];
+    for (int run = wave * DEPTH; run < col_tiles; run += waves * DEPTH) {
+        u32x4_t c[DEPTH][NT];
+        uint32_t sw[DEPTH][NT][SB / 4], zw[DEPTH][NT][GPT > 4 ? GPT / 4 : 1];
+        bf16x8 xf[DEPTH][4][MT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int64_t nt = min(nt0 + n, l.row_tiles - 1);
-            c[n] = ld16(w + (nt * l.col_tiles + kc) * 1024);
-        }
+        for (int d = 0; d < DEPTH; ++d) {
+            const int kc = run + d;
 #pragma unroll
-        for (int g = 0; g < GPT; ++g) {
-            f32x4 acc[NT][MT] = {}, xs[MT] = {};
-#pragma unroll
-            for (int st = 0; st < STEPS; ++st) {
-                const int i = g * STEPS + st;
-                const uint32_t k2 = (uint32_t)(kc * kTileCols + i * 32) * 2;
-                const bool in = kc * kTileCols + i * 32 < a.K;  // K is a multiple of 32
-                bf16x8 xf[MT];
-#pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    // rows and columns that are not there: an offset beyond the buffer reads zero
-                    xf[t] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(xr, in ? xoff[t] + k2 : 0x80000000u, 0, 0));
-                    xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, xf[t], xs[t], 0, 0, 0);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const bf16x8 wf = w4_operand(c[n][i]);
-#pragma unroll
-                    for (int t = 0; t < MT; ++t) acc[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[t], acc[n][t], 0, 0, 0);
-                }
-            }
+            for (int n = 0; n < NT; ++n) c[d][n] = __builtin_amdgcn_raw_buffer_load_b128(wr[n], kc * 1024 + lane * 16, 0, 0);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int64_t nt = min(nt0 + n, l.row_tiles - 1);
-                const int64_t at = (nt * l.groups + kc * GPT + g) * kTileRows + quad * 4;
-                const f32x4 s = ld4(reinterpret_cast<const TS*>(a.packed + l.scales) + at);
-                uint32_t z4 = 0;
-                if constexpr (ZEROS) z4 = *reinterpret_cast<const uint32_t*>(a.packed + l.zeros + at);
+                load_bytes<SB>(sr[n], kc * (SB * 4) + quad * SB, sw[d][n]);
+                if constexpr (ZEROS) load_bytes<GPT>(zr[n], (kc * 16 + col) * GPT, zw[d][n]);
+            }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float z = ZEROS ? -16.0f - (float)((z4 >> (8 * r)) & 255u) : -24.0f;
+            for (int i = 0; i < 4; ++i) {
+                const int k = kc * kTileCols + i * 32;
+                const uint32_t k2 = k < K ? (uint32_t)k * 2 : kNowhere;  // K is a multiple of 32
 #pragma unroll
-                    for (int t = 0; t < MT; ++t)
-                        tot[n][t][r] = fmaf(s[r], fmaf(z, xs[t][r], acc[n][t][r]), tot[n][t][r]);
-                }
+                for (int t = 0; t < MT; ++t)
+                    xf[d][i][t] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(xr, xoff[t] + k2, 0, 0));
             }
         }
+        __builtin_amdgcn_sched_barrier(0);  // (the compiler would put the loads of x off until they are used)
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+#pragma unroll
+            for (int g = 0; g < GPT; ++g)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 acc[MT] = {};
+                    const uint32_t zp = ZEROS ? w4_zero_pair((zw[d][n][0] >> (8 * g)) & 255u) : 0xc1c0c1c0u;
+                    const u32x4_t z4 = {zp, zp, zp, zp};
+                    const bf16x8 zf = __builtin_bit_cast(bf16x8, z4);
+#pragma unroll
+                    for (int i = g * STEPS; i < (g + 1) * STEPS; ++i) {
+                        const bf16x8 wf = w4_operand(c[d][n][i]);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[d][i][t], acc[t], 0, 0, 0);
+                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf, xf[d][i][t], acc[t], 0, 0, 0);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float s = scale_at<TS>(sw[d][n], r * GPT + g);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) tot[n][t][r] = fmaf(s, acc[t][r], tot[n][t][r]);
+                    }
+                }
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -210,23 +258,23 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
     }
 }
 
-template <int MT, int NT, int G, typename TS, bool ZEROS>
+template <int MT, int NT, int DEPTH, int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_tiles(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
     const int64_t blocks = (l.row_tiles + NT - 1) / NT;
     int waves = 4;
     while (waves < 8 && blocks * waves < 4096) waves *= 2;
     const dim3 grid((unsigned)blocks, (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
-    hipLaunchKernelGGL((w4_gemm_kernel<MT, NT, G, TS, ZEROS>), grid, dim3(waves * 64), waves * NT * MT * 1024, s, a, l);
+    hipLaunchKernelGGL((w4_gemm_kernel<MT, NT, DEPTH, G, TS, ZEROS>), grid, dim3(waves * 64), waves * NT * MT * 1024, s, a, l);
     return hipGetLastError();
 }
 
 template <int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_form(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
-    if (a.M <= 16) return launch_gemm_tiles<1, 1, G, TS, ZEROS>(a, l, s);
-    if (a.M <= 32) return launch_gemm_tiles<2, 2, G, TS, ZEROS>(a, l, s);
-    return launch_gemm_tiles<4, 2, G, TS, ZEROS>(a, l, s);
+    if (a.M <= 16) return launch_gemm_tiles<1, 1, 4, G, TS, ZEROS>(a, l, s);
+    if (a.M <= 32) return launch_gemm_tiles<2, 2, 2, G, TS, ZEROS>(a, l, s);
+    return launch_gemm_tiles<4, 2, 1, G, TS, ZEROS>(a, l, s);
 }
 
 template <typename TS, bool ZEROS>
