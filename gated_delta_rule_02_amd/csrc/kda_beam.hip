@@ -36,8 +36,12 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// the value of the lane before (lane 0: undefined use)
-__device__ __forceinline__ uint32_t lane_before(uint32_t v) { return (uint32_t)__shfl_up((int)v, 1, 64); }
+// the value of the lane before (lane 0: 0), by the wavefront shift of the vector unit: a
+// list's shifts follow one another, and a shuffle through LDS takes many times as long
+__device__ __forceinline__ uint32_t lane_before(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x138, 0xf, 0xf, false);
+}
 
 __device__ __forceinline__ bool finite(float f) { return fabsf(f) < __builtin_inff(); }
 
@@ -52,7 +56,31 @@ struct BestList {
         if (lane > pos) key = pk, index = pi;
         if (lane == pos) key = k, index = i;
     }
+    // every lane's (k, i) with `in` set
+    __device__ __forceinline__ void put_lanes(bool in, uint32_t k, uint32_t i, int lane)
+    {
+        uint64_t todo = __ballot(in);
+        while (todo) {
+            const int from = __ffsll((unsigned long long)todo) - 1;
+            todo &= todo - 1;
+            put((uint32_t)__builtin_amdgcn_readlane((int)k, from), (uint32_t)__builtin_amdgcn_readlane((int)i, from), lane);
+        }
+    }
+    __device__ __forceinline__ uint32_t key_of(int place) const { return (uint32_t)__builtin_amdgcn_readlane((int)key, place); }
 };
+
+// a bound that at least n of the lanes' keys reach: the n-th largest, its lower 16 bits
+// cleared (1, below every key, if fewer lanes have a key)
+__device__ __forceinline__ uint32_t lower_bound_of(uint32_t k, int n)
+{
+    uint32_t bound = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t t = bound | (1u << bit);
+        if (__popcll(__ballot(k >= t)) >= n) bound = t;
+    }
+    return bound | (bound == 0);
+}
 
 // ---------------------------------------------------------------- first pass
 constexpr int kStep = 1024;  // logits of a wavefront's step: 16 a lane
@@ -88,17 +116,18 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamSelectArgs a)
     if (unit >= (int64_t)a.B * a.W * a.parts) return;
     const int64_t row_i = unit / a.parts;
     const int part = unit % a.parts;
-    // an ended or dead beam's logits decide nothing
-    if ((a.finished && a.finished[row_i]) || !finite(a.scores[row_i])) return;
     const T* row = static_cast<const T*>(a.logits) + row_i * a.ld;
     const int begin = part * a.part_len, end = min(begin + a.part_len, a.V);
+    float x[16];
+    load_step(row, begin, end, lane, x);
+    // an ended or dead beam's logits decide nothing
+    if ((a.finished && a.finished[row_i]) || !finite(a.scores[row_i])) return;
 
     float top = -3.402823466e38f, sum = 0.0f;  // finite, so that -inf - top is no NaN
     BestList best;
-    float last = __builtin_nanf("");  // the W-th best value (NaN: fewer than W so far)
+    uint32_t bound = 0;  // keys below it cannot be among the W best
     for (int at = begin; at < end; at += kStep) {
-        float x[16];
-        load_step(row, at, end, lane, x);
+        if (at != begin) load_step(row, at, end, lane, x);
         float here = x[0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) here = fmaxf(here, x[i]);
@@ -107,45 +136,18 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamSelectArgs a)
         top = m;
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum += exp2_fast((x[i] - m) * kLog2e);
-        if (at == begin) {
-            // a bound that at least W of the step's values reach (0 if it has fewer lanes' worth)
-            const uint32_t k = at + lane * VEC < end ? order_key(here) : 0;
-            uint32_t bound = 0;
+        const uint32_t k = at + lane * VEC < end ? order_key(here) : 0;
+        if (at == begin) bound = lower_bound_of(k, a.W);
+        if (!__ballot(k >= bound)) continue;
 #pragma unroll
-            for (int bit = 31; bit >= 16; --bit) {
-                const uint32_t t = bound | (1u << bit);
-                if (__popcll(__ballot(k >= t)) >= a.W) bound = t;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = at + (i / VEC * 64 + lane) * VEC + i % VEC;
-                const uint32_t ki = order_key(x[i]);
-                uint64_t todo = __ballot(e < end && ki >= bound);
-                while (todo) {
-                    const int from = __ffsll((unsigned long long)todo) - 1;
-                    todo &= todo - 1;
-                    best.put((uint32_t)__builtin_amdgcn_readlane((int)ki, from),
-                             (uint32_t)__builtin_amdgcn_readlane(e, from), lane);
-                }
-            }
-        } else if (__ballot(!(here <= last))) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = at + (i / VEC * 64 + lane) * VEC + i % VEC;
-                const uint32_t ki = order_key(x[i]);
-                uint64_t todo = __ballot(e < end && !(x[i] <= last));
-                while (todo) {
-                    const int from = __ffsll((unsigned long long)todo) - 1;
-                    todo &= todo - 1;
-                    best.put((uint32_t)__builtin_amdgcn_readlane((int)ki, from),
-                             (uint32_t)__builtin_amdgcn_readlane(e, from), lane);
-                }
-            }
-        } else {
-            continue;
+        for (int i = 0; i < 16; ++i) {
+            const int e = at + (i / VEC * 64 + lane) * VEC + i % VEC;
+            const uint32_t ki = order_key(x[i]);
+            best.put_lanes(e < end && ki >= bound, ki, (uint32_t)e, lane);
+            bound = max(bound, best.key_of(a.W - 1));  // (one as large may be of a lower token: in this step)
         }
-        const uint32_t lk = (uint32_t)__builtin_amdgcn_readlane((int)best.key, a.W - 1);
-        last = lk ? key_value(lk) : __builtin_nanf("");
+        const uint32_t last = best.key_of(a.W - 1);
+        if (last) bound = max(bound, last + 1);  // later ones have higher tokens
     }
     // join the lanes
     const float m = wave_max(top);
@@ -163,46 +165,54 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamSelectArgs a)
 }
 
 // ---------------------------------------------------------------- second pass
-// A workgroup per sequence: a wavefront per beam joins its parts' lists and sums
-// into W offers in 64 bits; then every offer counts the better ones.
-__global__ __launch_bounds__(256) void beam_join_kernel(BeamSelectArgs a)
+// A workgroup per sequence. A wavefront joins the parts of a beam: its sum, and of the
+// entries that reach the W-th largest of the parts' best the W first. Then
+// every offer finds its place: its own in its beam's list and, by bisection, how many
+// of every other beam's list come before it.
+constexpr int kMaxW = 32;
+
+__global__ __launch_bounds__(1024) void beam_join_kernel(BeamSelectArgs a)
 {
-    __shared__ double value[32 * 32];
-    __shared__ uint32_t token[32 * 32];
-    __shared__ uint8_t ended[32];
-    const int lane = threadIdx.x & 63, W = a.W;
+    __shared__ double value[kMaxW][kMaxW];
+    __shared__ uint32_t token[kMaxW][kMaxW];
+    __shared__ uint8_t ended[kMaxW];
+    const int lane = threadIdx.x & 63, W = a.W, entries = a.parts * W;
     const int64_t b = blockIdx.x;
     const double none = -__builtin_inf();
-    for (int w = threadIdx.x >> 6; w < W; w += 4) {
+    for (int w = threadIdx.x >> 6; w < W; w += blockDim.x >> 6) {
         const int64_t row = b * W + w;
+        const uint32_t *keys = a.part_key + row * entries, *tokens = a.part_token + row * entries;
+        // lane p: part p (what an ended or dead beam's parts hold is not used)
+        const bool on = lane < a.parts;
+        const float top = on ? a.part_top[row * a.parts + lane] : -3.402823466e38f;
+        const double sum = on ? a.part_sum[row * a.parts + lane] : 0.0;
+        const uint32_t head = on ? keys[lane * W] : 0;
         const bool done = a.finished && a.finished[row];
         const float score = a.scores[row];
         const bool dead = !finite(score);
         double v = none;
         uint32_t t = lane;  // a dead beam offers its first tokens, at -inf
         if (!done && !dead) {
-            // lane p: part p
-            const bool on = lane < a.parts;
-            const float top = on ? a.part_top[row * a.parts + lane] : -3.402823466e38f;
             const float m = wave_max(top);
-            double s = on ? a.part_sum[row * a.parts + lane] * exp((double)top - (double)m) : 0.0;
+            double s = sum * exp((double)top - (double)m);
 #pragma unroll
             for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
             if (s > 0.0 && s < __builtin_inf()) {  // not so if no logit is finite, or one is +inf or NaN: dead
                 BestList best;
-                uint32_t last = 0;
-                for (int64_t e = 0; e < (int64_t)a.parts * W; e += 64) {
-                    const bool in = e + lane < (int64_t)a.parts * W;
-                    const uint32_t k = in ? a.part_key[row * a.parts * W + e + lane] : 0;
-                    const uint32_t i = in ? a.part_token[row * a.parts * W + e + lane] : 0xffffffffu;
-                    uint64_t todo = __ballot(in && k != 0 && k >= last);
-                    while (todo) {
-                        const int from = __ffsll((unsigned long long)todo) - 1;
-                        todo &= todo - 1;
-                        best.put((uint32_t)__builtin_amdgcn_readlane((int)k, from),
-                                 (uint32_t)__builtin_amdgcn_readlane((int)i, from), lane);
+                uint32_t bound = lower_bound_of(head, W);
+                for (int e = 0; e < entries; e += 256) {
+                    uint32_t k[4], i[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = e + j * 64 + lane;
+                        k[j] = at < entries ? keys[at] : 0;
+                        i[j] = at < entries ? tokens[at] : 0;
                     }
-                    last = (uint32_t)__builtin_amdgcn_readlane((int)best.key, W - 1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        best.put_lanes(k[j] >= bound, k[j], i[j], lane);
+                        bound = max(bound, best.key_of(W - 1));
+                    }
                 }
                 t = best.index;
                 if (best.key) v = (double)score + ((double)key_value(best.key) - (double)m - log(s));
@@ -213,31 +223,36 @@ __global__ __launch_bounds__(256) void beam_join_kernel(BeamSelectArgs a)
             else t = lane - 1 < a.eos ? lane - 1 : lane;
         }
         if (lane < W) {
-            value[w * W + lane] = v;
-            token[w * W + lane] = t;
+            value[w][lane] = v;
+            token[w][lane] = t;
         }
         if (lane == 0) ended[w] = done;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < W * W; i += 256) {
-        const double v = value[i];
-        const uint32_t t = token[i];
-        const int w = i / W;
-        if (t >= (uint32_t)a.V) continue;  // fewer tokens than beams
-        int before = 0;
-        for (int j = 0; j < W * W; ++j) {
-            const double vj = value[j];
-            const uint32_t tj = token[j];
-            const int wj = j / W;
-            const bool better = vj > v || (vj == v && (wj < w || (wj == w && tj < t)));
-            before += better && tj < (uint32_t)a.V;
+    const int n = min(W, a.V);  // offers of a beam
+    for (int i = threadIdx.x; i < W * n; i += blockDim.x) {
+        const int w = i / n, j = i % n;
+        const double v = value[w][j];
+        int place = j;
+        for (int u = 0; u < W && place < W; ++u) {
+            if (u == w) continue;
+            // the entries of beam u before this one: larger, or equal and of a lower beam
+            int lo = 0, hi = n;
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                const double o = value[u][mid];
+                if (o > v || (o == v && u < w)) lo = mid + 1;
+                else hi = mid;
+            }
+            place += lo;
         }
-        if (before < W) {
-            const int64_t o = b * W + before;
+        if (place < W) {
+            const int64_t o = b * W + place;
+            const int32_t t = (int32_t)token[w][j];
             a.next_scores[o] = (float)v;
             a.parents[o] = w;
-            a.tokens[o] = (int32_t)t;
-            if (a.next_finished) a.next_finished[o] = ended[w] || (int)t == a.eos;
+            a.tokens[o] = t;
+            if (a.next_finished) a.next_finished[o] = ended[w] || t == a.eos;
         }
     }
 }
@@ -303,7 +318,7 @@ hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s)
     const dim3 grid((unsigned)((units + 3) / 4));
     if (a.dtype == F32) hipLaunchKernelGGL((beam_part_kernel<float>), grid, dim3(256), 0, s, a);
     else hipLaunchKernelGGL((beam_part_kernel<bf16_t>), grid, dim3(256), 0, s, a);
-    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)a.B), dim3(64 * std::min(a.W, 16)), 0, s, a);
     return hipGetLastError();
 }
 
