@@ -27,6 +27,8 @@
 namespace kda {
 namespace {
 
+typedef __attribute__((address_space(3))) void lds_void;
+
 constexpr int kTileRows = 16, kTileCols = 128;
 
 // where the parts of a packed weight lie
@@ -46,17 +48,22 @@ __host__ __device__ inline W4Layout w4_layout(int64_t N, int64_t K, int G, DType
     return l;
 }
 
-// bfloat16 pairs 16 + c from a packed word: operand register p of 4
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int p)
-{
-    const uint32_t t = p == 0 ? w << 3 : w >> (4 * p - 3);
-    return (t & 0x00780078u) | 0x41804180u;
-}
-__device__ __forceinline__ bf16x8 w4_operand(uint32_t w)
-{
-    const u32x4_t r = {w4_pair(w, 0), w4_pair(w, 1), w4_pair(w, 2), w4_pair(w, 3)};
-    return __builtin_bit_cast(bf16x8, r);
-}
+// bfloat16 pairs 16 + c from a packed word. The two constants are in registers, and the
+// compiler kept from knowing them: it would take an and and an or with a constant each
+// in place of one and-or.
+struct W4Unpack {
+    uint32_t mask, bias;
+    __device__ __forceinline__ W4Unpack()
+    {
+        asm("s_mov_b32 %0, 0x00780078" : "=s"(mask));
+        asm("v_mov_b32 %0, 0x41804180" : "=v"(bias));
+    }
+    __device__ __forceinline__ bf16x8 operator()(uint32_t w) const
+    {
+        const u32x4_t r = {((w << 3) & mask) | bias, ((w >> 1) & mask) | bias, ((w >> 5) & mask) | bias, ((w >> 9) & mask) | bias};
+        return __builtin_bit_cast(bf16x8, r);
+    }
+};
 
 // ---------------------------------------------------------------- packing
 __global__ __launch_bounds__(256) void w4_pack_kernel(W4PackArgs a, W4Layout l)
@@ -150,6 +157,32 @@ __device__ __forceinline__ float scale_at(const uint32_t* w, int i)
 
 constexpr uint32_t kNowhere = 0x40000000u;  // an offset beyond every buffer here: reads zero
 
+// v + residual -> columns n .. n + 3 of row m of y
+__device__ __forceinline__ void store4(const W4GemmArgs& a, int64_t m, int64_t n, f32x4 v)
+{
+    if (m >= a.M) return;
+    if (n + 4 <= a.N && (a.y_ld | a.res_ld) % 4 == 0) {  // (res_ld is 0 without a residual)
+        if (a.res) {
+            const f32x4 r = a.res_dtype == F32 ? ld4(static_cast<const float*>(a.res) + m * a.res_ld + n)
+                                               : ld4(static_cast<const bf16_t*>(a.res) + m * a.res_ld + n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += r[i];
+        }
+        if (a.y_dtype == F32) st4(static_cast<float*>(a.y) + m * a.y_ld + n, v);
+        else st4(static_cast<bf16_t*>(a.y) + m * a.y_ld + n, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (n + i >= a.N) break;
+        float f = v[i];
+        if (a.res) f += a.res_dtype == F32 ? static_cast<const float*>(a.res)[m * a.res_ld + n + i]
+                                           : bf16_to_f32(static_cast<const bf16_t*>(a.res)[m * a.res_ld + n + i]);
+        if (a.y_dtype == F32) static_cast<float*>(a.y)[m * a.y_ld + n + i] = f;
+        else static_cast<bf16_t*>(a.y)[m * a.y_ld + n + i] = f32_to_bf16(f);
+    }
+}
+
 // A workgroup takes NT row tiles of W and MT tiles of 16 rows of x; its wavefronts
 // deal the column tiles among themselves in runs of DEPTH, whose loads all go out
 // before the first is used, and their sums are joined in LDS in a fixed order.
@@ -180,6 +213,7 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
     for (int t = 0; t < MT; ++t)
         xoff[t] = m0 + t * 16 + col < a.M ? (uint32_t)(((t * 16 + col) * a.x_ld + quad * 8) * 2) : kNowhere;
 
+    const W4Unpack unpack;
     f32x4 tot[NT][MT] = {};
     for (int run = wave * DEPTH; run < col_tiles; run += waves * DEPTH) {
         u32x4_t c[DEPTH][NT];
@@ -217,7 +251,7 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
                     const bf16x8 zf = __builtin_bit_cast(bf16x8, z4);
 #pragma unroll
                     for (int i = g * STEPS; i < (g + 1) * STEPS; ++i) {
-                        const bf16x8 wf = w4_operand(c[d][n][i]);
+                        const bf16x8 wf = unpack(c[d][n][i]);
 #pragma unroll
                         for (int t = 0; t < MT; ++t) {
                             acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[d][i][t], acc[t], 0, 0, 0);
@@ -244,37 +278,227 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[r] += o[r];
         }
-        const int64_t n = (nt0 + i / MT) * kTileRows + quad * 4, m = m0 + i % MT * 16 + col;
-        if (m >= a.M) continue;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (n + r >= a.N) break;
-            float f = v[r];
-            if (a.res) f += a.res_dtype == F32 ? static_cast<const float*>(a.res)[m * a.res_ld + n + r]
-                                               : bf16_to_f32(static_cast<const bf16_t*>(a.res)[m * a.res_ld + n + r]);
-            if (a.y_dtype == F32) static_cast<float*>(a.y)[m * a.y_ld + n + r] = f;
-            else static_cast<bf16_t*>(a.y)[m * a.y_ld + n + r] = f32_to_bf16(f);
-        }
+        store4(a, m0 + i % MT * 16 + col, (nt0 + i / MT) * kTileRows + quad * 4, v);
     }
+}
+
+// More rows of x: what a compute unit takes in of x counts as much as the weights.
+// Four wavefronts with NT row tiles of W each share the x of a column tile in LDS,
+// copied there in the operands' order; two such groups take turns at the column
+// tiles. Copies and weights run two turns ahead. A group's sum of -24 x is formed once for
+// the NT tiles and their products start from it; with zero points the sum of x is, and
+// they are applied to it in float32.
+template <int MT, int NT, int G, typename TS, bool ZEROS>
+__global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
+{
+    constexpr int RW = 4, KW = 2, S = 3, kStage = MT * 4096;
+    constexpr int STEPS = G / 32, GPT = kTileCols / G, SB = 4 * GPT * sizeof(TS), ZB = 4 * GPT;
+    // loads of a wavefront per column tile
+    constexpr int kLoads = MT + NT * (1 + (SB + 15) / 16 + (ZEROS ? 1 : 0));
+    static_assert(RW * NT * MT * 1024 <= KW * S * kStage, "the partial sums fit the stages");
+    static_assert(kLoads < 64, "loads the wait can count");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[KW * S * kStage];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = wave % RW, kg = wave / RW, col = lane % 16, quad = lane / 16;
+    const int64_t nt0 = ((int64_t)blockIdx.x * RW + rw) * NT, m0 = (int64_t)blockIdx.y * (MT * 16);
+    const int K = (int)a.K, turns = ((int)l.col_tiles + KW - 1) / KW;
+    const rsrc_t xr = make_rsrc(static_cast<const bf16_t*>(a.x) + m0 * a.x_ld,
+                                ((min(a.M - m0, (int64_t)MT * 16) - 1) * a.x_ld + a.K) * 2);
+    rsrc_t wr[NT], sr[NT], zr[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int64_t at = min(nt0 + n, l.row_tiles - 1) * l.col_tiles;
+        wr[n] = make_rsrc(a.packed + at * 1024, l.col_tiles * 1024);
+        sr[n] = make_rsrc(a.packed + l.scales + at * (16 * GPT * sizeof(TS)), l.col_tiles * (16 * GPT * sizeof(TS)));
+        if constexpr (ZEROS) zr[n] = make_rsrc(a.packed + l.zeros + at * (16 * GPT), l.col_tiles * (16 * GPT));
+    }
+    // this wavefront copies step rw of the column tile for every tile of rows
+    uint32_t xoff[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+        xoff[t] = m0 + t * 16 + col < a.M ? (uint32_t)(((t * 16 + col) * a.x_ld + quad * 8) * 2) : kNowhere;
+    uint8_t* ring = smem + kg * (S * kStage);
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)ring;
+
+    u32x4_t c[S][NT];
+    uint32_t sw[S][NT][SB / 4], zw[S][NT][ZB / 4];
+    // part p of MT + NT of a column tile's loads
+    auto load = [&](int turn, int st, int p) {
+        const int kc = turn * KW + kg, k = kc * kTileCols + rw * 32;
+        if (p < MT) {
+            const uint32_t k2 = k < K ? (uint32_t)k * 2 : kNowhere;  // K is a multiple of 32
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(uintptr_t)(lds0 + st * kStage + (rw * MT + p) * 1024), 16,
+                                                     (int)(xoff[p] + k2), 0, 0, 0);
+        } else {
+            const int n = p - MT;
+            c[st][n] = __builtin_amdgcn_raw_buffer_load_b128(wr[n], kc * 1024 + lane * 16, 0, 0);
+            load_bytes<SB>(sr[n], kc * (SB * 4) + quad * SB, sw[st][n]);
+            if constexpr (ZEROS) load_bytes<ZB>(zr[n], kc * (ZB * 4) + quad * ZB, zw[st][n]);
+        }
+    };
+    constexpr uint32_t kShift = ZEROS ? 0x3f803f80u : 0xc1c0c1c0u;  // 1, or -24
+    const u32x4_t shift4 = {kShift, kShift, kShift, kShift};
+    const bf16x8 shift = __builtin_bit_cast(bf16x8, shift4);
+
+    f32x4 tot[NT][MT] = {};
+#pragma unroll
+    for (int p = 0; p < MT + NT; ++p) load(0, 0, p);
+#pragma unroll
+    for (int p = 0; p < MT + NT; ++p) load(1, 1, p);
+    // (so that the compiler has nothing left of these to wait for within the loop)
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    const W4Unpack unpack;
+    auto step = [&](int turn, int st, bool last) {
+        // this turn's copies have landed (those of the next may be under way)
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (last) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+        else __builtin_amdgcn_s_waitcnt(0x0f70 | (kLoads & 15) | ((kLoads >> 4) << 14));
+        lds_barrier();  // everyone's; and every read of the stage refilled now is done
+        __builtin_amdgcn_sched_barrier(0);
+        const uint8_t* lds = ring + st * kStage + lane * 16;
+#pragma unroll
+        for (int g = 0; g < GPT; ++g) {
+            bf16x8 xf[STEPS][MT];
+            f32x4 xs[MT] = {};
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    xf[i][t] = __builtin_bit_cast(bf16x8, ld16(lds + ((g * STEPS + i) * MT + t) * 1024));
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) xs[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(shift, xf[i][t], xs[t], 0, 0, 0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                f32x4 acc[MT] = {};
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) {
+                    const bf16x8 wf = unpack(c[st][n][g * STEPS + i]);
+#pragma unroll
+                    for (int t = 0; t < MT; ++t)
+                        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[i][t], !ZEROS && i == 0 ? xs[t] : acc[t], 0, 0, 0);
+                    // The loads of the turn after the next, spread over this one's products: issued in
+                    // one go they hold a wavefront up for as long as its products take. (Beyond the last
+                    // column tile too, where they read nothing: loads on a condition would make
+                    // the compiler wait for all of them before it uses any.)
+                    const int done = (g * NT + n) * STEPS + i;
+#pragma unroll
+                    for (int p = done * (MT + NT) / (4 * NT); p < (done + 1) * (MT + NT) / (4 * NT); ++p) {
+                        if (last) break;
+                        load(turn + 2, (st + 2) % S, p);
+                        __builtin_amdgcn_sched_barrier(0x38f);  // (what is no memory access may cross)
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = r * GPT + g;
+                    const float s = scale_at<TS>(sw[st][n], at);
+                    const float z = ZEROS ? -16.0f - (float)((zw[st][n][at / 4] >> (8 * (at % 4))) & 255u) : 0.0f;
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        if constexpr (ZEROS) tot[n][t][r] = fmaf(s, fmaf(z, xs[t][r], acc[t][r]), tot[n][t][r]);
+                        else tot[n][t][r] = fmaf(s, acc[t][r], tot[n][t][r]);
+                    }
+                }
+            }
+        }
+    };
+    int turn = 0;
+    for (; turn + S <= turns; turn += S) {
+        step(turn, 0, false);
+        step(turn + 1, 1, false);
+        step(turn + 2, 2, false);
+    }
+    if (turn < turns) step(turn, 0, true);  // (turn + 1 is loaded, and nothing is left to load)
+    if (turn + 1 < turns) step(turn + 1, 1, true);
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the copies beyond the last column tile
+    lds_barrier();                        // every wavefront has read its last stage
+    f32x4* part = reinterpret_cast<f32x4*>(smem) + rw * (NT * MT * 64) + lane;
+    if (kg == 1) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) part[(n * MT + t) * 64] = tot[n][t];
+    }
+    lds_barrier();
+    if (kg == 1) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const f32x4 o = part[(n * MT + t) * 64];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) tot[n][t][r] += o[r];
+            store4(a, m0 + t * 16 + col, (nt0 + n) * kTileRows + quad * 4, tot[n][t]);
+        }
 }
 
 template <int MT, int NT, int DEPTH, int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_tiles(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
     const int64_t blocks = (l.row_tiles + NT - 1) / NT;
-    int waves = 4;
-    while (waves < 8 && blocks * waves < 4096) waves *= 2;
+    const int waves = (int)min((l.col_tiles + DEPTH - 1) / DEPTH, (int64_t)8);
     const dim3 grid((unsigned)blocks, (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
     hipLaunchKernelGGL((w4_gemm_kernel<MT, NT, DEPTH, G, TS, ZEROS>), grid, dim3(waves * 64), waves * NT * MT * 1024, s, a, l);
     return hipGetLastError();
 }
 
+template <int MT, int NT, int G, typename TS, bool ZEROS>
+hipError_t launch_gemm_rows(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
+{
+    const dim3 grid((unsigned)((l.row_tiles + 4 * NT - 1) / (4 * NT)), (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
+    hipLaunchKernelGGL((w4_rows_kernel<MT, NT, G, TS, ZEROS>), grid, dim3(512), 0, s, a, l);
+    return hipGetLastError();
+}
+
+// The form: the least of `start + rounds (tile + steps step)` us, with rounds of workgroups
+// over the 256 compute units and steps of a tile, column tiles (w4_gemm_kernel: a part of
+// a step follows the rows of x that there are) or turns at two of them. Fitted to
+// every form's time at 130 sizes (M 1..64, N 500..41,024, K 64..8,192, all groups and
+// types): off by 7 to 15 per cent, and the form picked on average 1 per cent above the
+// best (always the first: 4 per cent up to 16 rows, 20 beyond; at worst 2.8 times).
+struct W4Form {
+    int rows, row_tiles;  // of x and of W, per workgroup
+    bool turns;
+    int least;  // rows of x below which a smaller form does the same
+    float start, tile, step, step_rows;
+    float cost(const W4GemmArgs& a, const W4Layout& l) const
+    {
+        const int64_t tiles = ((l.row_tiles + row_tiles - 1) / row_tiles) * ((a.M + rows - 1) / rows);
+        const int64_t steps = turns ? (l.col_tiles + 1) / 2 : l.col_tiles;
+        const float fill = (float)min(a.M, (int64_t)rows) / (float)rows;
+        return start + (float)((tiles + 255) / 256) * (tile + (float)steps * (step + step_rows * fill));
+    }
+};
+constexpr W4Form kForms[] = {
+    {16, 1, false, 0, 2.8f, 0.07f, 0.064f, 0.060f}, {32, 2, false, 17, 3.2f, 0.35f, 0.135f, 0.121f},
+    {16, 4, true, 0, 2.7f, 0.49f, 0.393f, 0.0f},    {32, 4, true, 17, 2.9f, 0.50f, 0.545f, 0.0f},
+    {32, 8, true, 17, 3.5f, 0.60f, 0.863f, 0.0f},   {32, 12, true, 17, 2.4f, 2.4f, 1.173f, 0.0f},
+    {64, 12, true, 33, 3.3f, 3.3f, 1.668f, 0.0f},
+};
+
 template <int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_form(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
-    if (a.M <= 16) return launch_gemm_tiles<1, 1, 4, G, TS, ZEROS>(a, l, s);
-    if (a.M <= 32) return launch_gemm_tiles<2, 2, 2, G, TS, ZEROS>(a, l, s);
-    return launch_gemm_tiles<4, 2, 1, G, TS, ZEROS>(a, l, s);
+    int best = 0;
+    float least = kForms[0].cost(a, l);
+    for (int f = 1; f < 7; ++f) {
+        const float c = kForms[f].cost(a, l);
+        if (a.M >= kForms[f].least && c < least) best = f, least = c;
+    }
+    // (float32 scales of groups of 32 take too many registers beside three tiles)
+    constexpr int THREE = G == 32 && sizeof(TS) == 4 ? 2 : 3;
+    switch (best) {
+    case 0: return launch_gemm_tiles<1, 1, 2, G, TS, ZEROS>(a, l, s);
+    case 1: return launch_gemm_tiles<2, 2, 2, G, TS, ZEROS>(a, l, s);
+    case 2: return launch_gemm_rows<1, 1, G, TS, ZEROS>(a, l, s);
+    case 3: return launch_gemm_rows<2, 1, G, TS, ZEROS>(a, l, s);
+    case 4: return launch_gemm_rows<2, 2, G, TS, ZEROS>(a, l, s);
+    case 5: return launch_gemm_rows<2, THREE, G, TS, ZEROS>(a, l, s);
+    default: return launch_gemm_rows<4, THREE, G, TS, ZEROS>(a, l, s);
+    }
 }
 
 template <typename TS, bool ZEROS>

@@ -145,3 +145,19 @@ def test_empty_and_repeated():
     K.kda_gemm_w4(x, w, a)
     K.kda_gemm_w4(x, w, b)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N,k,G,sd,zeros", [
+    # the forms for more rows: many row tiles, few, two turns of column tiles and odd numbers of them
+    (9, 41000, 640, 128, BF, True), (16, 30000, 1184, 32, F, False), (17, 41000, 128, 64, BF, True), (20, 9000, 1152, 128, F, False), (29, 30000, 640, 32, F, True), (32, 7000, 2176, 128, BF, False),
+    (33, 16000, 896, 64, F, True), (47, 41024, 256, 32, BF, True), (64, 30011, 1280, 128, BF, False), (64, 41024, 512, 32, F, True),
+    (64, 20000, 2048, 64, BF, False), (97, 12345, 384, 128, F, True), (64, 3000, 8192, 32, F, True)])
+def test_forms_for_more_rows(M, N, k, G, sd, zeros):
+    """Exact sums (whole), against a float64 product on the GPU."""
+    announce("gemm_w4 forms %s" % ((M, N, k, G, sd, zeros),))
+    dev, W, _ = weight(N, k, G, sd, zeros, M + N + k, True)
+    x = torch.randint(-2, 3, (M, k), generator=torch.Generator().manual_seed(k)).to(BF).cuda()
+    y = torch.full((M, N), float("nan"), device="cuda")
+    K.kda_gemm_w4(x, packed(dev), y)
+    ref = torch.mm(x.double(), W.cuda().t().contiguous())
+    assert torch.equal(y.double(), ref)
