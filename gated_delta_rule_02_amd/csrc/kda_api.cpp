@@ -805,7 +805,7 @@ namespace {
 constexpr int kMaxBeams = 32;
 struct BeamParts {
     int parts, len;
-    size_t sums, tops, keys, tokens, bytes;  // offsets in the workspace, total
+    size_t sums, tops, entries, bytes;  // offsets in the workspace, total
 };
 BeamParts beam_parts(int64_t B, int W, int64_t V)
 {
@@ -815,9 +815,8 @@ BeamParts beam_parts(int64_t B, int W, int64_t V)
     auto up = [](size_t n) { return (n + 15) & ~(size_t)15; };
     p.sums = 0;
     p.tops = up(units * 8);
-    p.keys = p.tops + up(units * 4);
-    p.tokens = p.keys + up(units * W * 4);
-    p.bytes = p.tokens + up(units * W * 4);
+    p.entries = p.tops + up(units * 4);
+    p.bytes = p.entries + up(units * W * 8);
     return p;
 }
 bool beam_sizes(int64_t B, int64_t W, int64_t V)
@@ -870,7 +869,7 @@ int kda_beam_select(const void* logits, int64_t ld, kda_dtype dtype, const float
     BeamSelectArgs a{logits, ld, (DType)dtype, scores, finished, B, W, (int)V,
                      eos >= 0 && eos < V ? (int)eos : -1, p.parts, p.len, next_scores, parents, tokens, next_finished,
                      reinterpret_cast<double*>(ws + p.sums), reinterpret_cast<float*>(ws + p.tops),
-                     reinterpret_cast<uint32_t*>(ws + p.keys), reinterpret_cast<uint32_t*>(ws + p.tokens)};
+                     reinterpret_cast<uint64_t*>(ws + p.entries)};
     return hip_status(launch_beam_select(a, static_cast<hipStream_t>(hip_stream)), fn);
 }
 

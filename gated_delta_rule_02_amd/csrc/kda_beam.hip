@@ -12,9 +12,9 @@
 // 1024 logits costs one comparison of the lanes' maxima with the W-th best, and only
 // steps that hold a better value look at their elements. The first step starts from
 // the W-th largest of the lanes' maxima (its upper 16 bits, found by bisection
-// with ballots), a bound that at least W values reach. A second kernel joins the
-// parts, and the beams in 64 bits: beams are compared by sums of scores whose
-// rounding to 32 bits would make new ties.
+// with ballots), a bound that at least W values reach. Then the parts of a beam are joined,
+// and the beams in 64 bits: they are compared by sums of scores whose rounding to 32 bits
+// would make new ties.
 #include <algorithm>
 
 #include "kda_device.h"
@@ -45,28 +45,72 @@ __device__ __forceinline__ uint32_t lane_before(uint32_t v)
 
 __device__ __forceinline__ bool finite(float f) { return fabsf(f) < __builtin_inff(); }
 
-// The W best of what was put in, lane i the i-th: higher key first, then lower index.
+// An entry's place in the order as one number: higher keys first, then lower indexes
+// (distinct for distinct indexes; 0 only for none).
+__device__ __forceinline__ uint64_t entry(uint32_t key, uint32_t index) { return (uint64_t)key << 32 | (uint32_t)~index; }
+__device__ __forceinline__ uint64_t lane_entry(uint64_t e, int lane)
+{
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e, lane);
+    return lo | (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(e >> 32), lane) << 32;
+}
+
+// The best of what was put in, lane i the i-th.
 struct BestList {
-    uint32_t key = 0, index = 0xffffffffu;
-    __device__ __forceinline__ void put(uint32_t k, uint32_t i, int lane)
+    uint64_t e = 0;
+    __device__ __forceinline__ void put(uint64_t n, int lane)
     {
-        // lanes whose entry comes before the new one form a prefix
-        const int pos = __popcll(__ballot(key > k || (key == k && index < i)));
-        const uint32_t pk = lane_before(key), pi = lane_before(index);
-        if (lane > pos) key = pk, index = pi;
-        if (lane == pos) key = k, index = i;
+        const int pos = __popcll(__ballot(e > n));  // lanes whose entry comes before the new one form a prefix
+        const uint64_t before = (uint64_t)lane_before((uint32_t)(e >> 32)) << 32 | lane_before((uint32_t)e);
+        e = lane > pos ? before : lane == pos ? n : e;
     }
-    // every lane's (k, i) with `in` set
-    __device__ __forceinline__ void put_lanes(bool in, uint32_t k, uint32_t i, int lane)
+    // every lane's entry with `in` set
+    __device__ __forceinline__ void put_lanes(bool in, uint64_t n, int lane)
     {
         uint64_t todo = __ballot(in);
         while (todo) {
             const int from = __ffsll((unsigned long long)todo) - 1;
             todo &= todo - 1;
-            put((uint32_t)__builtin_amdgcn_readlane((int)k, from), (uint32_t)__builtin_amdgcn_readlane((int)i, from), lane);
+            put(lane_entry(n, from), lane);
         }
     }
-    __device__ __forceinline__ uint32_t key_of(int place) const { return (uint32_t)__builtin_amdgcn_readlane((int)key, place); }
+    // the list of count <= 64 entries, lane i's the i-th (distinct): each counts those before
+    // it, which do not depend on one another as the places of a list under way do (20
+    // entries put one by one took four times as long)
+    __device__ __forceinline__ void sort(uint64_t n, int count, int lane)
+    {
+        int rank = lane < count ? 0 : lane;
+        for (int c = 0; c < count; ++c) {
+            const uint64_t o = lane_entry(n, c);
+            rank += lane < count && o > n;
+        }
+        if (lane >= count) n = 0;
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_permute(rank * 4, (int)(uint32_t)n);
+        e = (uint64_t)(uint32_t)__builtin_amdgcn_ds_permute(rank * 4, (int)(uint32_t)(n >> 32)) << 32 | lo;
+    }
+    __device__ __forceinline__ uint32_t key_of(int place) const { return (uint32_t)(lane_entry(e, place) >> 32); }
+    __device__ __forceinline__ uint32_t key() const { return (uint32_t)(e >> 32); }
+    __device__ __forceinline__ uint32_t index() const { return ~(uint32_t)e; }
+};
+
+// Entries picked lane by lane, gathered in LDS (64 of the wavefront's own) to be sorted;
+// beyond 64 they only count.
+struct Gather {
+    uint64_t* slots;
+    int count = 0;
+    __device__ __forceinline__ void add(bool in, uint64_t n, int lane)
+    {
+        const uint64_t mask = __ballot(in);
+        const int at = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+        if (in && at < 64) slots[at] = n;
+        count += __popcll(mask);
+    }
+    __device__ __forceinline__ uint64_t mine(int lane) const
+    {
+        wave_lds_order();
+        const uint64_t n = lane < count ? slots[lane] : 0;
+        wave_lds_order();
+        return n;
+    }
 };
 
 // a bound that at least n of the lanes' keys reach: the n-th largest, its lower 16 bits
@@ -80,6 +124,46 @@ __device__ __forceinline__ uint32_t lower_bound_of(uint32_t k, int n)
         if (__popcll(__ballot(k >= t)) >= n) bound = t;
     }
     return bound | (bound == 0);
+}
+
+// ---------------------------------------------------------------- a wavefront's maximum and sum
+// By shifts within rows of 16 lanes and broadcasts of a row's last lane to the next (on the
+// vector unit); every lane gets lane 63's.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = dpp<CTRL, ROWS>(0, (uint32_t)u), hi = dpp<CTRL, ROWS>(0, (uint32_t)(u >> 32));
+    return __builtin_bit_cast(double, lo | hi << 32);
+}
+__device__ __forceinline__ float wave_top(float v)
+{
+    auto step = [&](uint32_t moved) { v = fmaxf(v, __uint_as_float(moved)); };
+    step(dpp<0x111, 0xf>(__float_as_uint(v), __float_as_uint(v)));  // from 1, 2, 4 and 8 lanes before
+    step(dpp<0x112, 0xf>(__float_as_uint(v), __float_as_uint(v)));
+    step(dpp<0x114, 0xf>(__float_as_uint(v), __float_as_uint(v)));
+    step(dpp<0x118, 0xf>(__float_as_uint(v), __float_as_uint(v)));
+    step(dpp<0x142, 0xa>(__float_as_uint(v), __float_as_uint(v)));  // rows 1 and 3: from the row before
+    step(dpp<0x143, 0xc>(__float_as_uint(v), __float_as_uint(v)));  // rows 2 and 3: from row 1
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ double wave_total(double v)
+{
+    v += dpp_or_zero<0x111, 0xf>(v);
+    v += dpp_or_zero<0x112, 0xf>(v);
+    v += dpp_or_zero<0x114, 0xf>(v);
+    v += dpp_or_zero<0x118, 0xf>(v);
+    v += dpp_or_zero<0x142, 0xa>(v);
+    v += dpp_or_zero<0x143, 0xc>(v);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, lo | hi << 32);
 }
 
 // ---------------------------------------------------------------- first pass
@@ -107,23 +191,28 @@ __device__ __forceinline__ void load_step(const T* row, int at, int end, int lan
     }
 }
 
+// What the parts of all rows leave for the joining: top (largest logit) and sum (of
+// exponentials) per part, and the W best entries.
+struct PartResults {
+    float* top;
+    double* sum;
+    uint64_t* entries;
+};
+
+// Part `unit` of row `row_i`: the tokens begin .. end - 1.
 template <typename T>
-__global__ __launch_bounds__(256) void beam_part_kernel(BeamSelectArgs a)
+__device__ __forceinline__ void part_of_row(const BeamSelectArgs& a, int64_t row_i, int begin, int end, int64_t unit,
+                                            const PartResults& out, uint64_t* slots, int lane)
 {
     constexpr int VEC = Vec16<T>::N;
-    const int lane = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (unit >= (int64_t)a.B * a.W * a.parts) return;
-    const int64_t row_i = unit / a.parts;
-    const int part = unit % a.parts;
     const T* row = static_cast<const T*>(a.logits) + row_i * a.ld;
-    const int begin = part * a.part_len, end = min(begin + a.part_len, a.V);
     float x[16];
     load_step(row, begin, end, lane, x);
     // an ended or dead beam's logits decide nothing
     if ((a.finished && a.finished[row_i]) || !finite(a.scores[row_i])) return;
 
-    float top = -3.402823466e38f, sum = 0.0f;  // finite, so that -inf - top is no NaN
+    float top = -3.402823466e38f;  // finite, so that -inf - top is no NaN
+    double sum = 0.0;              // over the steps; a step's own 16 terms in float32
     BestList best;
     uint32_t bound = 0;  // keys below it cannot be among the W best
     for (int at = begin; at < end; at += kStep) {
@@ -132,90 +221,103 @@ __global__ __launch_bounds__(256) void beam_part_kernel(BeamSelectArgs a)
 #pragma unroll
         for (int i = 1; i < 16; ++i) here = fmaxf(here, x[i]);
         const float m = fmaxf(top, here);
-        sum *= exp2_fast((top - m) * kLog2e);
-        top = m;
+        float part[4] = {};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum += exp2_fast((x[i] - m) * kLog2e);
+        for (int i = 0; i < 16; ++i) part[i % 4] += exp2_fast((x[i] - m) * kLog2e);
+        sum = sum * (double)exp2_fast((top - m) * kLog2e) + (double)((part[0] + part[1]) + (part[2] + part[3]));
+        top = m;
         const uint32_t k = at + lane * VEC < end ? order_key(here) : 0;
         if (at == begin) bound = lower_bound_of(k, a.W);
         if (!__ballot(k >= bound)) continue;
+        auto token = [&](int i) { return at + (i / VEC * 64 + lane) * VEC + i % VEC; };
+        bool sorted = false;
+        if (at == begin) {
+            Gather g{slots};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int e = at + (i / VEC * 64 + lane) * VEC + i % VEC;
-            const uint32_t ki = order_key(x[i]);
-            best.put_lanes(e < end && ki >= bound, ki, (uint32_t)e, lane);
-            bound = max(bound, best.key_of(a.W - 1));  // (one as large may be of a lower token: in this step)
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t ki = order_key(x[i]);
+                g.add(token(i) < end && ki >= bound, entry(ki, (uint32_t)token(i)), lane);
+            }
+            sorted = g.count <= 64;
+            if (sorted) best.sort(g.mine(lane), g.count, lane);
+        }
+        if (!sorted) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t ki = order_key(x[i]);
+                best.put_lanes(token(i) < end && ki >= bound, entry(ki, (uint32_t)token(i)), lane);
+                bound = max(bound, best.key_of(a.W - 1));  // (one as large may be of a lower token: in this step)
+            }
         }
         const uint32_t last = best.key_of(a.W - 1);
         if (last) bound = max(bound, last + 1);  // later ones have higher tokens
     }
-    // join the lanes
-    const float m = wave_max(top);
-    double s = (double)(sum * exp2_fast((top - m) * kLog2e));
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+    const float m = wave_top(top);
+    const double s = wave_total(sum * (double)exp2_fast((top - m) * kLog2e));
     if (lane == 0) {
-        a.part_top[unit] = m;
-        a.part_sum[unit] = s;
+        out.top[unit] = m;
+        out.sum[unit] = s;
     }
     if (lane < a.W) {
-        a.part_key[unit * a.W + lane] = best.key;
-        a.part_token[unit * a.W + lane] = best.index;
+        out.entries[unit * a.W + lane] = best.e;
     }
 }
 
-// ---------------------------------------------------------------- second pass
-// A workgroup per sequence. A wavefront joins the parts of a beam: its sum, and of the
+// ---------------------------------------------------------------- joining
+// A workgroup joins a sequence, a wavefront a beam's parts: its sum, and of the
 // entries that reach the W-th largest of the parts' best the W first. Then
 // every offer finds its place: its own in its beam's list and, by bisection, how many
-// of every other beam's list come before it.
+// of every other beam's list come before it. `in` holds the sequence's parts.
 constexpr int kMaxW = 32;
+struct Offers {
+    double value[kMaxW][kMaxW];
+    uint32_t token[kMaxW][kMaxW];
+    int place[kMaxW][kMaxW];
+    uint8_t ended[kMaxW];
+    uint64_t slots[16][64];  // of the wavefronts
+};
 
-__global__ __launch_bounds__(1024) void beam_join_kernel(BeamSelectArgs a)
+__device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b, const PartResults& in, Offers& offers)
 {
-    __shared__ double value[kMaxW][kMaxW];
-    __shared__ uint32_t token[kMaxW][kMaxW];
-    __shared__ uint8_t ended[kMaxW];
-    const int lane = threadIdx.x & 63, W = a.W, entries = a.parts * W;
-    const int64_t b = blockIdx.x;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, W = a.W, count = a.parts * W;
     const double none = -__builtin_inf();
-    for (int w = threadIdx.x >> 6; w < W; w += blockDim.x >> 6) {
+    for (int w = wave; w < W; w += blockDim.x >> 6) {
         const int64_t row = b * W + w;
-        const uint32_t *keys = a.part_key + row * entries, *tokens = a.part_token + row * entries;
+        const uint64_t* entries = in.entries + w * count;
         // lane p: part p (what an ended or dead beam's parts hold is not used)
         const bool on = lane < a.parts;
-        const float top = on ? a.part_top[row * a.parts + lane] : -3.402823466e38f;
-        const double sum = on ? a.part_sum[row * a.parts + lane] : 0.0;
-        const uint32_t head = on ? keys[lane * W] : 0;
+        const float top = on ? in.top[w * a.parts + lane] : -3.402823466e38f;
+        const double sum = on ? in.sum[w * a.parts + lane] : 0.0;
+        const uint32_t head = on ? (uint32_t)(entries[lane * W] >> 32) : 0;
         const bool done = a.finished && a.finished[row];
         const float score = a.scores[row];
         const bool dead = !finite(score);
         double v = none;
         uint32_t t = lane;  // a dead beam offers its first tokens, at -inf
         if (!done && !dead) {
-            const float m = wave_max(top);
-            double s = sum * exp((double)top - (double)m);
-#pragma unroll
-            for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+            const float m = wave_top(top);
+            const double s = wave_total(sum * exp((double)top - (double)m));
             if (s > 0.0 && s < __builtin_inf()) {  // not so if no logit is finite, or one is +inf or NaN: dead
                 BestList best;
-                uint32_t bound = lower_bound_of(head, W);
-                for (int e = 0; e < entries; e += 256) {
-                    uint32_t k[4], i[4];
+                const uint32_t bound = lower_bound_of(head, W);
+                Gather g{offers.slots[wave]};
+                for (int at = 0; at < count; at += 256) {
+                    uint64_t e[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int at = e + j * 64 + lane;
-                        k[j] = at < entries ? keys[at] : 0;
-                        i[j] = at < entries ? tokens[at] : 0;
-                    }
+                    for (int j = 0; j < 4; ++j) e[j] = at + j * 64 + lane < count ? entries[at + j * 64 + lane] : 0;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        best.put_lanes(k[j] >= bound, k[j], i[j], lane);
-                        bound = max(bound, best.key_of(W - 1));
+                    for (int j = 0; j < 4; ++j) g.add((uint32_t)(e[j] >> 32) >= bound, e[j], lane);
+                }
+                if (g.count <= 64) {
+                    best.sort(g.mine(lane), g.count, lane);
+                } else {
+                    for (int at = 0; at < count; at += 64) {
+                        const uint64_t e = at + lane < count ? entries[at + lane] : 0;
+                        best.put_lanes((uint32_t)(e >> 32) >= max(bound, best.key_of(W - 1)), e, lane);
                     }
                 }
-                t = best.index;
-                if (best.key) v = (double)score + ((double)key_value(best.key) - (double)m - log(s));
+                t = best.index();
+                if (best.e) v = (double)score + ((double)key_value(best.key()) - (double)m - log(s));
             }
         } else if (!dead) {
             // ended: its end token at its score, then the first others at -inf
@@ -223,38 +325,87 @@ __global__ __launch_bounds__(1024) void beam_join_kernel(BeamSelectArgs a)
             else t = lane - 1 < a.eos ? lane - 1 : lane;
         }
         if (lane < W) {
-            value[w][lane] = v;
-            token[w][lane] = t;
+            offers.value[w][lane] = v;
+            offers.token[w][lane] = t;
+            offers.place[w][lane] = lane;
         }
-        if (lane == 0) ended[w] = done;
+        if (lane == 0) offers.ended[w] = done;
     }
     __syncthreads();
-    const int n = min(W, a.V);  // offers of a beam
-    for (int i = threadIdx.x; i < W * n; i += blockDim.x) {
-        const int w = i / n, j = i % n;
-        const double v = value[w][j];
-        int place = j;
-        for (int u = 0; u < W && place < W; ++u) {
-            if (u == w) continue;
-            // the entries of beam u before this one: larger, or equal and of a lower beam
-            int lo = 0, hi = n;
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                const double o = value[u][mid];
-                if (o > v || (o == v && u < w)) lo = mid + 1;
-                else hi = mid;
+    // An offer's place: its own in its list (set above) and, for every other beam, how many of
+    // that one's come before it: larger ones, and equal ones of a lower beam. A thread
+    // takes an offer and every `share`-th beam.
+    const int n = min(W, a.V), offered = W * n;  // of a beam, of all
+    const int share = max((int)blockDim.x / offered, 1);
+    for (int i = threadIdx.x; i < offered * share; i += blockDim.x) {
+        const int w = i % offered / n, j = i % n;
+        const double v = offers.value[w][j];
+        int before = 0;
+        for (int u = i / offered; u < W; u += share) {
+            int c = 0;
+            for (int step = 32; step; step >>= 1) {
+                const double o = offers.value[u][min(c + step, n) - 1];
+                if (c + step <= n && (o > v || (o == v && u < w))) c += step;
             }
-            place += lo;
+            if (u != w) before += c;
         }
+        if (before) atomicAdd(&offers.place[w][j], before);  // (whole numbers: in any order)
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < offered; i += blockDim.x) {
+        const int w = i / n, j = i % n, place = offers.place[w][j];
         if (place < W) {
             const int64_t o = b * W + place;
-            const int32_t t = (int32_t)token[w][j];
-            a.next_scores[o] = (float)v;
+            const int32_t t = (int32_t)offers.token[w][j];
+            a.next_scores[o] = (float)offers.value[w][j];
             a.parents[o] = w;
             a.tokens[o] = t;
-            if (a.next_finished) a.next_finished[o] = ended[w] || t == a.eos;
+            if (a.next_finished) a.next_finished[o] = offers.ended[w] || t == a.eos;
         }
     }
+}
+
+// ---------------------------------------------------------------- two launches: parts over the chip
+template <typename T>
+__global__ __launch_bounds__(256) void beam_part_kernel(BeamSelectArgs a)
+{
+    __shared__ uint64_t slots[4][64];
+    const int wave = threadIdx.x >> 6;
+    const int64_t unit = (int64_t)blockIdx.x * 4 + wave;
+    if (unit >= (int64_t)a.B * a.W * a.parts) return;
+    const int begin = (int)(unit % a.parts) * a.part_len;
+    part_of_row<T>(a, unit / a.parts, begin, min(begin + a.part_len, a.V), unit,
+                   PartResults{a.part_top, a.part_sum, a.part_entries}, slots[wave], threadIdx.x & 63);
+}
+
+__global__ __launch_bounds__(1024) void beam_join_kernel(BeamSelectArgs a)
+{
+    __shared__ Offers offers;
+    const int64_t b = blockIdx.x, units = b * a.W * a.parts;
+    join_sequence(a, b, PartResults{a.part_top + units, a.part_sum + units, a.part_entries + units * a.W}, offers);
+}
+
+// ---------------------------------------------------------------- one launch: a workgroup per sequence
+// where its wavefronts have a part of one step each, at most
+constexpr int kOneParts = 16;
+
+template <typename T>
+__global__ __launch_bounds__(1024) void beam_one_kernel(BeamSelectArgs a)
+{
+    __shared__ Offers offers;
+    __shared__ float top[kOneParts];
+    __shared__ double sum[kOneParts];
+    __shared__ uint64_t entries[kOneParts * kOneParts];  // (at most as many beams as parts)
+    const int64_t b = blockIdx.x;
+    const int part = threadIdx.x >> 6;
+    const PartResults parts{top, sum, entries};
+    if (part < a.W * a.parts) {
+        const int begin = part % a.parts * a.part_len;
+        part_of_row<T>(a, b * a.W + part / a.parts, begin, min(begin + a.part_len, a.V), part, parts, offers.slots[part],
+                       threadIdx.x & 63);
+    }
+    __syncthreads();
+    join_sequence(a, b, parts, offers);
 }
 
 // ---------------------------------------------------------------- states
@@ -314,6 +465,15 @@ int beam_part_count(int64_t rows, int64_t V, int* len)
 
 hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s)
 {
+    const int steps = (a.V + kStep - 1) / kStep;
+    if (a.W * steps <= kOneParts) {
+        BeamSelectArgs o = a;
+        o.parts = steps;
+        o.part_len = kStep;
+        if (a.dtype == F32) hipLaunchKernelGGL((beam_one_kernel<float>), dim3((unsigned)a.B), dim3(1024), 0, s, o);
+        else hipLaunchKernelGGL((beam_one_kernel<bf16_t>), dim3((unsigned)a.B), dim3(1024), 0, s, o);
+        return hipGetLastError();
+    }
     const int64_t units = (int64_t)a.B * a.W * a.parts;
     const dim3 grid((unsigned)((units + 3) / 4));
     if (a.dtype == F32) hipLaunchKernelGGL((beam_part_kernel<float>), grid, dim3(256), 0, s, a);

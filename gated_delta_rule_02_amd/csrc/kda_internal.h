@@ -307,10 +307,10 @@ struct BeamSelectArgs {
     float* next_scores;
     int32_t *parents, *tokens;
     uint8_t* next_finished;  // or null
-    // workspace, [B * W * parts] each, the last two with W entries each
+    // workspace, [B * W * parts] each, the last with W entries each
     double* part_sum;
     float* part_top;
-    uint32_t *part_key, *part_token;
+    uint64_t* part_entries;
 };
 // parts (at most 64) into which a row of V logits is cut, and their length
 int beam_part_count(int64_t rows, int64_t V, int* len);
