@@ -265,12 +265,13 @@ __device__ __forceinline__ void part_of_row(const BeamSelectArgs& a, int64_t row
 
 // ---------------------------------------------------------------- joining
 // A workgroup joins a sequence, a wavefront a beam's parts: its sum, and of the
-// entries that reach the W-th largest of the parts' best the W first. Then
+// entries that reach a bound the W first. Then
 // every offer finds its place: its own in its beam's list and, by bisection, how many
 // of every other beam's list come before it. `in` holds the sequence's parts.
 constexpr int kMaxW = 32;
 struct Offers {
     double value[kMaxW][kMaxW];
+    double score[kMaxW], top[kMaxW], log_sum[kMaxW];
     uint32_t token[kMaxW][kMaxW];
     int place[kMaxW][kMaxW];
     uint8_t ended[kMaxW];
@@ -288,36 +289,47 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
         const bool on = lane < a.parts;
         const float top = on ? in.top[w * a.parts + lane] : -3.402823466e38f;
         const double sum = on ? in.sum[w * a.parts + lane] : 0.0;
-        const uint32_t head = on ? (uint32_t)(entries[lane * W] >> 32) : 0;
+        // and the first entries of every part, as many as there are lanes for: the W-th largest
+        // of them is reached by few more than W of all (of the parts' best alone, where the
+        // parts are not many more than W, by more than there is room to sort)
+        const int of = lane % a.parts, nth = lane / a.parts;
+        const uint32_t head = nth < W && nth < 64 / a.parts ? (uint32_t)(entries[of * W + nth] >> 32) : 0;
         const bool done = a.finished && a.finished[row];
         const float score = a.scores[row];
         const bool dead = !finite(score);
         double v = none;
         uint32_t t = lane;  // a dead beam offers its first tokens, at -inf
+        bool live = false;
         if (!done && !dead) {
-            const float m = wave_top(top);
-            const double s = wave_total(sum * exp((double)top - (double)m));
+            const float m = a.parts == 1 ? in.top[w] : wave_top(top);
+            const double s = a.parts == 1 ? in.sum[w] : wave_total(sum * exp((double)top - (double)m));
             if (s > 0.0 && s < __builtin_inf()) {  // not so if no logit is finite, or one is +inf or NaN: dead
                 BestList best;
-                const uint32_t bound = lower_bound_of(head, W);
-                Gather g{offers.slots[wave]};
-                for (int at = 0; at < count; at += 256) {
-                    uint64_t e[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) e[j] = at + j * 64 + lane < count ? entries[at + j * 64 + lane] : 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) g.add((uint32_t)(e[j] >> 32) >= bound, e[j], lane);
-                }
-                if (g.count <= 64) {
-                    best.sort(g.mine(lane), g.count, lane);
+                if (a.parts == 1) {
+                    best.e = lane < W ? entries[lane] : 0;
                 } else {
-                    for (int at = 0; at < count; at += 64) {
-                        const uint64_t e = at + lane < count ? entries[at + lane] : 0;
-                        best.put_lanes((uint32_t)(e >> 32) >= max(bound, best.key_of(W - 1)), e, lane);
+                    const uint32_t bound = lower_bound_of(head, W);
+                    Gather g{offers.slots[wave]};
+                    for (int at = 0; at < count; at += 256) {
+                        uint64_t e[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) e[j] = at + j * 64 + lane < count ? entries[at + j * 64 + lane] : 0;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) g.add((uint32_t)(e[j] >> 32) >= bound, e[j], lane);
+                    }
+                    if (g.count <= 64) {
+                        best.sort(g.mine(lane), g.count, lane);
+                    } else {
+                        for (int at = 0; at < count; at += 64) {
+                            const uint64_t e = at + lane < count ? entries[at + lane] : 0;
+                            best.put_lanes((uint32_t)(e >> 32) >= max(bound, best.key_of(W - 1)), e, lane);
+                        }
                     }
                 }
                 t = best.index();
-                if (best.e) v = (double)score + ((double)key_value(best.key()) - (double)m - log(s));
+                if (best.e) v = (double)key_value(best.key());
+                live = true;
+                if (lane == 0) offers.top[w] = m, offers.log_sum[w] = s;
             }
         } else if (!dead) {
             // ended: its end token at its score, then the first others at -inf
@@ -329,7 +341,18 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
             offers.token[w][lane] = t;
             offers.place[w][lane] = lane;
         }
-        if (lane == 0) offers.ended[w] = done;
+        if (lane == 0) {
+            offers.ended[w] = done;
+            offers.score[w] = live ? (double)score : none;  // (none: the values are the offers already)
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < W) offers.log_sum[threadIdx.x] = log(offers.log_sum[threadIdx.x]);  // (all beams' at once)
+    __syncthreads();
+    for (int i = threadIdx.x; i < W * W; i += blockDim.x) {
+        const int w = i / W;
+        if (offers.score[w] != none)
+            offers.value[w][i % W] = offers.score[w] + ((offers.value[w][i % W] - offers.top[w]) - offers.log_sum[w]);
     }
     __syncthreads();
     // An offer's place: its own in its list (set above) and, for every other beam, how many of

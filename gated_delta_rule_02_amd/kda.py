@@ -741,16 +741,21 @@ def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stre
     return C
 
 
+def _ld(name, t, shape):
+    """_mat of a tensor that is dense as a rule."""
+    return shape[1] if t.shape == shape and t.is_contiguous() else _mat(name, t, shape)
+
+
 def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
                    branch_scale, post_eps, eps):
     shape = x.shape
     if len(shape) != 2:
         raise ValueError("x must be [M, K]")
+    M, K = shape
     for name, w in (("post_weight", post_weight), ("norm_weight", norm_weight)):
-        if w.shape != shape[1:] or w.dtype is not torch.float32 or not w.is_contiguous():
+        if w.dim() != 1 or w.numel() != K or w.dtype is not torch.float32 or not w.is_contiguous():
             raise TypeError("%s must be dense float32 [K]" % name)
-    act = ACTIVATIONS.get(gate_activation)
-    if gate_activation not in ("none", "sigmoid"):
+    if gate_activation != "none" and gate_activation != "sigmoid":
         raise ValueError("gate_activation must be 'none' or 'sigmoid' (got %r)" % (gate_activation,))
     pg, g_ld, gd = None, 0, KDA_F32
     if gate is not None:
@@ -759,13 +764,16 @@ def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, ga
             _tensor("gate", gate, shape[1:])
         else:
             g_ld = _mat("gate", gate, shape)
-    ro, ro_ld = None, 0
-    if residual_out is not None:
-        _type("residual_out", residual_out, residual.dtype)
-        ro, ro_ld = residual_out.data_ptr(), _mat("residual_out", residual_out, shape)
-    return (x.data_ptr(), _mat("x", x, shape), _code(x, "x"), post_weight.data_ptr(), post_eps, pg, g_ld, gd, act,
-            residual.data_ptr(), _mat("residual", residual, shape), ro, ro_ld, _code(residual, "residual"), residual_scale,
-            branch_scale, norm_weight.data_ptr(), shape[0], shape[1], eps)
+    r, r_ld = residual.data_ptr(), _ld("residual", residual, shape)
+    ro, ro_ld = r, r_ld
+    if residual_out is not residual:
+        ro, ro_ld = None, 0
+        if residual_out is not None:
+            _type("residual_out", residual_out, residual.dtype)
+            ro, ro_ld = residual_out.data_ptr(), _ld("residual_out", residual_out, shape)
+    return (x.data_ptr(), _ld("x", x, shape), _code(x, "x"), post_weight.data_ptr(), post_eps, pg, g_ld, gd,
+            ACTIVATIONS[gate_activation], r, r_ld, ro, ro_ld, _code(residual, "residual"), residual_scale, branch_scale,
+            norm_weight.data_ptr(), M, K, eps)
 
 
 def kda_sandwich_rmsnorm(x, post_weight, residual, residual_out, norm_weight, y, gate=None, gate_activation="none",
@@ -778,7 +786,7 @@ def kda_sandwich_rmsnorm(x, post_weight, residual, residual_out, norm_weight, y,
     args = _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
                           branch_scale, post_eps, eps)
     _call_on("kda_sandwich_rmsnorm", (x, post_weight, residual, residual_out, norm_weight, y, gate), stream, *args,
-             y.data_ptr(), _mat("y", y, x.shape), _code(y, "y"))
+             y.data_ptr(), _ld("y", y, x.shape), _code(y, "y"))
     return y
 
 
@@ -792,8 +800,7 @@ def kda_sandwich_rmsnorm_fp8(x, post_weight, residual, residual_out, norm_weight
     _type("codes", codes, torch.uint8), _type("scales", scales, torch.float32)
     M, K = x.shape
     _call_on("kda_sandwich_rmsnorm_fp8", (x, post_weight, residual, residual_out, norm_weight, codes, scales, gate), stream,
-             *args, codes.data_ptr(), _mat("codes", codes, x.shape), scales.data_ptr(),
-             _mat("scales", scales, (M, K // 128)))
+             *args, codes.data_ptr(), _ld("codes", codes, x.shape), scales.data_ptr(), _ld("scales", scales, (M, K // 128)))
     return codes, scales
 
 
