@@ -818,6 +818,9 @@ class W4Weight:
     def shape(self):
         return torch.Size((self.N, self.K))
 
+    def get_device(self):
+        return self.packed.get_device()
+
 
 def kda_w4_packed_bytes(N, K, group, scale_dtype=KDA_F32, has_zeros=False):
     return lib().kda_w4_packed_bytes(N, K, group, scale_dtype, int(bool(has_zeros)))

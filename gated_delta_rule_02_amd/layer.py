@@ -90,12 +90,16 @@ class KDAMixer:
         W = self.W
         return [P[:, i * W:(i + 1) * W] for i in range(5)] + [P[:, 5 * W:5 * W + self.H]]
 
-    def projections_of_norm(self, x, residual, norm_weight, eps, tag):
+    def projections_of_norm(self, x, residual, norm_weight, eps, tag, post=None):
         """The columns of RMSNorm(x + residual) norm_weight W_in^T (bf16); the
-        residual (or None) is updated in place."""
+        residual (or None) is updated in place. With post (a BranchNorm) x joins the
+        residual through it."""
         T, hidden = x.shape
         y = self._buf("ny", (T, hidden), torch.bfloat16)
-        K.kda_add_rmsnorm(x, norm_weight, y, residual=residual, residual_out=residual, eps=eps)
+        if post is None:
+            K.kda_add_rmsnorm(x, norm_weight, y, residual=residual, residual_out=residual, eps=eps)
+        else:
+            K.kda_sandwich_rmsnorm(x, post.weight, residual, residual, norm_weight, y, eps=eps, **post.form)
         P = self._buf(tag + "nP", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm_epilogue(y, self.W_in, P)
         return self._columns(P)
@@ -105,6 +109,15 @@ class KDAMixer:
         y = self._buf(tag + "y", (o.shape[0], self.W), torch.bfloat16)
         K.kda_output_norm_gate(o, gp, self.norm_w, y, eps=self.rms_eps)
         K.kda_gemm_epilogue(y, self.Wo, hidden, residual=hidden)
+
+    def output_branch(self, o, gp, tag):
+        """output's result alone, through the product that has forms for few rows."""
+        T = o.shape[0]
+        y = self._buf(tag + "y", (T, self.W), torch.bfloat16)
+        K.kda_output_norm_gate(o, gp, self.norm_w, y, eps=self.rms_eps)
+        out = self._buf(tag + "out", (T, self.hidden), torch.float32)
+        K.kda_gemm_epilogue(y, self.Wo, out)
+        return out
 
     def output(self, o, gp, tag=""):
         """y = RMSNorm(o) x w x sigmoid(gate) (bf16), out = y W_o^T (float32)."""
@@ -233,52 +246,133 @@ class DraftTree:
             K.kda_conv_tree_commit(x, self.parents, accepted, cs)
 
 
+class BranchNorm:
+    """How a block's output x joins the residual stream h in a block with a norm after
+    it too: h = residual_scale h + branch_scale act(gate) RMSNorm(x) weight. weight
+    float32 [width]; gate a learned [width] vector (float32 or bfloat16) or None, through
+    gate_activation ('none' or 'sigmoid')."""
+
+    def __init__(self, weight, gate=None, gate_activation="none", residual_scale=1.0, branch_scale=1.0, eps=1e-6):
+        self.weight = weight
+        self.form = dict(gate=gate, gate_activation=gate_activation, residual_scale=residual_scale,
+                         branch_scale=branch_scale, post_eps=eps)
+
+
+class Branch:
+    """A block's output still to be joined to the residual stream through its norm."""
+
+    __slots__ = ("x", "post")
+
+    def __init__(self, x, post):
+        self.x, self.post = x, post
+
+
 class KDABlock:
     """A mixer in its pre-norm residual block: hidden += mixer(RMSNorm(hidden) norm_weight).
 
     The residual stream `hidden` (bfloat16 or float32 rows) is updated in place.
-    With bfloat16 weights the output projection adds into it (the product's
+    With bfloat16 or 4-bit weights the output projection adds into it (the product's
     epilogue). With block-FP8 weights the block's output is returned as `delta`,
     and the next block adds it while it normalises: one pass then updates the
     stream, norms it and quantizes the projections' input. So every method takes
     the delta still to be added (None: nothing) and returns the one it leaves
     (None: added; else a buffer of the mixer, valid until that method's next call on
-    the same stream); `finish` adds a last one."""
+    the same stream); `finish` adds a last one.
 
-    def __init__(self, mixer, norm_weight, eps=1e-6):
-        self.mixer, self.norm_weight, self.eps = mixer, norm_weight, eps
+    With `post` (a BranchNorm) the output is normalised, gated and scaled before it is
+    added: every kind of mixer then returns a delta (a Branch), and the next block's
+    norm takes both norms in one pass."""
+
+    def __init__(self, mixer, norm_weight, eps=1e-6, post=None):
+        self.mixer, self.norm_weight, self.eps, self.post = mixer, norm_weight, eps, post
 
     def _enter(self, hidden, delta, tag=""):
         """hidden += delta in place; the projections of its norm -> their columns."""
         m = self.mixer
+        if isinstance(delta, Branch):
+            return m.projections_of_norm(delta.x, hidden, self.norm_weight, self.eps, tag, post=delta.post)
         x, residual = (hidden, None) if delta is None else (delta, hidden)
         return m.projections_of_norm(x, residual, self.norm_weight, self.eps, tag)
+
+    def _leave(self, o, gp, hidden, tag):
+        if self.post is None:
+            return self.mixer.output_into(o, gp, hidden, tag=tag)
+        return Branch(self.mixer.output_branch(o, gp, tag), self.post)
 
     def forward(self, hidden, delta=None, **states):
         """Prefill: hidden [T, width] rows, states as KDAMixer.forward's arguments."""
         cols = self._enter(hidden, delta)
         o, _ = self.mixer._core(cols, **states)
-        return self.mixer.output_into(o, cols[4], hidden, tag="b")
+        return self._leave(o, cols[4], hidden, "b")
 
     def decode(self, hidden, state, conv_states, delta=None):
         """One token per sequence: hidden [B, width], states (as KDAMixer.decode's,
         float32) updated in place."""
         cols = self._enter(hidden, delta)
         o = self.mixer._core_decode(cols, state, conv_states)
-        return self.mixer.output_into(o, cols[4], hidden, tag="bd")
+        return self._leave(o, cols[4], hidden, "bd")
 
     def decode_tree(self, hidden, parents, state, conv_states, delta=None):
         """A tree of drafts per sequence: hidden [B * N, width], states as
         KDAMixer.decode_tree's. Returns (delta, DraftTree)."""
         cols = self._enter(hidden, delta, tag="t")  # the commit reads them: not decode's buffer
         o, tree = self.mixer._core_tree(cols, parents, state, conv_states)
-        return self.mixer.output_into(o.view(hidden.shape[0], self.mixer.H, D), cols[4], hidden, tag="bt"), tree
+        return self._leave(o.view(hidden.shape[0], self.mixer.H, D), cols[4], hidden, "bt"), tree
 
     def finish(self, hidden, delta, norm_weight, y):
         """After the last block: y = RMSNorm(hidden + delta) norm_weight, hidden += delta."""
         if delta is None:
             return K.kda_add_rmsnorm(hidden, norm_weight, y, eps=self.eps)
+        if isinstance(delta, Branch):
+            return K.kda_sandwich_rmsnorm(delta.x, delta.post.weight, hidden, hidden, norm_weight, y, eps=self.eps,
+                                          **delta.post.form)
         return K.kda_add_rmsnorm(delta, norm_weight, y, residual=hidden, residual_out=hidden, eps=self.eps)
+
+
+class BeamSearch:
+    """Beam search with a stack of blocks: B sequences of W beams, a token each a step.
+
+    blocks KDABlocks, norm_weight [width] the norm after the last, head [V, width] (a
+    bfloat16 tensor or a W4Weight) the vocabulary's projection, eos the end token (-1: no
+    beam ends); states float32 [B * W, H,
+    128, 128] and conv_states bf16 [3, B * W, 3, H*128] of every block, updated in place:
+    row b * W + w is beam w of sequence b. `start` makes beam 0 of every sequence the
+    one that lives (prefill its row; the first step spreads it over the others). After a
+    step scores float32, parents (the beam followed), tokens int32 and finished bool
+    [B, W] hold the new beams, best first; they and `logits` are overwritten by the next."""
+
+    def __init__(self, blocks, norm_weight, head, B, W, eos, states, conv_states):
+        self.blocks, self.norm_weight, self.head, self.eos = blocks, norm_weight, head, eos
+        self.states, self.conv_states = states, conv_states
+        new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="cuda")
+        V, width = head.shape
+        self.scores, self.finished = new(B, W), new(B, W, dtype=torch.bool)
+        self.parents, self.tokens = new(B, W, dtype=torch.int32), new(B, W, dtype=torch.int32)
+        self.logits, self.y = new(B * W, V), new(B * W, width, dtype=torch.bfloat16)
+        self.start()
+
+    def start(self):
+        self.scores.fill_(float("-inf"))
+        self.scores[:, 0] = 0
+        self.finished.fill_(False)
+
+    def step(self, hidden):
+        """hidden [B * W, width] (bfloat16 or float32, changed in place): the embeddings of
+        the last step's tokens. Chooses the next ones and moves the beams' states."""
+        delta = None
+        for block, state, conv in zip(self.blocks, self.states, self.conv_states):
+            delta = block.decode(hidden, state, conv, delta)
+        self.blocks[-1].finish(hidden, delta, self.norm_weight, self.y)
+        if isinstance(self.head, K.W4Weight):
+            K.kda_gemm_w4(self.y, self.head, self.logits)
+        else:
+            K.kda_gemm_epilogue(self.y, self.head, self.logits)
+        finished = self.finished if self.eos >= 0 else None
+        K.kda_beam_select(self.logits, self.scores, self.scores, self.parents, self.tokens, finished=finished,
+                          next_finished=finished, eos=self.eos)
+        for state, conv in zip(self.states, self.conv_states):
+            K.kda_beam_reorder(self.parents, state, conv)
+        return self.tokens
 
 
 class DecodeGraph:
@@ -354,19 +448,25 @@ class KDAMixerFP8(KDAMixer):
         K.kda_gemm_fp8(xq, xs, self.W_in, self.W_in_s, P)
         return P, self._columns(P)
 
-    def projections_of_norm(self, x, residual, norm_weight, eps, tag):
+    def projections_of_norm(self, x, residual, norm_weight, eps, tag, post=None):
         """As KDAMixer's, the norm quantized in the same pass."""
         T, hidden = x.shape
         xq = self._buf("nq", (T, hidden), torch.uint8)
         xs = self._buf("ns", (T, hidden // 128), torch.float32)
-        K.kda_add_rmsnorm_fp8(x, norm_weight, xq, xs, residual=residual, residual_out=residual, eps=eps)
+        if post is None:
+            K.kda_add_rmsnorm_fp8(x, norm_weight, xq, xs, residual=residual, residual_out=residual, eps=eps)
+        else:
+            K.kda_sandwich_rmsnorm_fp8(x, post.weight, residual, residual, norm_weight, xq, xs, eps=eps, **post.form)
         P = self._buf(tag + "nP", (T, self.W_in.shape[0]), torch.bfloat16)
         K.kda_gemm_fp8(xq, xs, self.W_in, self.W_in_s, P)
         return self._columns(P)
 
+    def output_branch(self, o, gp, tag):
+        return self.output(o, gp, tag)[0]
+
     def output_into(self, o, gp, hidden, tag):
         """The block's output, left for the next norm to add."""
-        return self.output(o, gp, tag)[0]
+        return self.output_branch(o, gp, tag)
 
     def output(self, o, gp, tag=""):
         """The epilogue quantized per (token, head), then out = Y W_o^T (float32)."""
@@ -377,3 +477,55 @@ class KDAMixerFP8(KDAMixer):
         out = self._buf(tag + "out", (T, self.hidden), torch.float32)
         K.kda_gemm_fp8(yq, ys, self.Wo, self.Wo_s, out)
         return out, (yq, ys)
+
+
+class KDAMixerW4(KDAMixer):
+    """The same mixer with its projections in 4 bits (kda_w4_pack): W_in [5*H*128 + H (+
+    zero rows to a multiple of 8), hidden] and Wo [hidden, H*128] are W4Weights. Below
+    EXPAND rows (decode, draft trees, beams) the products read the packed weights; a
+    prefill expands them to bfloat16 in the mixer's scratch first (once a call: the
+    weights' roundings to bfloat16 are the difference between the two)."""
+
+    # Rows from which expanding pays; direct | expanded, us: with 41,024 x 4096 weights 512
+    # rows 219 | 296, 768 338 | 318, 1,024 433 | 415; with 4096 x 8192 80 | 88 for 768, 100 | 92
+    EXPAND = 768
+
+    def __init__(self, W_in, Wo, conv_q, conv_k, conv_v, A_log, norm_w, H, **kw):
+        super().__init__(W_in, conv_q, conv_k, conv_v, A_log, norm_w, Wo, H, **kw)
+
+    def _product(self, x, w, y, residual=None):
+        if x.shape[0] < self.EXPAND:
+            return K.kda_gemm_w4(x, w, y, residual=residual)
+        return K.kda_gemm_epilogue(x, K.kda_w4_expand(w, self._buf("w%dx%d" % (w.N, w.K), w.shape, torch.bfloat16)), y, residual=residual)
+
+    def projections(self, x, tag=""):
+        P = self._buf(tag + "P", (x.shape[0], self.W_in.N), torch.bfloat16)
+        self._product(x, self.W_in, P)
+        return P, self._columns(P)
+
+    def projections_of_norm(self, x, residual, norm_weight, eps, tag, post=None):
+        T, hidden = x.shape
+        y = self._buf("ny", (T, hidden), torch.bfloat16)
+        if post is None:
+            K.kda_add_rmsnorm(x, norm_weight, y, residual=residual, residual_out=residual, eps=eps)
+        else:
+            K.kda_sandwich_rmsnorm(x, post.weight, residual, residual, norm_weight, y, eps=eps, **post.form)
+        P = self._buf(tag + "nP", (T, self.W_in.N), torch.bfloat16)
+        self._product(y, self.W_in, P)
+        return self._columns(P)
+
+    def output_into(self, o, gp, hidden, tag):
+        y = self._buf(tag + "y", (o.shape[0], self.W), torch.bfloat16)
+        K.kda_output_norm_gate(o, gp, self.norm_w, y, eps=self.rms_eps)
+        self._product(y, self.Wo, hidden, residual=hidden)
+
+    def output_branch(self, o, gp, tag):
+        return self.output(o, gp, tag)[0]
+
+    def output(self, o, gp, tag=""):
+        T = o.shape[0]
+        y = self._buf(tag + "y", (T, self.W), torch.bfloat16)
+        K.kda_output_norm_gate(o, gp, self.norm_w, y, eps=self.rms_eps)
+        out = self._buf(tag + "out", (T, self.hidden), torch.float32)
+        self._product(y, self.Wo, out)
+        return out, y
