@@ -100,6 +100,7 @@ struct Gather {
     __device__ __forceinline__ void add(bool in, uint64_t n, int lane)
     {
         const uint64_t mask = __ballot(in);
+        if (!mask) return;
         const int at = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
         if (in && at < 64) slots[at] = n;
         count += __popcll(mask);
@@ -294,6 +295,9 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
         // parts are not many more than W, by more than there is room to sort)
         const int of = lane % a.parts, nth = lane / a.parts;
         const uint32_t head = nth < W && nth < 64 / a.parts ? (uint32_t)(entries[of * W + nth] >> 32) : 0;
+        uint64_t e[4];  // the first 256, on their way together with the rest
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[j] = j * 64 + lane < count ? entries[j * 64 + lane] : 0;
         const bool done = a.finished && a.finished[row];
         const float score = a.scores[row];
         const bool dead = !finite(score);
@@ -306,23 +310,23 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
             if (s > 0.0 && s < __builtin_inf()) {  // not so if no logit is finite, or one is +inf or NaN: dead
                 BestList best;
                 if (a.parts == 1) {
-                    best.e = lane < W ? entries[lane] : 0;
+                    best.e = e[0];
                 } else {
                     const uint32_t bound = lower_bound_of(head, W);
                     Gather g{offers.slots[wave]};
-                    for (int at = 0; at < count; at += 256) {
-                        uint64_t e[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) e[j] = at + j * 64 + lane < count ? entries[at + j * 64 + lane] : 0;
+                    for (int at = 0;;) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) g.add((uint32_t)(e[j] >> 32) >= bound, e[j], lane);
+                        if ((at += 256) >= count) break;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) e[j] = at + j * 64 + lane < count ? entries[at + j * 64 + lane] : 0;
                     }
                     if (g.count <= 64) {
                         best.sort(g.mine(lane), g.count, lane);
                     } else {
                         for (int at = 0; at < count; at += 64) {
-                            const uint64_t e = at + lane < count ? entries[at + lane] : 0;
-                            best.put_lanes((uint32_t)(e >> 32) >= max(bound, best.key_of(W - 1)), e, lane);
+                            const uint64_t n = at + lane < count ? entries[at + lane] : 0;
+                            best.put_lanes((uint32_t)(n >> 32) >= max(bound, best.key_of(W - 1)), n, lane);
                         }
                     }
                 }

@@ -556,7 +556,7 @@ def _tensor(name, t, shape):
 
 
 def _type(name, t, dtype):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s (got %s)" % (name, dtype, t.dtype))
 
 
@@ -743,7 +743,7 @@ def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stre
 
 def _ld(name, t, shape):
     """_mat of a tensor that is dense as a rule."""
-    return shape[1] if t.shape == shape and t.is_contiguous() else _mat(name, t, shape)
+    return shape[1] if t.is_contiguous() and t.shape == shape else _mat(name, t, shape)
 
 
 def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
@@ -752,28 +752,33 @@ def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, ga
     if len(shape) != 2:
         raise ValueError("x must be [M, K]")
     M, K = shape
-    for name, w in (("post_weight", post_weight), ("norm_weight", norm_weight)):
-        if w.dim() != 1 or w.numel() != K or w.dtype is not torch.float32 or not w.is_contiguous():
-            raise TypeError("%s must be dense float32 [K]" % name)
-    if gate_activation != "none" and gate_activation != "sigmoid":
+    act, rd, wshape = ACTIVATIONS.get(gate_activation), residual.dtype, shape[1:]
+    dense = (x.is_contiguous() and residual.is_contiguous() and residual.shape == shape and
+             (residual_out is residual or residual_out is not None and residual_out.is_contiguous() and
+              residual_out.shape == shape and residual_out.dtype is rd))
+    if not ((act == 0 or act == 4) and post_weight.shape == wshape and norm_weight.shape == wshape and
+            post_weight.dtype is torch.float32 and norm_weight.dtype is torch.float32 and post_weight.is_contiguous() and
+            norm_weight.is_contiguous()):
+        for name, w in (("post_weight", post_weight), ("norm_weight", norm_weight)):
+            if w.shape != wshape or w.dtype is not torch.float32 or not w.is_contiguous():
+                raise TypeError("%s must be dense float32 [K]" % name)
         raise ValueError("gate_activation must be 'none' or 'sigmoid' (got %r)" % (gate_activation,))
     pg, g_ld, gd = None, 0, KDA_F32
     if gate is not None:
         pg, gd = gate.data_ptr(), _code(gate, "gate")
         if gate.dim() == 1:
-            _tensor("gate", gate, shape[1:])
+            _tensor("gate", gate, wshape)
         else:
             g_ld = _mat("gate", gate, shape)
-    r, r_ld = residual.data_ptr(), _ld("residual", residual, shape)
-    ro, ro_ld = r, r_ld
-    if residual_out is not residual:
-        ro, ro_ld = None, 0
+    x_ld = r_ld = ro_ld = K
+    if not dense:
+        x_ld, r_ld = _mat("x", x, shape), _mat("residual", residual, shape)
         if residual_out is not None:
-            _type("residual_out", residual_out, residual.dtype)
-            ro, ro_ld = residual_out.data_ptr(), _ld("residual_out", residual_out, shape)
-    return (x.data_ptr(), _ld("x", x, shape), _code(x, "x"), post_weight.data_ptr(), post_eps, pg, g_ld, gd,
-            ACTIVATIONS[gate_activation], r, r_ld, ro, ro_ld, _code(residual, "residual"), residual_scale, branch_scale,
-            norm_weight.data_ptr(), M, K, eps)
+            _type("residual_out", residual_out, rd)
+            ro_ld = _mat("residual_out", residual_out, shape)
+    return (x.data_ptr(), x_ld, _code(x, "x"), post_weight.data_ptr(), post_eps, pg, g_ld, gd, act, residual.data_ptr(),
+            r_ld, None if residual_out is None else residual_out.data_ptr(), ro_ld, _code(residual, "residual"),
+            residual_scale, branch_scale, norm_weight.data_ptr(), M, K, eps)
 
 
 def kda_sandwich_rmsnorm(x, post_weight, residual, residual_out, norm_weight, y, gate=None, gate_activation="none",
@@ -798,9 +803,9 @@ def kda_sandwich_rmsnorm_fp8(x, post_weight, residual, residual_out, norm_weight
     args = _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
                           branch_scale, post_eps, eps)
     _type("codes", codes, torch.uint8), _type("scales", scales, torch.float32)
-    M, K = x.shape
+    M, K = shape = x.shape
     _call_on("kda_sandwich_rmsnorm_fp8", (x, post_weight, residual, residual_out, norm_weight, codes, scales, gate), stream,
-             *args, codes.data_ptr(), _ld("codes", codes, x.shape), scales.data_ptr(), _ld("scales", scales, (M, K // 128)))
+             *args, codes.data_ptr(), _ld("codes", codes, shape), scales.data_ptr(), _ld("scales", scales, (M, K // 128)))
     return codes, scales
 
 
