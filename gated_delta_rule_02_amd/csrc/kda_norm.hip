@@ -318,18 +318,29 @@ __global__ __launch_bounds__(1024) void sandwich_wide_kernel(SandwichArgs a)
     }
 }
 
+// Few columns a thread, so that many rows are under way at once: us with THREADS x NV, rows of
+// bfloat16 (a gate of their own) 8191 x 4096 65.6 with 512 x 1, 68.0 with 256 x 2; 2000 x 8192
+// 38.3 with 512 x 2, 41.1 with 256 x 4; 2048 x 16,384 without a gate 55.9 with 1024 x 2, 79.9
+// read again; 1000 x 30,720 75 with 1024 x 4, 90 read again (a copy's rate: 65.5, 32.0, 52.4, 60.0).
+template <typename TX, typename TR, typename TG, typename TY, int GATE, int TPR, int NV>
+hipError_t sandwich_launch(const SandwichArgs& a, hipStream_t s)
+{
+    constexpr int THREADS = TPR > 256 ? TPR : 256;
+    const dim3 grid((unsigned)((a.M + THREADS / TPR - 1) / (THREADS / TPR)));
+    hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, TPR, NV>), grid, dim3(THREADS), 0, s, a);
+    return hipGetLastError();
+}
+
 template <typename TX, typename TR, typename TG, typename TY, int GATE>
 hipError_t sandwich_rows(const SandwichArgs& a, hipStream_t s)
 {
-    const dim3 rows((unsigned)a.M);
-    if (a.K <= 1024)
-        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, 64, 2>), dim3((unsigned)((a.M + 3) / 4)), dim3(256), 0, s, a);
-    else if (a.K <= 4096)
-        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, 256, 2>), rows, dim3(256), 0, s, a);
-    else if (a.K <= 8192)
-        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, 256, 4>), rows, dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((sandwich_wide_kernel<TX, TR, TG, TY, GATE>), rows, dim3(1024), 0, s, a);
+    if (a.K <= 1024) return sandwich_launch<TX, TR, TG, TY, GATE, 64, 2>(a, s);
+    if (a.K <= 2048) return sandwich_launch<TX, TR, TG, TY, GATE, 256, 1>(a, s);
+    if (a.K <= 4096) return sandwich_launch<TX, TR, TG, TY, GATE, 512, 1>(a, s);
+    if (a.K <= 8192) return sandwich_launch<TX, TR, TG, TY, GATE, 512, 2>(a, s);
+    if (a.K <= 16384) return sandwich_launch<TX, TR, TG, TY, GATE, 1024, 2>(a, s);
+    if (a.K <= 32768) return sandwich_launch<TX, TR, TG, TY, GATE, 1024, 4>(a, s);
+    hipLaunchKernelGGL((sandwich_wide_kernel<TX, TR, TG, TY, GATE>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
     return hipGetLastError();
 }
 

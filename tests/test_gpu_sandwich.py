@@ -28,7 +28,7 @@ def half_step(dtype):
 
 
 def lanes(k):
-    return 64 if k <= 1024 else 256 if k <= 8192 else 1024
+    return 64 if k <= 1024 else 256 if k <= 2048 else 512 if k <= 8192 else 1024
 
 
 def make(M, k, xd, rd, gate, gd, pad, seed):
@@ -78,6 +78,8 @@ CASES = [
     (2, 4104, F, F, F, "rows", F, "sigmoid", 8), (33, 5128, BF, BF, BF, "rows", BF, "sigmoid", 24),
     (4, 8192, BF, BF, F, None, F, "none", 0), (3, 8200, BF, F, F, "rows", BF, "sigmoid", 8), (2, 40968, F, BF, F, "vector", F, "none", 0),
     (4099, 136, BF, BF, BF, "vector", BF, "sigmoid", 0), (6, 16384, F, F, BF, "rows", BF, "none", 0),
+    (5, 2048, F, BF, F, "rows", F, "sigmoid", 0), (3, 2056, BF, F, BF, "vector", F, "none", 8), (2, 16392, BF, BF, F, "rows", BF, "sigmoid", 0),
+    (2, 32768, F, F, F, None, F, "none", 0), (3, 32776, BF, F, BF, "rows", F, "sigmoid", 8),
 ]
 
 
