@@ -439,33 +439,29 @@ __global__ __launch_bounds__(1024) void beam_one_kernel(BeamSelectArgs a)
 // Rows of a sequence's W beams exchanged in place: a thread owns the same 16 bytes
 // of every beam, loads those that another beam takes over, then stores them. Only
 // beams that another one follows are read and only beams that change are written.
-template <int MAXW>
-__global__ __launch_bounds__(256) void beam_reorder_kernel(BeamReorderArgs a)
+template <int MAXW, int THREADS>
+__global__ __launch_bounds__(THREADS) void beam_reorder_kernel(BeamReorderArgs a)
 {
-    const int64_t state_blocks = (a.state_vecs + 255) / 256, conv_blocks = (a.conv_vecs + 255) / 256;
+    const int64_t state_blocks = (a.state_vecs + THREADS - 1) / THREADS, conv_blocks = (a.conv_vecs + THREADS - 1) / THREADS;
     const int64_t per = state_blocks + a.streams * conv_blocks;
+    const int lane = threadIdx.x & 63;
     for (int64_t blk = blockIdx.x; blk < per * a.B; blk += gridDim.x) {
         const int64_t b = blk / per, i = blk % per;
         int64_t vecs, at;
         u32x4_t* base;
         if (i < state_blocks) {
-            vecs = a.state_vecs, at = i * 256 + threadIdx.x;
+            vecs = a.state_vecs, at = i * THREADS + threadIdx.x;
             base = static_cast<u32x4_t*>(a.state) + b * a.W * vecs;
         } else {
             const int64_t j = i - state_blocks;
-            vecs = a.conv_vecs, at = j % conv_blocks * 256 + threadIdx.x;
+            vecs = a.conv_vecs, at = j % conv_blocks * THREADS + threadIdx.x;
             base = static_cast<u32x4_t*>(a.conv) + (j / conv_blocks * a.B + b) * a.W * vecs;
         }
         // followers[p]: the beams (but p) that become p's continuation
+        const int from = lane < a.W ? a.parents[b * a.W + lane] : -1;
         uint32_t followers[MAXW];
 #pragma unroll
-        for (int p = 0; p < MAXW; ++p) followers[p] = 0;
-        for (int w = 0; w < a.W; ++w) {
-            const int from = a.parents[b * a.W + w];
-#pragma unroll
-            for (int p = 0; p < MAXW; ++p)
-                if (p == from && p < a.W && p != w) followers[p] |= 1u << w;
-        }
+        for (int p = 0; p < MAXW; ++p) followers[p] = p < a.W ? (uint32_t)__ballot(from == p && lane != p) : 0;
         if (at >= vecs) continue;
         u32x4_t v[MAXW];
 #pragma unroll
@@ -475,6 +471,15 @@ __global__ __launch_bounds__(256) void beam_reorder_kernel(BeamReorderArgs a)
         for (int p = 0; p < MAXW; ++p)
             for (uint32_t f = followers[p]; f; f &= f - 1) base[(int64_t)(__ffs(f) - 1) * vecs + at] = v[p];
     }
+}
+
+template <int MAXW, int THREADS>
+hipError_t launch_reorder(const BeamReorderArgs& a, hipStream_t s)
+{
+    const int64_t per = (a.state_vecs + THREADS - 1) / THREADS + a.streams * ((a.conv_vecs + THREADS - 1) / THREADS);
+    hipLaunchKernelGGL((beam_reorder_kernel<MAXW, THREADS>), dim3((unsigned)min(per * a.B, (int64_t)1 << 20)), dim3(THREADS), 0,
+                       s, a);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -511,13 +516,10 @@ hipError_t launch_beam_select(const BeamSelectArgs& a, hipStream_t s)
 
 hipError_t launch_beam_reorder(const BeamReorderArgs& a, hipStream_t s)
 {
-    const int64_t per = (a.state_vecs + 255) / 256 + a.streams * ((a.conv_vecs + 255) / 256);
-    const dim3 grid((unsigned)min(per * a.B, (int64_t)1 << 20)), block(256);
-    if (a.W <= 4) hipLaunchKernelGGL((beam_reorder_kernel<4>), grid, block, 0, s, a);
-    else if (a.W <= 8) hipLaunchKernelGGL((beam_reorder_kernel<8>), grid, block, 0, s, a);
-    else if (a.W <= 16) hipLaunchKernelGGL((beam_reorder_kernel<16>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((beam_reorder_kernel<32>), grid, block, 0, s, a);
-    return hipGetLastError();
+    if (a.W <= 4) return launch_reorder<4, 256>(a, s);
+    if (a.W <= 8) return launch_reorder<8, 512>(a, s);
+    if (a.W <= 16) return launch_reorder<16, 512>(a, s);
+    return launch_reorder<32, 512>(a, s);
 }
 
 }  // namespace kda
