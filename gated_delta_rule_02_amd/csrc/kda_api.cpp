@@ -778,7 +778,7 @@ int kda_gemm_w4(const void* x, int64_t ldx, kda_dtype x_dtype, const void* packe
     REQUIRE(x_dtype == KDA_BF16, KDA_ERR_UNSUPPORTED, "%s: only bfloat16 x is supported", fn);
     if (int rc = check_w4(fn, N, K, group, scale_dtype); rc != KDA_OK) return rc;
     REQUIRE(M >= 0, KDA_ERR_INVALID_ARG, "%s: M must be >= 0", fn);
-    REQUIRE(M < ((int64_t)1 << 20), KDA_ERR_UNSUPPORTED, "%s: at most 2^20 - 1 rows (got %lld)", fn, (long long)M);
+    REQUIRE(M < ((int64_t)1 << 19), KDA_ERR_UNSUPPORTED, "%s: at most 2^19 - 1 rows (got %lld)", fn, (long long)M);
     if (M == 0) return ok();
     REQUIRE(x && packed && y, KDA_ERR_INVALID_ARG, "%s: null pointer", fn);
     // (the kernel addresses up to 64 rows of x through 32-bit offsets)

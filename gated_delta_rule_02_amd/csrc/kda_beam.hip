@@ -274,7 +274,7 @@ struct Offers {
     double value[kMaxW][kMaxW];
     double score[kMaxW], top[kMaxW], log_sum[kMaxW];
     uint32_t token[kMaxW][kMaxW];
-    int place[kMaxW][kMaxW];
+    int before[1024];  // of each thread's share of the other beams
     uint8_t ended[kMaxW];
     uint64_t slots[16][64];  // of the wavefronts
 };
@@ -343,7 +343,6 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
         if (lane < W) {
             offers.value[w][lane] = v;
             offers.token[w][lane] = t;
-            offers.place[w][lane] = lane;
         }
         if (lane == 0) {
             offers.ended[w] = done;
@@ -359,9 +358,9 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
             offers.value[w][i % W] = offers.score[w] + ((offers.value[w][i % W] - offers.top[w]) - offers.log_sum[w]);
     }
     __syncthreads();
-    // An offer's place: its own in its list (set above) and, for every other beam, how many of
-    // that one's come before it: larger ones, and equal ones of a lower beam. A thread
-    // takes an offer and every `share`-th beam.
+    // An offer's place: its own in its list and, for every other beam, how many of that one's
+    // come before it: larger ones, and equal ones of a lower beam. A thread takes an offer and
+    // every `share`-th beam.
     const int n = min(W, a.V), offered = W * n;  // of a beam, of all
     const int share = max((int)blockDim.x / offered, 1);
     for (int i = threadIdx.x; i < offered * share; i += blockDim.x) {
@@ -376,11 +375,13 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
             }
             if (u != w) before += c;
         }
-        if (before) atomicAdd(&offers.place[w][j], before);  // (whole numbers: in any order)
+        offers.before[i] = before;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < offered; i += blockDim.x) {
-        const int w = i / n, j = i % n, place = offers.place[w][j];
+        const int w = i / n, j = i % n;
+        int place = j;
+        for (int q = 0; q < share; ++q) place += offers.before[q * offered + i];
         if (place < W) {
             const int64_t o = b * W + place;
             const int32_t t = (int32_t)offers.token[w][j];

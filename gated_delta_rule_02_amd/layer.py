@@ -493,6 +493,20 @@ class KDAMixerW4(KDAMixer):
     def __init__(self, W_in, Wo, conv_q, conv_k, conv_v, A_log, norm_w, H, **kw):
         super().__init__(W_in, conv_q, conv_k, conv_v, A_log, norm_w, Wo, H, **kw)
 
+    @classmethod
+    def from_host(cls, d):
+        """Build from host arrays: the convolutions, A_log, norm_w and H as in
+        ``synth.workload_layer``, and for both weights (Win, Wo) kda_w4_pack's inputs:
+        codes uint8 [N, K/2], scales float32 [N, K/group] and, where given, zeros uint8."""
+        def packed(name, pad):
+            parts = [d[name + "_codes"], d[name + "_scales"], d.get(name + "_zeros")]
+            # rows of zero scale up to a multiple of 8 (16-byte aligned columns of the output)
+            rows = (-parts[0].shape[0]) % 8 if pad else 0
+            parts = [None if p is None else np.concatenate([p, np.zeros((rows, p.shape[1]), p.dtype)]) for p in parts]
+            return K.kda_w4_pack(*(None if p is None else torch.from_numpy(p).cuda() for p in parts))
+        return cls(packed("Win", True), packed("Wo", False), _dev_bf16(d["conv_q"]), _dev_bf16(d["conv_k"]),
+                   _dev_bf16(d["conv_v"]), torch.from_numpy(d["A_log"]).cuda(), torch.from_numpy(d["norm_w"]).cuda(), d["H"])
+
     def _product(self, x, w, y, residual=None):
         if x.shape[0] < self.EXPAND:
             return K.kda_gemm_w4(x, w, y, residual=residual)

@@ -744,7 +744,7 @@ int kda_w4_pack(const uint8_t* codes, int64_t ldc, const void* scales, int64_t l
  * residual  [M, N] residual_dtype, row stride residual_ld, or NULL. It may be y itself
  *           (same pointer, stride and dtype); any other overlap is rejected.
  * y         rows of N at y + m * ldy (y_dtype; any ldy >= N).
- * M < 2^20, M = 0 does nothing.
+ * M < 2^19, M = 0 does nothing.
  * ---------------------------------------------------------------------- */
 int kda_gemm_w4(const void* x, int64_t ldx, kda_dtype x_dtype, const void* packed, int group, kda_dtype scale_dtype,
                 int has_zeros, const void* residual, int64_t residual_ld, kda_dtype residual_dtype, void* y,

@@ -111,7 +111,7 @@ def test_gemm_w4_validation():
         assert gemm(**{name: fake(9) + 8}) == INVALID, name
     assert gemm(xd=K.KDA_F32) == UNSUPPORTED and gemm(xd=9) == INVALID and gemm(yd=9) == INVALID and gemm(rd=9) == INVALID
     assert gemm(sd=9) == INVALID and gemm(G=16) == UNSUPPORTED and gemm(K=288, ldx=288) == UNSUPPORTED
-    assert gemm(M=-1) == INVALID and gemm(M=1 << 20) == UNSUPPORTED and gemm(N=0) == INVALID
+    assert gemm(M=-1) == INVALID and gemm(M=1 << 19) == UNSUPPORTED and gemm(N=0) == INVALID
     assert gemm(ldx=248) == INVALID and gemm(ldx=260) == INVALID and gemm(ldx=1 << 22) == INVALID
     assert gemm(ldy=99) == INVALID and gemm(ldr=99) == INVALID
     assert gemm(y=fake(1)) == INVALID and gemm(y=fake(2) + 256) == INVALID

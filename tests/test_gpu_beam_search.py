@@ -65,6 +65,28 @@ def test_w4_mixer_is_the_bf16_mixer_of_its_weights(T):
         tree.commit(torch.full((T // 5,), 4, dtype=I32, device="cuda"), st, cv)
 
 
+def test_w4_mixer_from_host_arrays():
+    """Codes, scales and zero points on the host, an odd number of rows: the bfloat16 mixer of
+    the values they stand for (powers of two as scales: exact)."""
+    d = synth.workload_layer(T=4, hidden=WIDTH, H=H, seed=12)
+    rng = np.random.default_rng(3)
+    for name, n, k in (("Win", 5 * H * 128 + H, WIDTH), ("Wo", WIDTH, H * 128)):
+        d[name + "_codes"] = rng.integers(0, 256, (n, k // 2), dtype=np.uint8)
+        d[name + "_scales"] = (2.0 ** rng.integers(-9, -7, (n, k // 32))).astype(np.float32)
+        d[name + "_zeros"] = rng.integers(4, 12, (n, k // 32), dtype=np.uint8)
+    m = layer.KDAMixerW4.from_host(d)
+    assert m.W_in.shape == (5 * H * 128 + 8, WIDTH) and m.Wo.shape == (WIDTH, H * 128)
+
+    def values(name):
+        c = np.stack([d[name + "_codes"] & 15, d[name + "_codes"] >> 4], -1).reshape(d[name + "_codes"].shape[0], -1)
+        wide = lambda a: np.repeat(a.astype(np.float32), 32, 1)
+        return torch.from_numpy((c - wide(d[name + "_zeros"])) * wide(d[name + "_scales"])).to(BF).cuda()
+    win = torch.cat([values("Win"), torch.zeros((6, WIDTH), dtype=BF, device="cuda")])
+    b = layer.KDAMixer(win, *m.conv, m.A_log, m.norm_w, values("Wo"), H)
+    x = rows(9, 13, BF)
+    assert relerr(host64(m.forward(x)), host64(b.forward(x))) < TOL_BF16
+
+
 def test_w4_block_expanded_equals_bf16_block():
     """Above EXPAND rows the block makes the bfloat16 block's calls on the same values."""
     a, b = mixers(7)
