@@ -20,7 +20,11 @@
 // the same float32 accumulators leaves the group's sum of x (c - z). The terms are at
 // most three times as large as x (c - z)'s own, so the sums lose less than two bits.
 //
-// Bound by HBM: N K / 2 bytes of codes for up to about a hundred rows of x.
+// Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 20 us, 4.3 TB/s. For
+// more, by the instructions of a column tile, since those of the vector unit find little room
+// beside the matrix instruction's with two wavefronts a SIMD: 64 rows 31 to 38 us (31 with
+// part of the weights in the last-level cache), where each of a wavefront's turns takes 64
+// matrix and about 170 vector instructions, and the weights at a copy's rate 18 us.
 #include "kda_device.h"
 #include "kda_internal.h"
 
@@ -96,7 +100,7 @@ __global__ __launch_bounds__(256) void w4_pack_kernel(W4PackArgs a, W4Layout l)
 }
 
 // ---------------------------------------------------------------- expansion
-// A wavefront per tile: W in bfloat16, for products of many rows.
+// A wavefront per tile: W in bfloat16, for products of many rows. 41,024 x 4096 98 us, 4.3 TB/s.
 template <typename TS, bool ZEROS>
 __global__ __launch_bounds__(256) void w4_expand_kernel(W4ExpandArgs a, W4Layout l)
 {
