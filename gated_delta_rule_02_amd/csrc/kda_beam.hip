@@ -364,14 +364,14 @@ __device__ __forceinline__ void join_sequence(const BeamSelectArgs& a, int64_t b
     // come before it: larger ones, and equal ones of a lower beam. A thread takes an offer and
     // every `share`-th beam.
     const int n = min(W, a.V), offered = W * n;  // of a beam, of all
-    const int share = max((int)blockDim.x / offered, 1);
+    const int share = max(min((int)blockDim.x / offered, W), 1);
     for (int i = threadIdx.x; i < offered * share; i += blockDim.x) {
         const int w = i % offered / n, j = i % n;
         const double v = offers.value[w][j];
         int before = 0;
         for (int u = i / offered; u < W; u += share) {
             int c = 0;
-            for (int step = 32; step; step >>= 1) {
+            for (int step = 1 << (31 - __clz(n)); step; step >>= 1) {
                 const double o = offers.value[u][min(c + step, n) - 1];
                 if (c + step <= n && (o > v || (o == v && u < w))) c += step;
             }
