@@ -547,6 +547,11 @@ def _mat(name, t, shape):
     return ld if shape[0] != 1 else (shape[1] + 15) // 16 * 16
 
 
+def _ld(name, t, shape):
+    """_mat of a tensor that is dense as a rule."""
+    return shape[1] if t.is_contiguous() and t.shape == shape else _mat(name, t, shape)
+
+
 def _tensor(name, t, shape):
     """A dense tensor of this shape."""
     if t.shape != shape:
@@ -565,8 +570,12 @@ def _call_on(name, tensors, stream, *args):
     current for the call; without a stream on that device's current one."""
     index = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.get_device() != index or index < 0:
-            raise ValueError("%s: all tensors must be on one GPU device (got %s and %s)" % (name, tensors[0].device, t.device))
+        if t is not None and t.get_device() != index:
+            break
+    else:
+        t = tensors[0] if index < 0 else None
+    if t is not None:
+        raise ValueError("%s: all tensors must be on one GPU device (got %s and %s)" % (name, tensors[0].device, t.device))
     fn = _fns.get(name)
     if fn is None:
         fn = _fns[name] = getattr(lib(), name)
@@ -741,11 +750,6 @@ def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stre
     return C
 
 
-def _ld(name, t, shape):
-    """_mat of a tensor that is dense as a rule."""
-    return shape[1] if t.is_contiguous() and t.shape == shape else _mat(name, t, shape)
-
-
 def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
                    branch_scale, post_eps, eps):
     shape = x.shape
@@ -870,17 +874,19 @@ def kda_w4_expand(weight, out, stream=None):
 def kda_gemm_w4(x, weight, y, residual=None, stream=None):
     """y[M,N] = x[M,K] W^T (+ residual) from a W4Weight (bfloat16 x; y and the residual
     float32 or bfloat16; rows may be strided). residual may be y itself."""
-    M, K = x.shape
-    if K != weight.K:
-        raise ValueError("x must be [M, %d] (got %s)" % (weight.K, tuple(x.shape)))
-    shape = (M, weight.N)
+    xshape = x.shape
+    if len(xshape) != 2 or xshape[1] != weight.K:
+        raise ValueError("x must be [M, %d] (got %s)" % (weight.K, tuple(xshape)))
+    M, K = xshape
+    N = weight.N
+    shape = (M, N)
     pr, ldr, rd = None, 0, KDA_F32
     if residual is not None:
-        pr, ldr, rd = residual.data_ptr(), _mat("residual", residual, shape), _code(residual, "residual")
+        pr, ldr, rd = residual.data_ptr(), _ld("residual", residual, shape), _code(residual, "residual")
     packed = weight.packed
-    _call_on("kda_gemm_w4", (x, packed, y, residual), stream, x.data_ptr(), _mat("x", x, (M, K)), _code(x, "x"),
-             packed.data_ptr(), weight.group, weight.scale_code, 1 if weight.has_zeros else 0, pr, ldr, rd, y.data_ptr(),
-             _mat("y", y, shape), _code(y, "y"), M, weight.N, K)
+    _call_on("kda_gemm_w4", (x, packed, y, residual), stream, x.data_ptr(), K if x.is_contiguous() else _mat("x", x, xshape),
+             _code(x, "x"), packed.data_ptr(), weight.group, weight.scale_code, 1 if weight.has_zeros else 0, pr, ldr, rd,
+             y.data_ptr(), _ld("y", y, shape), _code(y, "y"), M, N, K)
     return y
 
 
@@ -942,24 +948,25 @@ def kda_beam_reorder(parents, state, conv_states=None, stream=None):
     """state[b, w] <- state[b, parents[b, w]] in place, and likewise every stream of
     conv_states. parents int32 [B, W]; state [B*W, ...] and conv_states [streams, B*W,
     ...] dense, of any dtype. A parent that is no beam leaves its row as it is."""
-    if parents.dim() != 2:
+    shape = parents.shape
+    if len(shape) != 2:
         raise ValueError("parents must be [B, W]")
-    B, W = parents.shape
-    _tensor("parents", parents, (B, W)), _type("parents", parents, torch.int32)
+    B, W = shape
     rows = B * W
-    if state.dim() < 1 or state.shape[0] != rows or not state.is_contiguous():
+    if not (parents.dtype is torch.int32 and parents.is_contiguous()):
+        _tensor("parents", parents, shape), _type("parents", parents, torch.int32)
+    if not state.is_contiguous() or state.dim() < 1 or state.shape[0] != rows:
         raise ValueError("state must be dense [%d, ...] for parents [%d, %d] (got %s)" % (rows, B, W, tuple(state.shape)))
-    nbytes = state.numel() * state.element_size()
     pc, streams, cbytes = None, 0, 0
     if conv_states is not None:
-        if conv_states.dim() < 2 or conv_states.shape[1] != rows or not conv_states.is_contiguous():
-            raise ValueError("conv_states must be dense [streams, %d, ...] (got %s)" % (rows, tuple(conv_states.shape)))
-        pc, streams = conv_states.data_ptr(), conv_states.shape[0]
-        cbytes = conv_states.numel() * conv_states.element_size()
+        cshape = conv_states.shape
+        if len(cshape) < 2 or cshape[1] != rows or not conv_states.is_contiguous():
+            raise ValueError("conv_states must be dense [streams, %d, ...] (got %s)" % (rows, tuple(cshape)))
+        pc, streams, cbytes = conv_states.data_ptr(), cshape[0], conv_states.nbytes
     if rows == 0:
         return state
     _call_on("kda_beam_reorder", (parents, state, conv_states), stream, parents.data_ptr(), B, W, state.data_ptr(),
-             nbytes // rows, pc, streams, cbytes // (rows * max(streams, 1)))
+             state.nbytes // rows, pc, streams, cbytes // (rows * (streams or 1)))
     return state
 
 
