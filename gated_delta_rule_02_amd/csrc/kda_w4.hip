@@ -129,7 +129,7 @@ __global__ __launch_bounds__(256) void w4_expand_kernel(W4ExpandArgs a, W4Layout
 // -(16 + z) twice, as bfloat16
 __device__ __forceinline__ uint32_t w4_zero_pair(uint32_t z) { return z * 0x00080008u + 0xc180c180u; }
 
-// What a lane reads of the scales or zero points of a tile: ROWS rows of GPT groups
+// BYTES of a lane's scales or zero points of a tile
 template <int BYTES>
 __device__ __forceinline__ void load_bytes(rsrc_t r, uint32_t off, uint32_t* w)
 {
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
     f32x4 tot[NT][MT] = {};
     for (int run = wave * DEPTH; run < col_tiles; run += waves * DEPTH) {
         u32x4_t c[DEPTH][NT];
-        uint32_t sw[DEPTH][NT][SB / 4], zw[DEPTH][NT][GPT > 4 ? GPT / 4 : 1];
+        uint32_t sw[DEPTH][NT][SB / 4], zw[DEPTH][NT][1];
         bf16x8 xf[DEPTH][4][MT];
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
