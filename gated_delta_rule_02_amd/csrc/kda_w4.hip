@@ -22,7 +22,7 @@
 //
 // Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 20 us, 4.3 TB/s. For
 // more, by the instructions of a column tile, since those of the vector unit find little room
-// beside the matrix instruction's with two wavefronts a SIMD: 64 rows 31 to 38 us (31 with
+// beside the matrix instruction's with two wavefronts a SIMD: 64 rows 30 to 36 us (30 with
 // part of the weights in the last-level cache), where each of a wavefront's turns takes 64
 // matrix and about 170 vector instructions, and the weights at a copy's rate 18 us.
 #include "kda_device.h"
@@ -187,119 +187,90 @@ __device__ __forceinline__ void store4(const W4GemmArgs& a, int64_t m, int64_t n
     }
 }
 
-// A workgroup takes NT row tiles of W and MT tiles of 16 rows of x; its wavefronts
-// deal the column tiles among themselves in runs of DEPTH, whose loads all go out
-// before the first is used, and their sums are joined in LDS in a fixed order.
-// Tiles beyond the last read as zero codes with zero scales.
-template <int MT, int NT, int DEPTH, int G, typename TS, bool ZEROS>
+// A workgroup takes a row tile of W and 16 rows of x; its wavefronts deal the column
+// tiles among themselves in runs of DEPTH, whose loads all go out before the first is
+// used, and their sums are joined in LDS in a fixed order. Tiles beyond the last read
+// as zero codes with zero scales.
+template <int DEPTH, int G, typename TS, bool ZEROS>
 __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
 {
-    extern __shared__ f32x4 part[];  // [wavefront][NT * MT][lane]
+    extern __shared__ f32x4 part[];  // [wavefront][lane]
     constexpr int STEPS = G / 32;    // matrix instructions per group
     constexpr int GPT = kTileCols / G;
     constexpr int SB = 4 * GPT * sizeof(TS);  // a lane's scales: the four rows of its results
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int col = lane % 16, quad = lane / 16;
-    const int64_t nt0 = (int64_t)blockIdx.x * NT, m0 = (int64_t)blockIdx.y * (MT * 16);
+    const int64_t nt = blockIdx.x, m0 = (int64_t)blockIdx.y * 16, at = nt * l.col_tiles;
     const int K = (int)a.K, col_tiles = (int)l.col_tiles;
-    const rsrc_t xr = make_rsrc(static_cast<const bf16_t*>(a.x) + m0 * a.x_ld,
-                                ((min(a.M - m0, (int64_t)MT * 16) - 1) * a.x_ld + a.K) * 2);
-    rsrc_t wr[NT], sr[NT], zr[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int64_t at = min(nt0 + n, l.row_tiles - 1) * l.col_tiles;
-        wr[n] = make_rsrc(a.packed + at * 1024, l.col_tiles * 1024);
-        sr[n] = make_rsrc(a.packed + l.scales + at * (16 * GPT * sizeof(TS)), l.col_tiles * (16 * GPT * sizeof(TS)));
-        if constexpr (ZEROS) zr[n] = make_rsrc(a.packed + l.zeros + at * (16 * GPT), l.col_tiles * (16 * GPT));
-    }
-    uint32_t xoff[MT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-        xoff[t] = m0 + t * 16 + col < a.M ? (uint32_t)(((t * 16 + col) * a.x_ld + quad * 8) * 2) : kNowhere;
+    const rsrc_t xr = make_rsrc(static_cast<const bf16_t*>(a.x) + m0 * a.x_ld, ((min(a.M - m0, (int64_t)16) - 1) * a.x_ld + a.K) * 2);
+    const rsrc_t wr = make_rsrc(a.packed + at * 1024, l.col_tiles * 1024);
+    const rsrc_t sr = make_rsrc(a.packed + l.scales + at * (16 * GPT * sizeof(TS)), l.col_tiles * (16 * GPT * sizeof(TS)));
+    const rsrc_t zr = make_rsrc(a.packed + l.zeros + at * (16 * GPT), ZEROS ? l.col_tiles * (16 * GPT) : 0);
+    const uint32_t xoff = m0 + col < a.M ? (uint32_t)((col * a.x_ld + quad * 8) * 2) : kNowhere;
 
     const W4Unpack unpack;
-    f32x4 tot[NT][MT] = {};
+    f32x4 tot = {};
     for (int run = wave * DEPTH; run < col_tiles; run += waves * DEPTH) {
-        u32x4_t c[DEPTH][NT];
-        uint32_t sw[DEPTH][NT][SB / 4], zw[DEPTH][NT][1];
-        bf16x8 xf[DEPTH][4][MT];
+        u32x4_t c[DEPTH];
+        uint32_t sw[DEPTH][SB / 4], zw[DEPTH][1];
+        bf16x8 xf[DEPTH][4];
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
             const int kc = run + d;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) c[d][n] = __builtin_amdgcn_raw_buffer_load_b128(wr[n], kc * 1024 + lane * 16, 0, 0);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                load_bytes<SB>(sr[n], kc * (SB * 4) + quad * SB, sw[d][n]);
-                if constexpr (ZEROS) load_bytes<GPT>(zr[n], (kc * 16 + col) * GPT, zw[d][n]);
-            }
+            c[d] = __builtin_amdgcn_raw_buffer_load_b128(wr, kc * 1024 + lane * 16, 0, 0);
+            load_bytes<SB>(sr, kc * (SB * 4) + quad * SB, sw[d]);
+            if constexpr (ZEROS) load_bytes<GPT>(zr, (kc * 16 + col) * GPT, zw[d]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int k = kc * kTileCols + i * 32;
                 const uint32_t k2 = k < K ? (uint32_t)k * 2 : kNowhere;  // K is a multiple of 32
-#pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    xf[d][i][t] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(xr, xoff[t] + k2, 0, 0));
+                xf[d][i] = __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(xr, xoff + k2, 0, 0));
             }
         }
         __builtin_amdgcn_sched_barrier(0);  // (the compiler would put the loads of x off until they are used)
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d)
 #pragma unroll
-            for (int g = 0; g < GPT; ++g)
+            for (int g = 0; g < GPT; ++g) {
+                f32x4 acc = {};
+                const uint32_t zp = ZEROS ? w4_zero_pair((zw[d][0] >> (8 * g)) & 255u) : 0xc1c0c1c0u;
+                const u32x4_t z4 = {zp, zp, zp, zp};
+                const bf16x8 zf = __builtin_bit_cast(bf16x8, z4);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 acc[MT] = {};
-                    const uint32_t zp = ZEROS ? w4_zero_pair((zw[d][n][0] >> (8 * g)) & 255u) : 0xc1c0c1c0u;
-                    const u32x4_t z4 = {zp, zp, zp, zp};
-                    const bf16x8 zf = __builtin_bit_cast(bf16x8, z4);
-#pragma unroll
-                    for (int i = g * STEPS; i < (g + 1) * STEPS; ++i) {
-                        const bf16x8 wf = unpack(c[d][n][i]);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, xf[d][i][t], acc[t], 0, 0, 0);
-                            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf, xf[d][i][t], acc[t], 0, 0, 0);
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float s = scale_at<TS>(sw[d][n], r * GPT + g);
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) tot[n][t][r] = fmaf(s, acc[t][r], tot[n][t][r]);
-                    }
+                for (int i = g * STEPS; i < (g + 1) * STEPS; ++i) {
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(unpack(c[d][i]), xf[d][i], acc, 0, 0, 0);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf, xf[d][i], acc, 0, 0, 0);
                 }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) tot[r] = fmaf(scale_at<TS>(sw[d], r * GPT + g), acc[r], tot[r]);
+            }
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) part[(wave * (NT * MT) + n * MT + t) * 64 + lane] = tot[n][t];
+    part[wave * 64 + lane] = tot;
     __syncthreads();
-    for (int i = wave; i < NT * MT; i += waves) {
-        f32x4 v = part[i * 64 + lane];
-        for (int j = 1; j < waves; ++j) {
-            const f32x4 o = part[(j * (NT * MT) + i) * 64 + lane];
+    if (wave > 0) return;
+    for (int j = 1; j < waves; ++j) {
+        const f32x4 o = part[j * 64 + lane];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] += o[r];
-        }
-        store4(a, m0 + i % MT * 16 + col, (nt0 + i / MT) * kTileRows + quad * 4, v);
+        for (int r = 0; r < 4; ++r) tot[r] += o[r];
     }
+    store4(a, m0 + col, nt * kTileRows + quad * 4, tot);
 }
 
 // More rows of x: what a compute unit takes in of x counts as much as the weights.
-// Four wavefronts with NT row tiles of W each share the x of a column tile in LDS,
-// copied there in the operands' order; two such groups take turns at the column
-// tiles. Copies and weights run two turns ahead. A group's sum of -24 x is formed once for
+// 8 / KW wavefronts with NT row tiles of W each share the x of a column tile in LDS,
+// copied there in whole lines; KW such groups take turns at the column tiles (four
+// instead of two where row tiles are few: 64 x 4096 x 8192 14.7 us instead of 20). Copies and weights run two turns ahead. A group's sum of -24 x is formed once for
 // the NT tiles and their products start from it; with zero points the sum of x is, and
 // they are applied to it in float32.
-template <int MT, int NT, int G, typename TS, bool ZEROS>
+template <int KW, int MT, int NT, int G, typename TS, bool ZEROS>
 __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
 {
-    constexpr int RW = 4, KW = 2, S = 3, kStage = MT * 4096;
+    constexpr int RW = 8 / KW, S = 3, kStage = MT * 4096;
+    constexpr int CP = MT * 4 / RW;  // copies of a wavefront per column tile
     constexpr int STEPS = G / 32, GPT = kTileCols / G, SB = 4 * GPT * sizeof(TS), ZB = 4 * GPT;
     // loads of a wavefront per column tile
-    constexpr int kLoads = MT + NT * (1 + (SB + 15) / 16 + (ZEROS ? 1 : 0));
-    static_assert(RW * NT * MT * 1024 <= KW * S * kStage, "the partial sums fit the stages");
+    constexpr int kLoads = CP + NT * (1 + (SB + 15) / 16 + (ZEROS ? 1 : 0));
+    static_assert((KW - 1) * RW * NT * MT * 1024 <= KW * S * kStage, "the partial sums fit the stages");
     static_assert(kLoads < 64, "loads the wait can count");
     __shared__ __attribute__((aligned(16))) uint8_t smem[KW * S * kStage];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -316,25 +287,32 @@ __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
         sr[n] = make_rsrc(a.packed + l.scales + at * (16 * GPT * sizeof(TS)), l.col_tiles * (16 * GPT * sizeof(TS)));
         if constexpr (ZEROS) zr[n] = make_rsrc(a.packed + l.zeros + at * (16 * GPT), l.col_tiles * (16 * GPT));
     }
-    // this wavefront copies step rw of the column tile for every tile of rows
-    uint32_t xoff[MT];
+    // A copy takes 8 rows of x and 64 columns, whole cache lines (16 rows of 32, an operand, would
+    // take in halves of twice as many); lane l row l / 8, and of its eight 16-byte pieces the one
+    // whose number, xored with the row's, is l % 8, so that an operand's reads meet all banks. Four
+    // copies a tile of rows: two columns of two.
+    uint32_t xoff[CP];
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
-        xoff[t] = m0 + t * 16 + col < a.M ? (uint32_t)(((t * 16 + col) * a.x_ld + quad * 8) * 2) : kNowhere;
+    for (int p = 0; p < CP; ++p) {
+        const int f = rw * CP + p, row = f / 4 * 16 + f % 4 / 2 * 8 + lane / 8;
+        xoff[p] = m0 + row < a.M ? (uint32_t)(row * a.x_ld * 2) : kNowhere;
+    }
+    const int xcol = ((lane ^ (lane / 8)) & 7) * 8;
+    const uint32_t xread = col / 8 * 2048 + col % 8 * 128 + ((quad ^ col) & 7) * 16;  // step 0; an odd one's: ^ 64
     uint8_t* ring = smem + kg * (S * kStage);
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)ring;
 
     u32x4_t c[S][NT];
     uint32_t sw[S][NT][SB / 4], zw[S][NT][ZB / 4];
-    // part p of MT + NT of a column tile's loads
+    // part p of CP + NT of a column tile's loads
     auto load = [&](int turn, int st, int p) {
-        const int kc = turn * KW + kg, k = kc * kTileCols + rw * 32;
-        if (p < MT) {
-            const uint32_t k2 = k < K ? (uint32_t)k * 2 : kNowhere;  // K is a multiple of 32
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(uintptr_t)(lds0 + st * kStage + (rw * MT + p) * 1024), 16,
-                                                     (int)(xoff[p] + k2), 0, 0, 0);
+        const int kc = turn * KW + kg;
+        if (p < CP) {
+            const int k = kc * kTileCols + (rw * CP + p) % 2 * 64 + xcol;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (lds_void*)(uintptr_t)(lds0 + st * kStage + (rw * CP + p) * 1024), 16,
+                                                     (int)(xoff[p] + (k < K ? (uint32_t)k * 2 : kNowhere)), 0, 0, 0);
         } else {
-            const int n = p - MT;
+            const int n = p - CP;
             c[st][n] = __builtin_amdgcn_raw_buffer_load_b128(wr[n], kc * 1024 + lane * 16, 0, 0);
             load_bytes<SB>(sr[n], kc * (SB * 4) + quad * SB, sw[st][n]);
             if constexpr (ZEROS) load_bytes<ZB>(zr[n], kc * (ZB * 4) + quad * ZB, zw[st][n]);
@@ -346,9 +324,9 @@ __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
 
     f32x4 tot[NT][MT] = {};
 #pragma unroll
-    for (int p = 0; p < MT + NT; ++p) load(0, 0, p);
+    for (int p = 0; p < CP + NT; ++p) load(0, 0, p);
 #pragma unroll
-    for (int p = 0; p < MT + NT; ++p) load(1, 1, p);
+    for (int p = 0; p < CP + NT; ++p) load(1, 1, p);
     // (so that the compiler has nothing left of these to wait for within the loop)
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     const W4Unpack unpack;
@@ -360,7 +338,7 @@ __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
         else __builtin_amdgcn_s_waitcnt(0x0f70 | (kLoads & 15) | ((kLoads >> 4) << 14));
         lds_barrier();  // everyone's; and every read of the stage refilled now is done
         __builtin_amdgcn_sched_barrier(0);
-        const uint8_t* lds = ring + st * kStage + lane * 16;
+        const uint8_t* lds = ring + st * kStage;
 #pragma unroll
         for (int g = 0; g < GPT; ++g) {
             bf16x8 xf[STEPS][MT];
@@ -369,7 +347,8 @@ __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
             for (int i = 0; i < STEPS; ++i)
 #pragma unroll
                 for (int t = 0; t < MT; ++t)
-                    xf[i][t] = __builtin_bit_cast(bf16x8, ld16(lds + ((g * STEPS + i) * MT + t) * 1024));
+                    xf[i][t] = __builtin_bit_cast(
+                        bf16x8, ld16(lds + t * 4096 + (g * STEPS + i) / 2 * 1024 + (xread ^ ((g * STEPS + i) % 2 * 64))));
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
 #pragma unroll
@@ -389,7 +368,7 @@ __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
                     // the compiler wait for all of them before it uses any.)
                     const int done = (g * NT + n) * STEPS + i;
 #pragma unroll
-                    for (int p = done * (MT + NT) / (4 * NT); p < (done + 1) * (MT + NT) / (4 * NT); ++p) {
+                    for (int p = done * (CP + NT) / (4 * NT); p < (done + 1) * (CP + NT) / (4 * NT); ++p) {
                         if (last) break;
                         load(turn + 2, (st + 2) % S, p);
                         __builtin_amdgcn_sched_barrier(0x38f);  // (what is no memory access may cross)
@@ -419,89 +398,103 @@ __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
     if (turn + 1 < turns) step(turn + 1, 1, true);
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the copies beyond the last column tile
     lds_barrier();                        // every wavefront has read its last stage
-    f32x4* part = reinterpret_cast<f32x4*>(smem) + rw * (NT * MT * 64) + lane;
-    if (kg == 1) {
+    f32x4* part = reinterpret_cast<f32x4*>(smem) + rw * (NT * MT * 64) + lane;  // of group 1, the others behind
+    if (kg > 0) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int t = 0; t < MT; ++t) part[(n * MT + t) * 64] = tot[n][t];
+            for (int t = 0; t < MT; ++t) part[((kg - 1) * RW * NT * MT + n * MT + t) * 64] = tot[n][t];
     }
     lds_barrier();
-    if (kg == 1) return;
+    if (kg > 0) return;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-            const f32x4 o = part[(n * MT + t) * 64];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) tot[n][t][r] += o[r];
+            for (int q = 1; q < KW; ++q) {
+                const f32x4 o = part[((q - 1) * RW * NT * MT + n * MT + t) * 64];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) tot[n][t][r] += o[r];
+            }
             store4(a, m0 + t * 16 + col, (nt0 + n) * kTileRows + quad * 4, tot[n][t]);
         }
 }
 
-template <int MT, int NT, int DEPTH, int G, typename TS, bool ZEROS>
+template <int DEPTH, int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_tiles(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
-    const int64_t blocks = (l.row_tiles + NT - 1) / NT;
     const int waves = (int)min((l.col_tiles + DEPTH - 1) / DEPTH, (int64_t)8);
-    const dim3 grid((unsigned)blocks, (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
-    hipLaunchKernelGGL((w4_gemm_kernel<MT, NT, DEPTH, G, TS, ZEROS>), grid, dim3(waves * 64), waves * NT * MT * 1024, s, a, l);
+    const dim3 grid((unsigned)l.row_tiles, (unsigned)((a.M + 15) / 16));
+    hipLaunchKernelGGL((w4_gemm_kernel<DEPTH, G, TS, ZEROS>), grid, dim3(waves * 64), waves * 1024, s, a, l);
     return hipGetLastError();
 }
 
-template <int MT, int NT, int G, typename TS, bool ZEROS>
+template <int KW, int MT, int NT, int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_rows(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
-    const dim3 grid((unsigned)((l.row_tiles + 4 * NT - 1) / (4 * NT)), (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
-    hipLaunchKernelGGL((w4_rows_kernel<MT, NT, G, TS, ZEROS>), grid, dim3(512), 0, s, a, l);
+    constexpr int TILES = 8 / KW * NT;
+    const dim3 grid((unsigned)((l.row_tiles + TILES - 1) / TILES), (unsigned)((a.M + MT * 16 - 1) / (MT * 16)));
+    hipLaunchKernelGGL((w4_rows_kernel<KW, MT, NT, G, TS, ZEROS>), grid, dim3(512), 0, s, a, l);
     return hipGetLastError();
 }
 
 // The form: the least of `start + rounds (tile + steps step)` us, with rounds of workgroups
 // over the 256 compute units and steps of a tile, column tiles (w4_gemm_kernel: a part of
-// a step follows the rows of x that there are) or turns at two of them. Fitted to
-// every form's time at 130 sizes (M 1..64, N 500..41,024, K 64..8,192, all groups and
-// types): off by 7 to 15 per cent, and the form picked on average 1 per cent above the
-// best (always the first: 4 per cent up to 16 rows, 20 beyond; at worst 2.8 times).
+// a step follows the rows of x that there are) or turns at KW of them; a part follows the bytes
+// of scales of a row of W in a column tile, and its zero points. The first form, which keeps
+// nothing in LDS, unless another is 5 per cent better. Fitted to every form's time at 190 sizes (M
+// 1..800, N 500..41,024, K 64..8,192, all groups and types): off by 7 to 12 per cent, and the form
+// picked on average 1 per cent above the best of up to eleven that were tried (up to 16 rows; from
+// 65 on 2.5), 38 at most. Always the first: 8 per cent up to 16 rows, 25 up to 64, 91 beyond, and at
+// worst 5.3 times.
 struct W4Form {
     int rows, row_tiles;  // of x and of W, per workgroup
-    bool turns;
-    int least;  // rows of x below which a smaller form does the same
-    float start, tile, step, step_rows;
+    int turns;            // column tiles that a workgroup takes at a time, 0: one
+    int least, most;      // rows of x: below, a smaller form does the same; above, a larger one nearly always better
+    float start, tile, step, step_rows, step_scales, step_zeros;
     float cost(const W4GemmArgs& a, const W4Layout& l) const
     {
         const int64_t tiles = ((l.row_tiles + row_tiles - 1) / row_tiles) * ((a.M + rows - 1) / rows);
-        const int64_t steps = turns ? (l.col_tiles + 1) / 2 : l.col_tiles;
-        const float fill = (float)min(a.M, (int64_t)rows) / (float)rows;
-        return start + (float)((tiles + 255) / 256) * (tile + (float)steps * (step + step_rows * fill));
+        const int64_t steps = turns ? (l.col_tiles + turns - 1) / turns : l.col_tiles;
+        const int groups = kTileCols / a.group, words = groups * (a.scale_dtype == F32 ? 2 : 1);
+        const float part = step_rows * (float)min(a.M, (int64_t)rows) / (float)rows + step_scales * (float)(words - 1) +
+                           (a.has_zeros ? step_zeros * (float)groups : 0.0f);
+        return start + (float)((tiles + 255) / 256) * (tile + (float)steps * (step + part));
     }
-};
-constexpr W4Form kForms[] = {
-    {16, 1, false, 0, 2.8f, 0.07f, 0.064f, 0.060f}, {32, 2, false, 17, 3.2f, 0.35f, 0.135f, 0.121f},
-    {16, 4, true, 0, 2.7f, 0.49f, 0.393f, 0.0f},    {32, 4, true, 17, 2.9f, 0.50f, 0.545f, 0.0f},
-    {32, 8, true, 17, 3.5f, 0.60f, 0.863f, 0.0f},   {32, 12, true, 17, 2.4f, 2.4f, 1.173f, 0.0f},
-    {64, 12, true, 33, 3.3f, 3.3f, 1.668f, 0.0f},
 };
 
 template <int G, typename TS, bool ZEROS>
 hipError_t launch_gemm_form(const W4GemmArgs& a, const W4Layout& l, hipStream_t s)
 {
+    // (float32 scales of groups of 32 take too many registers beside three tiles; bfloat16 ones
+    // with zero points keep nine in memory and still take 60 us where two tiles take 79, at 64 x
+    // 41,024 x 4096, since all their workgroups run at once)
+    constexpr int THREE = G == 32 && sizeof(TS) == 4 ? 2 : 3;
+    constexpr int ANY = 1 << 30;
+    constexpr W4Form kForms[] = {
+        {16, 1, 0, 0, ANY, 2.86f, 0.081f, 0.063f, 0.051f, 0.0f, 0.004f},
+        {16, 4, 2, 0, ANY, 2.91f, 0.386f, 0.307f, 0.0f, 0.024f, 0.033f},
+        {32, 4, 2, 17, ANY, 2.61f, 0.865f, 0.440f, 0.0f, 0.026f, 0.051f},
+        {16, 2, 4, 0, ANY, 2.89f, 0.428f, 0.328f, 0.0f, 0.026f, 0.029f},
+        {32, 2, 4, 17, ANY, 1.35f, 2.16f, 0.552f, 0.0f, 0.028f, 0.046f},
+        {32, THREE * 4, 2, 17, 32, 1.12f, 4.24f, 0.996f, 0.0f, -0.008f, 0.223f},
+        {64, THREE * 4, 2, 33, ANY, 0.0f, 7.22f, 1.555f, 0.0f, -0.050f, 0.269f},
+    };
     int best = 0;
     float least = kForms[0].cost(a, l);
     for (int f = 1; f < 7; ++f) {
-        const float c = kForms[f].cost(a, l);
-        if (a.M >= kForms[f].least && c < least) best = f, least = c;
+        const float c = kForms[f].cost(a, l) * 1.05f;
+        if (a.M >= kForms[f].least && a.M <= kForms[f].most && c < least) best = f, least = c;
     }
-    // (float32 scales of groups of 32 take too many registers beside three tiles)
-    constexpr int THREE = G == 32 && sizeof(TS) == 4 ? 2 : 3;
     switch (best) {
-    case 0: return launch_gemm_tiles<1, 1, 2, G, TS, ZEROS>(a, l, s);
-    case 1: return launch_gemm_tiles<2, 2, 2, G, TS, ZEROS>(a, l, s);
-    case 2: return launch_gemm_rows<1, 1, G, TS, ZEROS>(a, l, s);
-    case 3: return launch_gemm_rows<2, 1, G, TS, ZEROS>(a, l, s);
-    case 4: return launch_gemm_rows<2, 2, G, TS, ZEROS>(a, l, s);
-    case 5: return launch_gemm_rows<2, THREE, G, TS, ZEROS>(a, l, s);
-    default: return launch_gemm_rows<4, THREE, G, TS, ZEROS>(a, l, s);
+    case 0: return launch_gemm_tiles<2, G, TS, ZEROS>(a, l, s);
+    case 1: return launch_gemm_rows<2, 1, 1, G, TS, ZEROS>(a, l, s);
+    case 2: return launch_gemm_rows<2, 2, 1, G, TS, ZEROS>(a, l, s);
+    case 3: return launch_gemm_rows<4, 1, 1, G, TS, ZEROS>(a, l, s);
+    case 4: return launch_gemm_rows<4, 2, 1, G, TS, ZEROS>(a, l, s);
+    case 5: return launch_gemm_rows<2, 2, THREE, G, TS, ZEROS>(a, l, s);
+    default: return launch_gemm_rows<2, 4, THREE, G, TS, ZEROS>(a, l, s);
     }
 }
 

@@ -161,3 +161,23 @@ def test_forms_for_more_rows(M, N, k, G, sd, zeros):
     K.kda_gemm_w4(x, packed(dev), y)
     ref = torch.mm(x.double(), W.cuda().t().contiguous())
     assert torch.equal(y.double(), ref)
+
+
+@pytest.mark.parametrize("M,N,k,G,sd,zeros", [
+    # few row tiles and many column tiles, taken in turns of four with every remainder, and columns that end inside the last
+    (12, 8001, 4160, 64, BF, True), (5, 4999, 4128, 32, F, True), (16, 8000, 1184, 32, F, False), (9, 8000, 1920, 128, BF, False),
+    (28, 8100, 5152, 32, BF, True), (50, 4099, 8064, 128, F, True), (64, 4096, 8192, 64, BF, False), (40, 4010, 7072, 32, F, True),
+    # many row tiles and two or four tiles of rows
+    (31, 41024, 1216, 64, F, True), (32, 41000, 1056, 32, BF, False), (60, 40000, 704, 64, F, True),
+    # as many rows as several workgroups' and one more
+    (81, 12000, 352, 32, BF, False), (161, 1000, 4160, 64, F, True), (193, 9000, 1184, 32, BF, True)])
+def test_rows_beside_nan(M, N, k, G, sd, zeros):
+    """Exact sums (whole); NaN behind every row of x and behind the last one, which no copy may bring in."""
+    announce("gemm_w4 beside NaN %s" % ((M, N, k, G, sd, zeros),))
+    dev, W, _ = weight(N, k, G, sd, zeros, M + N + k, True)
+    x = torch.full((M + 3, k + 8), float("nan"), dtype=BF, device="cuda")
+    x[:M, :k] = torch.randint(-2, 3, (M, k), generator=torch.Generator().manual_seed(k)).to(BF).cuda()
+    y = torch.full((M + 2, N), float("nan"), device="cuda")
+    K.kda_gemm_w4(x[:M, :k], packed(dev), y[:M])
+    ref = torch.mm(x[:M, :k].double(), W.cuda().t().contiguous())
+    assert torch.equal(y[:M].double(), ref) and torch.isnan(y[M:]).all()
