@@ -20,7 +20,7 @@
 // the same float32 accumulators leaves the group's sum of x (c - z). The terms are at
 // most three times as large as x (c - z)'s own, so the sums lose less than two bits.
 //
-// Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 20 us, 4.3 TB/s. For
+// Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 21 us, 4.3 TB/s. For
 // more, by the instructions of a column tile, since those of the vector unit find little room
 // beside the matrix instruction's with two wavefronts a SIMD: 64 rows 30 to 36 us (30 with
 // part of the weights in the last-level cache), where each of a wavefront's turns takes 64
@@ -259,8 +259,9 @@ __global__ __launch_bounds__(512) void w4_gemm_kernel(W4GemmArgs a, W4Layout l)
 // More rows of x: what a compute unit takes in of x counts as much as the weights.
 // 8 / KW wavefronts with NT row tiles of W each share the x of a column tile in LDS,
 // copied there in whole lines; KW such groups take turns at the column tiles (four
-// instead of two where row tiles are few: 64 x 4096 x 8192 14.7 us instead of 20). Copies and weights run two turns ahead. A group's sum of -24 x is formed once for
-// the NT tiles and their products start from it; with zero points the sum of x is, and
+// instead of two where row tiles are few: 64 x 4096 x 8192 14.7 us instead of 17.5).
+// Copies and weights run two turns ahead. A group's sum of -24 x is formed once for the
+// NT tiles and their products start from it; with zero points the sum of x is, and
 // they are applied to it in float32.
 template <int KW, int MT, int NT, int G, typename TS, bool ZEROS>
 __global__ __launch_bounds__(512) void w4_rows_kernel(W4GemmArgs a, W4Layout l)
