@@ -85,7 +85,8 @@ int check_lower_bound(const char* fn, float lb, bool chunked)
 }
 
 // A launch holds less than 2^32 threads; the kernels that give a workgroup (of at
-// most 256) to a row, or a few to a tile of rows, take this many.
+// most 256; larger ones take the rows in several launches) to a row, or a few to a
+// tile of rows, take this many.
 constexpr int64_t kMaxRows = (int64_t)1 << 24;
 
 // cu_seqlens on the host: cu[0] = 0, non-decreasing, cu[N] = T.
@@ -677,7 +678,7 @@ static int sandwich_impl(const char* fn, const void* x, int64_t x_ld, kda_dtype 
     SandwichArgs a{x, x_ld, (DType)x_dtype, post_weight, gate, gate_ld, (DType)gate_dtype,
                    gate_activation == KDA_ACT_SIGMOID, residual_scale, branch_scale, post_eps, residual, residual_ld,
                    residual_out, residual_out_ld, (DType)residual_dtype, norm_weight, M, K, eps, y, y_ld,
-                   (DType)y_dtype, fp8 ? scales : nullptr, scale_ld};
+                   (DType)y_dtype, fp8 ? scales : nullptr, scale_ld, 0};
     return hip_status(launch_sandwich(a, static_cast<hipStream_t>(hip_stream)), fn);
 }
 

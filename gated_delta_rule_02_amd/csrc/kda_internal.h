@@ -248,6 +248,7 @@ struct SandwichArgs {
     DType y_dtype;
     float* scales;
     int64_t scale_ld;
+    int64_t row0;  // the first row of this launch (set by launch_sandwich)
 };
 hipError_t launch_sandwich(const SandwichArgs& a, hipStream_t s);
 

@@ -46,7 +46,7 @@ __device__ __forceinline__ void store8(T* p, const float* f)
     }
 }
 
-// Sum over the threads of one row (TPR = 64: a wavefront; 256: the workgroup).
+// Sum over the TPR threads of one row (64: a wavefront; more: the workgroup).
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* part)
 {
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void sandwich_kernel(Sandwic
     constexpr int THREADS = TPR > 256 ? TPR : 256;
     __shared__ float part[2][TPR / 64];
     const int t = threadIdx.x % TPR;
-    const int64_t m = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+    const int64_t m = a.row0 + (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
     if (m >= a.M) return;  // whole wavefronts (TPR = 64) leave; otherwise a workgroup has one row
     const TX* x = static_cast<const TX*>(a.x) + m * a.x_ld;
     float h[NV][8], r[NV][8], g[NV][8];
@@ -282,7 +282,7 @@ template <typename TX, typename TR, typename TG, typename TY, int GATE>
 __global__ __launch_bounds__(1024) void sandwich_wide_kernel(SandwichArgs a)
 {
     __shared__ float part[2][16];
-    const int64_t m = blockIdx.x;
+    const int64_t m = a.row0 + blockIdx.x;
     const TX* x = static_cast<const TX*>(a.x) + m * a.x_ld;
     float ss = 0.0f;
     for (int64_t c = threadIdx.x * 8; c < a.K; c += 8192) {
@@ -318,6 +318,20 @@ __global__ __launch_bounds__(1024) void sandwich_wide_kernel(SandwichArgs a)
     }
 }
 
+// launch(args, grid) for all rows, ROWS to a workgroup of THREADS. A launch holds less than
+// 2^32 threads, which rows of 512 and more pass below the row limit: calls that large go
+// out in several launches, each from its row0 on.
+template <int ROWS, int THREADS, typename Launch>
+hipError_t in_row_ranges(SandwichArgs a, Launch launch)
+{
+    constexpr int64_t MOST = ((int64_t)1 << 31) / THREADS * ROWS;
+    for (a.row0 = 0; a.row0 < a.M; a.row0 += MOST) {
+        launch(a, dim3((unsigned)((min(a.M - a.row0, MOST) + ROWS - 1) / ROWS)));
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // Few columns a thread, so that many rows are under way at once: us with THREADS x NV, rows of
 // bfloat16 (a gate of their own) 8191 x 4096 65.6 with 512 x 1, 68.0 with 256 x 2; 2000 x 8192
 // 38.3 with 512 x 2, 41.1 with 256 x 4; 2048 x 16,384 without a gate 55.9 with 1024 x 2, 79.9
@@ -326,9 +340,9 @@ template <typename TX, typename TR, typename TG, typename TY, int GATE, int TPR,
 hipError_t sandwich_launch(const SandwichArgs& a, hipStream_t s)
 {
     constexpr int THREADS = TPR > 256 ? TPR : 256;
-    const dim3 grid((unsigned)((a.M + THREADS / TPR - 1) / (THREADS / TPR)));
-    hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, TPR, NV>), grid, dim3(THREADS), 0, s, a);
-    return hipGetLastError();
+    return in_row_ranges<THREADS / TPR, THREADS>(a, [s](const SandwichArgs& part, dim3 grid) {
+        hipLaunchKernelGGL((sandwich_kernel<TX, TR, TG, TY, GATE, TPR, NV>), grid, dim3(THREADS), 0, s, part);
+    });
 }
 
 template <typename TX, typename TR, typename TG, typename TY, int GATE>
@@ -340,8 +354,9 @@ hipError_t sandwich_rows(const SandwichArgs& a, hipStream_t s)
     if (a.K <= 8192) return sandwich_launch<TX, TR, TG, TY, GATE, 512, 2>(a, s);
     if (a.K <= 16384) return sandwich_launch<TX, TR, TG, TY, GATE, 1024, 2>(a, s);
     if (a.K <= 32768) return sandwich_launch<TX, TR, TG, TY, GATE, 1024, 4>(a, s);
-    hipLaunchKernelGGL((sandwich_wide_kernel<TX, TR, TG, TY, GATE>), dim3((unsigned)a.M), dim3(1024), 0, s, a);
-    return hipGetLastError();
+    return in_row_ranges<1, 1024>(a, [s](const SandwichArgs& part, dim3 grid) {
+        hipLaunchKernelGGL((sandwich_wide_kernel<TX, TR, TG, TY, GATE>), grid, dim3(1024), 0, s, part);
+    });
 }
 
 template <typename TX, typename TR, typename TY>

@@ -147,3 +147,27 @@ def test_non_finite_rows_stay_in_their_rows():
     # a call of no rows
     e = torch.empty((0, 64), device="cuda")
     K.kda_sandwich_rmsnorm(e, torch.ones(64, device="cuda"), e, None, torch.ones(64, device="cuda"), torch.empty_like(e))
+
+
+@pytest.mark.parametrize("M,k", [((1 << 23) + 4099, 2176)])
+def test_more_rows_than_a_launch_holds(M, k):
+    """512 threads a row pass 2^32 threads at 2^23 rows: the rows beyond are as all others.
+    The rows repeat a block of 4096, whose results every block has to equal bit for bit."""
+    announce("sandwich_fp8 %d x %d" % (M, k))
+    if torch.cuda.mem_get_info()[0] < (70 << 30):
+        pytest.skip("takes 56 GB of device memory")
+    n = 4096
+    x, _, wp, w, gt = make(n, k, BF, BF, "vector", F, 0, 21)
+    want_q, want_s = torch.empty((n, k), dtype=torch.uint8, device="cuda"), torch.empty((n, k // 128), device="cuda")
+    K.kda_sandwich_rmsnorm_fp8(x, wp, x, None, w, want_q, want_s, gate=gt)
+    rows = torch.empty((M, k), dtype=BF, device="cuda")
+    for at in range(0, M, n):
+        rows[at:at + n] = x[:M - at]
+    q, s = torch.zeros((M, k), dtype=torch.uint8, device="cuda"), torch.zeros((M, k // 128), device="cuda")
+    K.kda_sandwich_rmsnorm_fp8(rows, wp, rows, None, w, q, s, gate=gt)  # (the residual's rows are x's)
+    whole = M // n * n
+    assert all(bool((t[:whole].view(-1, n, t.shape[1])[at:at + 64] == want).all())
+               for t, want in ((q, want_q), (s, want_s)) for at in range(0, M // n, 64))
+    assert torch.equal(q[whole:], want_q[:M - whole]) and torch.equal(s[whole:], want_s[:M - whole])
+    del rows, q, s
+    torch.cuda.empty_cache()
