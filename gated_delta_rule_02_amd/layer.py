@@ -339,7 +339,8 @@ class BeamSearch:
     row b * W + w is beam w of sequence b. `start` makes beam 0 of every sequence the
     one that lives (prefill its row; the first step spreads it over the others). After a
     step scores float32, parents (the beam followed), tokens int32 and finished bool
-    [B, W] hold the new beams, best first; they and `logits` are overwritten by the next."""
+    [B, W] hold the new beams, best first; they and `logits` [B * W, V] (its rows padded to a
+    multiple of 4, as the head's product asks) are overwritten by the next."""
 
     def __init__(self, blocks, norm_weight, head, B, W, eos, states, conv_states):
         self.blocks, self.norm_weight, self.head, self.eos = blocks, norm_weight, head, eos
@@ -348,7 +349,7 @@ class BeamSearch:
         V, width = head.shape
         self.scores, self.finished = new(B, W), new(B, W, dtype=torch.bool)
         self.parents, self.tokens = new(B, W, dtype=torch.int32), new(B, W, dtype=torch.int32)
-        self.logits, self.y = new(B * W, V), new(B * W, width, dtype=torch.bfloat16)
+        self.logits, self.y = new(B * W, (V + 3) // 4 * 4)[:, :V], new(B * W, width, dtype=torch.bfloat16)
         self.start()
 
     def start(self):

@@ -82,3 +82,12 @@ def test_beam_step_moves_every_blocks_states(calls, monkeypatch):
     assert names(tail) == ["kda_gemm_epilogue", "kda_beam_select", "kda_beam_reorder", "kda_beam_reorder"]
     assert tail[1][1][0] is s.logits and tail[1][1][1] is s.scores and tail[1][1][2] is s.scores
     assert [t[1][1] is st and t[1][2] is cv for t, st, cv in zip(tail[2:], sts, cvs)] == [True, True]
+
+
+@pytest.mark.parametrize("V", [40, 41, 42, 43])
+def test_logits_rows_suit_the_heads_product(calls, monkeypatch, V):
+    """kda_gemm_epilogue takes rows of y whose stride is a multiple of 4, whatever V is."""
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=torch.float32, device=None: torch.zeros(shape, dtype=dtype))
+    s = layer.BeamSearch([layer.KDABlock(mixer("bf16"), z(256))], z(256), bf(V, 256), 2, 3, -1, [z((6, H, 128, 128))],
+                         [bf(3, 6, 3, W)])
+    assert s.logits.shape == (6, V) and s.logits.stride(0) % 4 == 0 and s.logits.stride(1) == 1

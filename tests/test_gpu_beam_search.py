@@ -277,3 +277,30 @@ def test_ended_beams_stay():
         assert torch.equal(s.scores[:, 0], best) and bool(s.finished[:, 0].all())
         assert (s.tokens[:, 0] == V - 1).all()
         assert ((s.tokens == V - 1) <= s.finished).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "w4"])
+@pytest.mark.parametrize("vocabulary", [1, 61, 62, 63, 1027])
+def test_any_vocabulary(kind, vocabulary, monkeypatch):
+    """Vocabularies of no whole number of 4 tokens: the logits are y head^T (256 exact products, their
+    sum off by at most 2 u a term; from 4 bits 2 u (64 + 4 + 16) sum |s| |y| (32 + c + 8) with s <= 2^-8, c <=
+    15), and the beams those of a selection on dense logits."""
+    announce("beam search %s V=%d" % (kind, vocabulary))
+    monkeypatch.setitem(globals(), "V", vocabulary)
+    B, W = 2, 3
+    s, embed = search(kind, B, W, 110, eos=0)
+    head = s.head if kind == "bf16" else K.kda_w4_expand(s.head, torch.empty((vocabulary, WIDTH), dtype=BF, device="cuda"))
+    tokens = torch.zeros(B * W, dtype=torch.int64, device="cuda")
+    for step in range(3):
+        before, ended = s.scores.clone(), s.finished.clone()
+        s.step(embed[tokens].clone())
+        torch.cuda.synchronize()
+        y, w = s.y.double(), head.double().t().contiguous()
+        size = y.abs() @ w.abs() if kind == "bf16" else y.abs().sum(1, keepdim=True) * (55 / 256)
+        tol = 2 * U * (WIDTH + 8 if kind == "bf16" else 84) * size
+        assert ((s.logits.double() - y @ w).abs() <= tol).all()
+        out = [torch.empty_like(t) for t in (s.scores, s.parents, s.tokens, s.finished)]
+        K.kda_beam_select(s.logits.contiguous(), before, *out[:3], finished=ended, next_finished=out[3], eos=0)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, (s.scores, s.parents, s.tokens, s.finished)))
+        tokens = s.tokens.view(-1).long()
