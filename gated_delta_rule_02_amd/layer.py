@@ -340,9 +340,29 @@ class BeamSearch:
     one that lives (prefill its row; the first step spreads it over the others). After a
     step scores float32, parents (the beam followed), tokens int32 and finished bool
     [B, W] hold the new beams, best first; they and `logits` [B * W, V] (its rows padded to a
-    multiple of 4, as the head's product asks) are overwritten by the next."""
+    multiple of 4, as the head's product asks) are overwritten by the next. What does not
+    fit together is refused here or before a step's first call: a call refused in the middle
+    of a step would leave the states of the blocks before it advanced."""
 
     def __init__(self, blocks, norm_weight, head, B, W, eos, states, conv_states):
+        blocks, states, conv_states = list(blocks), list(states), list(conv_states)
+        if not blocks or len(states) != len(blocks) or len(conv_states) != len(blocks):
+            raise ValueError("a state and a history of every block, one block at least (got %d blocks, %d states, %d histories)" %
+                             (len(blocks), len(states), len(conv_states)))
+        if B < 0 or not 1 <= W <= 32:
+            raise ValueError("B >= 0 sequences of 1 to 32 beams (got %d, %d)" % (B, W))
+        if not isinstance(head, K.W4Weight):
+            K._type("head", head, torch.bfloat16)
+        if eos >= head.shape[0]:
+            raise ValueError("eos must be a token below %d, or negative: none (got %d)" % (head.shape[0], eos))
+        K._type("norm_weight", norm_weight, torch.float32), K._tensor("norm_weight", norm_weight, head.shape[1:])
+        for block, state, conv in zip(blocks, states, conv_states):
+            m = block.mixer
+            if m.hidden != head.shape[1]:
+                raise ValueError("the head is %d wide, a block %d" % (head.shape[1], m.hidden))
+            K._type("state", state, torch.float32), K._tensor("state", state, (B * W, m.H, D, D))
+            K._type("conv_states", conv, torch.bfloat16)
+            K._tensor("conv_states", conv, (3, B * W, m.conv[0].shape[1] - 1, m.W))
         self.blocks, self.norm_weight, self.head, self.eos = blocks, norm_weight, head, eos
         self.states, self.conv_states = states, conv_states
         new = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device="cuda")
@@ -360,6 +380,8 @@ class BeamSearch:
     def step(self, hidden):
         """hidden [B * W, width] (bfloat16 or float32, changed in place): the embeddings of
         the last step's tokens. Chooses the next ones and moves the beams' states."""
+        if hidden.shape != self.y.shape:  # fewer rows would advance some of the beams alone
+            raise ValueError("hidden must have shape %s (got %s)" % (tuple(self.y.shape), tuple(hidden.shape)))
         delta = None
         for block, state, conv in zip(self.blocks, self.states, self.conv_states):
             delta = block.decode(hidden, state, conv, delta)

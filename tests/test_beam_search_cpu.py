@@ -91,3 +91,33 @@ def test_logits_rows_suit_the_heads_product(calls, monkeypatch, V):
     s = layer.BeamSearch([layer.KDABlock(mixer("bf16"), z(256))], z(256), bf(V, 256), 2, 3, -1, [z((6, H, 128, 128))],
                          [bf(3, 6, 3, W)])
     assert s.logits.shape == (6, V) and s.logits.stride(0) % 4 == 0 and s.logits.stride(1) == 1
+
+
+def test_search_refuses_what_does_not_fit_together(calls, monkeypatch):
+    """Before anything is called: a step refused half-way would leave some states advanced."""
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=torch.float32, device=None: torch.zeros(shape, dtype=dtype))
+    block, st, cv = layer.KDABlock(mixer("bf16"), z(256)), z((6, H, 128, 128)), bf(3, 6, 3, W)
+
+    def search(**over):
+        a = dict(blocks=[block, block], norm_weight=z(256), head=bf(40, 256), B=2, W=3, eos=5, states=[st, st], conv_states=[cv, cv])
+        a.update(over)
+        return layer.BeamSearch(**a)
+
+    for bad in (dict(states=[st]), dict(conv_states=[cv]), dict(blocks=[block]), dict(blocks=[], states=[], conv_states=[]),
+                dict(states=[st, st[:5]]), dict(states=[st, z((8, H, 128, 128))]), dict(states=[st, z((6, H, 128, 256))[..., :128]]),
+                dict(conv_states=[cv, bf(3, 5, 3, W)]), dict(conv_states=[cv, bf(2, 6, 3, W)]), dict(conv_states=[cv, bf(3, 6, 2, W)]),
+                dict(W=33, B=1), dict(W=0), dict(B=-1), dict(eos=40), dict(head=bf(40, 128)), dict(norm_weight=z(255)),
+                dict(norm_weight=z(128), head=bf(40, 128))):
+        with pytest.raises(ValueError):
+            search(**bad)
+    for bad in (dict(states=[st, bf(6, H, 128, 128)]), dict(conv_states=[cv, z((3, 6, 3, W))]), dict(head=z((40, 256))),
+                dict(norm_weight=bf(256))):
+        with pytest.raises(TypeError):
+            search(**bad)
+    s = search(states=(st, st), eos=-1)
+    for hidden in (z((5, 256)), z((12, 256)), z((6, 128)), z(6 * 256)):
+        with pytest.raises(ValueError, match="hidden must have shape"):
+            s.step(hidden)
+    assert not calls
+    s.step(z((6, 256)))
+    assert names(calls)[-2:] == ["kda_beam_reorder"] * 2
