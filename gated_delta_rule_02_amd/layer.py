@@ -17,12 +17,22 @@ produces q|k|v|f|gate|b.
 """
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import torch
 
 from . import kda as K
 
 D = 128
+
+# The expansion of a 4-bit weight (a name for KDAMixer._buf): one buffer per device and
+# stream for all mixers, which their products use one after the other; one of each
+# mixer's own would hold a stack's weights in bfloat16 beside their four bits. The lock keeps
+# an expansion and its product together where host threads share a stream.
+EXPANDED = "expanded"
+_expanded = {}
+_expanding = threading.Lock()
 
 
 def _dev_bf16(t):
@@ -72,6 +82,13 @@ class KDAMixer:
         if stream:  # (nothing can be captured on the default stream, 0)
             if torch.cuda.is_current_stream_capturing():
                 return torch.empty(shape, dtype=dtype, device="cuda")
+        if name is EXPANDED:
+            n, key = shape.numel(), (self._device, stream)
+            b = _expanded.get(key)
+            if b is None or b.numel() < n:
+                b = _expanded[key] = torch.empty(n, dtype=dtype, device=torch.device("cuda", self._device))
+            return b[:n].view(shape)
+        if stream:
             name = (name, stream)
         b = self._bufs.get(name)
         if b is None or b.shape != shape or b.dtype is not dtype:
@@ -506,8 +523,9 @@ class KDAMixerW4(KDAMixer):
     """The same mixer with its projections in 4 bits (kda_w4_pack): W_in [5*H*128 + H (+
     zero rows to a multiple of 8), hidden] and Wo [hidden, H*128] are W4Weights. Below
     EXPAND rows (decode, draft trees, beams) the products read the packed weights; a
-    prefill expands them to bfloat16 in the mixer's scratch first (once a call: the
-    weights' roundings to bfloat16 are the difference between the two)."""
+    prefill expands each to bfloat16 before its product, in a scratch that all mixers of a
+    device and stream share (in every call anew: the weights' roundings to bfloat16 are the
+    difference between the two)."""
 
     # Rows from which expanding pays; direct | expanded, us: with 41,024 x 4096 weights 512
     # rows 219 | 296, 768 338 | 318, 1,024 433 | 415; with 4096 x 8192 80 | 88 for 768, 100 | 92
@@ -533,7 +551,9 @@ class KDAMixerW4(KDAMixer):
     def _product(self, x, w, y, residual=None):
         if x.shape[0] < self.EXPAND:
             return K.kda_gemm_w4(x, w, y, residual=residual)
-        return K.kda_gemm_epilogue(x, K.kda_w4_expand(w, self._buf("w%dx%d" % (w.N, w.K), w.shape, torch.bfloat16)), y, residual=residual)
+        with _expanding:
+            W = K.kda_w4_expand(w, self._buf(EXPANDED, w.shape, torch.bfloat16))
+            return K.kda_gemm_epilogue(x, W, y, residual=residual)
 
     def projections(self, x, tag=""):
         P = self._buf(tag + "P", (x.shape[0], self.W_in.N), torch.bfloat16)

@@ -304,3 +304,40 @@ def test_any_vocabulary(kind, vocabulary, monkeypatch):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, (s.scores, s.parents, s.tokens, s.finished)))
         tokens = s.tokens.view(-1).long()
+
+
+def test_mixers_share_the_expansion_of_their_weights():
+    """Prefills of several 4-bit mixers, in turn and on two streams, hold no weights in bfloat16
+    but one buffer a stream, as large as the largest weight, and equal the bfloat16 mixers'."""
+    pairs = [mixers(120), mixers(130)]
+    w, x = torch.ones(WIDTH, device="cuda"), [rows(150, 121), rows(170, 131)]
+    for a, _ in pairs:
+        a.EXPAND = 64
+
+    def run(m, h):
+        h = h.clone()
+        assert layer.KDABlock(m, w).forward(h) is None
+        return h
+
+    want = [run(b, h) for (_, b), h in zip(pairs, x)]
+    main, streams = torch.cuda.current_stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(main)
+    y = torch.empty((150, WIDTH), device="cuda")
+    with torch.cuda.stream(streams[0]):  # the smaller weight first: the buffer grows under work in flight
+        pairs[0][0]._product(x[0].to(BF), pairs[0][0].Wo, y)
+    got = []
+    for _ in range(3):
+        for i, (a, _) in enumerate(pairs):
+            got.append((i, run(a, x[i])))
+            for st in streams:
+                with torch.cuda.stream(st):
+                    got.append((i, run(a, x[i])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(h, want[i]) for i, h in got)
+    for a, _ in pairs:
+        held = [(b.shape, b.dtype) for b in a._bufs.values()]
+        assert (a.W_in.shape, BF) not in held and (a.Wo.shape, BF) not in held
+    device = torch.cuda.current_device()
+    for st in [main] + streams:
+        assert layer._expanded[device, st.cuda_stream].numel() >= pairs[0][0].W_in.N * WIDTH
