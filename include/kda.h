@@ -765,8 +765,9 @@ int kda_w4_expand(const void* packed, int64_t N, int64_t K, int group, kda_dtype
  * A beam that has ended (finished) offers its end token alone, at scores[b, w]: all
  * others at -inf. The W best of the W * V offers become the new beams, best first;
  * equal ones in the order of beam, then token. A beam's own offers are ordered by its
- * logits; those of different beams are compared in 64 bits, with logarithms whose sums
- * are off by about 1e-8 (the exponentials are float32).
+ * logits; those of different beams are compared in 64 bits, with logarithms that the
+ * float32 exponentials of their sums leave off by 1e-8 as a rule for thousands of tokens, by up
+ * to 2e-7 where a few hold the sum (measured).
  *   next_scores[b, i], parents[b, i] (the beam followed), tokens[b, i],
  *   next_finished[b, i] = the followed beam had ended, or the token is eos.
  * Logits of -inf are tokens that are not offered: like all offers of -inf they come

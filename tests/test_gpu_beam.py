@@ -255,3 +255,48 @@ def test_reorder_of_nothing():
     K.kda_beam_reorder(p, torch.empty((0, 8), device="cuda"))
     K.kda_beam_reorder(torch.zeros((2, 2), dtype=I32, device="cuda"), torch.empty((4, 0), device="cuda"),
                        torch.empty((0, 4, 8), device="cuda"))
+
+
+# ---------------------------------------------------------------- the logarithm
+# A score that cancels its offer shows the logarithm's error whole: next_scores is near 0, where
+# float32 is fine. Per term, u = 2^-24: x - m is rounded (u |x - m| of the value), the exponent (u of
+# it, u |x - m| again), the hardware exponential 2 u; the largest value so far changes at most once a step
+# and once between the lanes (each factor as a term: 2 u, and its distances add up to the term's own); 16
+# terms are summed in 5 roundings, everything later in 64 bits.
+def log_error(x, logs):
+    """Error of the kernel's logarithm of every row's sum of exponentials of x - max, given it in 64 bits."""
+    s = logs.float()[:, None].contiguous()
+    ns, p, t, _ = select(x, s)
+    return ns[:, 0].double() - (s[:, 0].double() - logs)
+
+
+@pytest.mark.parametrize("rows,V,std,dtype", [(300, 8, 1.0, F), (256, 1000, 1.0, BF), (256, 1000, 5.0, F), (128, 32000, 1.0, F),
+                                              (128, 32000, 2.5, BF), (5, 200003, 2.5, F)])
+def test_logarithm(rows, V, std, dtype):
+    announce("beam_select logarithm %s" % ((rows, V, std, dtype),))
+    x = inputs(rows, 1, V, dtype, rows + V, std)[0]
+    d = x.double().amax(1, keepdim=True) - x.double()
+    total = torch.exp(-d).sum(1)
+    mean = (torch.exp(-d) * d).sum(1) / total
+    steps = -(-V // 1024)
+    error = log_error(x, torch.log(total))
+    print("  mean %.1e, worst %.1e" % (float(error.mean()), float(error.abs().max())), flush=True)
+    assert (error.abs() <= (2 * mean + 7 + 2 * (steps + 1)) * U + 1e-13).all()
+
+
+def test_exponents_are_rounded_once():
+    """Rows of one distance d, at which float32's log2(e) gives a neighbour of the correctly rounded
+    exponent: that moves the logarithm by more than 8 u, and all other errors stay below 5 u."""
+    V, tops, log2e = 131072, 64, 1.4426950408889634
+    rounded = lambda v: float(torch.tensor(v, dtype=torch.float64).float())
+    logarithm = lambda exponent: math.log(tops + (V - tops) * 2.0 ** -exponent)
+    ds = [i / 32 for i in range(178, 256)]
+    ds = [d for d in ds if abs(logarithm(rounded(d * rounded(log2e))) - logarithm(rounded(d * log2e))) > 8 * U]
+    assert len(ds) >= 5
+    want = [logarithm(rounded(d * log2e)) for d in ds]
+    rows = 4096  # one part a row, whose first step has a largest value for every lane
+    x = (-torch.tensor(ds)).repeat(rows // len(ds) + 1)[:rows, None].to(BF).cuda().repeat(1, V)
+    x[:, :8 * tops:8] = 0
+    error = log_error(x, torch.tensor(want, dtype=torch.float64).repeat(rows // len(ds) + 1)[:rows].cuda())
+    print("  worst %.1f u" % (float(error.abs().max()) / U), flush=True)
+    assert (error.abs() <= 5 * U).all()
