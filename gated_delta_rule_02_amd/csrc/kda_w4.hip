@@ -17,8 +17,10 @@
 // A code becomes the number 16 + c, exact in bfloat16 with c in the upper
 // four bits of its mantissa: one shift and one and-or for two weights, and no
 // conversion. Adding -(16 + z) x, another product on the matrix instruction, into
-// the same float32 accumulators leaves the group's sum of x (c - z). The terms are at
-// most three times as large as x (c - z)'s own, so the sums lose less than two bits.
+// the same float32 accumulators leaves the group's sum of x (c - z). What is summed is up to
+// 31 |x| whatever c - z is, so an output is off by a part of sum |s| |x| (32 + c + z), not of its
+// own size: for uniform codes by 1.2e-7 (norm of all, 41,024 x 4096), for codes within 1 of the
+// zero point by 2e-7 to 6e-7, and codes at it throughout need not give exactly 0.
 //
 // Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 21 us, 4.3 TB/s. For
 // more, by the instructions of a column tile, since those of the vector unit find little room

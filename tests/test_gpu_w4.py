@@ -181,3 +181,27 @@ def test_rows_beside_nan(M, N, k, G, sd, zeros):
     K.kda_gemm_w4(x[:M, :k], packed(dev), y[:M])
     ref = torch.mm(x[:M, :k].double(), W.cuda().t().contiguous())
     assert torch.equal(y[:M].double(), ref) and torch.isnan(y[M:]).all()
+
+
+@pytest.mark.parametrize("M,N,k,G,sd,zeros", [(1, 500, 4096, 64, BF, True), (5, 700, 4096, 128, F, False), (1, 41024, 1024, 64, BF, True),
+                                              (40, 3000, 4096, 128, F, False), (64, 16000, 1024, 32, F, True)])
+def test_codes_near_their_zero_point(M, N, k, G, sd, zeros):
+    """Codes within 1 of the zero point, and rows at it throughout (W = 0): the sums of (16 + c) x and
+    (16 + z) x nearly cancel. The bound is that of any codes, in terms of what is summed."""
+    announce("gemm_w4 near the zero point %s" % ((M, N, k, G, sd, zeros),))
+    g = torch.Generator().manual_seed(N + k)
+    z = torch.randint(0, 16, (N, k // G), generator=g) if zeros else torch.full((N, k // G), 8)
+    zz = z.repeat_interleave(G, 1)
+    c = (zz + torch.randint(-1, 2, (N, k), generator=g)).clamp(0, 15)
+    c[::7] = zz[::7]
+    scales = ((torch.rand((N, k // G), generator=g) + 0.5) * 0.02).to(sd)
+    w = K.kda_w4_pack((c[:, 0::2] + 16 * c[:, 1::2]).to(torch.uint8).cuda(), scales.cuda(), z.to(torch.uint8).cuda() if zeros else None)
+    x = torch.randn((M, k), generator=g).to(BF).cuda()
+    y = torch.empty((M, N), device="cuda")
+    K.kda_gemm_w4(x, w, y)
+    s, c, zz = scales.cuda().double().repeat_interleave(G, 1), c.cuda().double(), zz.cuda().double()
+    ref = torch.mm(x.double(), (s * (c - zz)).t().contiguous())
+    tol = 2 * U * (G + k / G + 16) * torch.mm(x.double().abs(), (s * (32 + c + zz)).t().contiguous())
+    error = (y.double() - ref).abs()
+    print("  worst %.2e of the bound, off by %.1e of the norm" % (float((error / tol).max()), float(error.norm() / ref.norm())), flush=True)
+    assert (error <= tol).all()
