@@ -205,3 +205,39 @@ def test_codes_near_their_zero_point(M, N, k, G, sd, zeros):
     error = (y.double() - ref).abs()
     print("  worst %.2e of the bound, off by %.1e of the norm" % (float((error / tol).max()), float(error.norm() / ref.norm())), flush=True)
     assert (error <= tol).all()
+
+
+@pytest.mark.parametrize("M,N,k,G,zeros", [(1, 41024, 4096, 64, True), (5, 4999, 4128, 32, True), (64, 41024, 4096, 128, False),
+                                           (20, 4096, 8192, 128, False), (200, 8200, 1152, 64, True)])
+def test_calls_repeat_themselves(M, N, k, G, zeros):
+    """The same bits in every call: after other work, on two streams at once and from a graph."""
+    announce("gemm_w4 repeated %s" % ((M, N, k, G, zeros),))
+    g = torch.Generator(device="cuda").manual_seed(N)
+    codes = torch.randint(0, 256, (N, k // 2), generator=g, device="cuda", dtype=torch.uint8)
+    z = torch.randint(5, 11, (N, k // G), generator=g, device="cuda", dtype=torch.uint8) if zeros else None
+    w = K.kda_w4_pack(codes, ((torch.rand((N, k // G), generator=g, device="cuda") + 0.5) * 0.01).to(BF), z)
+    x = torch.randn((M, k), generator=g, device="cuda").to(BF)
+    new = lambda: torch.full((M, N), float("nan"), device="cuda")
+    want = new()
+    K.kda_gemm_w4(x, w, want)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    outs = [[new() for _ in range(6)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(6):
+        K.kda_gemm_w4(x, w, outs[0][i], stream=streams[0])
+        K.kda_gemm_w4(x, w, outs[1][i], stream=streams[1])
+        torch.empty(1 << 28, dtype=torch.uint8, device="cuda").fill_(i)  # (other lines in the caches)
+        K.kda_gemm_w4(x, w, outs[2][i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for row in outs for o in row)
+    graph, y = torch.cuda.CUDAGraph(), new()
+    with torch.cuda.stream(streams[0]), torch.cuda.graph(graph, stream=streams[0]):
+        K.kda_gemm_w4(x, w, y)
+    for i in range(3):
+        torch.cuda.synchronize()
+        y.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
