@@ -9,6 +9,7 @@ not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -894,7 +895,7 @@ def kda_beam_select_workspace_bytes(B, W, V):
     return lib().kda_beam_select_workspace_bytes(B, W, V)
 
 
-_beam_bytes = {}
+_beam_bytes = functools.lru_cache(maxsize=64)(kda_beam_select_workspace_bytes)
 
 
 def kda_beam_select(logits, scores, next_scores, parents, tokens, finished=None, next_finished=None, eos=-1,
@@ -933,10 +934,7 @@ def kda_beam_select(logits, scores, next_scores, parents, tokens, finished=None,
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError("workspace must be 'auto' or a tensor")
-        need = _beam_bytes.get((B, W, V))
-        if need is None:
-            need = _beam_bytes[(B, W, V)] = lib().kda_beam_select_workspace_bytes(B, W, V)
-        workspace = _workspace_on(logits, need, stream)
+        workspace = _workspace_on(logits, _beam_bytes(B, W, V), stream)
     pw, wbytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _call_on("kda_beam_select", (logits, scores, next_scores, parents, tokens, finished, next_finished, workspace), stream,
              logits.data_ptr(), ld, _code(logits, "logits"), scores.data_ptr(), pf, B, W, V, eos, next_scores.data_ptr(),

@@ -231,3 +231,10 @@ def test_binding_refuses_other_shapes_and_types():
         K.kda_beam_reorder(p, z((6, 8)), z((6, 3)))
     with pytest.raises(TypeError, match="parents"):
         K.kda_beam_reorder(p.long(), z((6, 8)))
+
+
+def test_sizes_kept_of_past_calls_are_bounded():
+    """A server's batches come in many sizes: what the binding keeps of them has an end."""
+    for B in range(1, 400):
+        assert K._beam_bytes(B, 4, 1000 + B) == K.kda_beam_select_workspace_bytes(B, 4, 1000 + B)
+    assert K._beam_bytes.cache_info().currsize <= 64
