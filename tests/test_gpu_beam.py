@@ -300,3 +300,22 @@ def test_exponents_are_rounded_once():
     error = log_error(x, torch.tensor(want, dtype=torch.float64).repeat(rows // len(ds) + 1)[:rows].cuda())
     print("  worst %.1f u" % (float(error.abs().max()) / U), flush=True)
     assert (error.abs() <= 5 * U).all()
+
+
+def test_rows_beyond_32_bits():
+    """More than 2^31 logits: the last sequences' rows lie past what 32-bit offsets reach."""
+    B, W, V = 271, 8, 1000003
+    announce("beam_select %d x %d x %d" % (B, W, V))
+    if torch.cuda.mem_get_info()[0] < (12 << 30):
+        pytest.skip("takes 5 GB of device memory")
+    few, s = inputs(3, W, V, BF, 50)
+    x = torch.zeros((B * W, V), dtype=BF, device="cuda")
+    at = (0, 134, B - 1)
+    for i, b in enumerate(at):
+        x[b * W:(b + 1) * W] = few[i * W:(i + 1) * W]
+    scores = torch.zeros((B, W), device="cuda")
+    scores[list(at)] = s
+    got, want = select(x, scores), select(few, s)  # in parts of other lengths: scores of up to 32 may round otherwise
+    for g, w in zip(got[:3], want[:3]):
+        assert torch.equal(g[list(at)], w) if g.dtype == I32 else ((g[list(at)] - w).abs() <= 4 * U * 32).all()
+    check(few, s)

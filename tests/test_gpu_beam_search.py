@@ -341,3 +341,36 @@ def test_mixers_share_the_expansion_of_their_weights():
     device = torch.cuda.current_device()
     for st in [main] + streams:
         assert layer._expanded[device, st.cuda_stream].numel() >= pairs[0][0].W_in.N * WIDTH
+
+
+@pytest.mark.parametrize("B,W", [(1, 2), (3, 4)])
+def test_search_over_a_stack_of_all_mixers(B, W):
+    """W8A8, 4-bit with a norm after it, bfloat16, W8A8 with a norm after it: every way in which a block
+    hands its output to the next. States and scores as in the tests above."""
+    announce("beam search over all mixers B=%d W=%d" % (B, W))
+    g = torch.Generator().manual_seed(140)
+    vec = lambda: (torch.rand(WIDTH, generator=g) + 0.5).cuda()
+    fp8 = lambda seed: layer.KDAMixerFP8.from_host(synth.workload_layer_fp8(T=4, hidden=WIDTH, H=H, seed=seed))
+    post = lambda: layer.BranchNorm(vec(), gate=vec(), gate_activation="sigmoid", branch_scale=0.7)
+    blocks = [layer.KDABlock(fp8(141), vec()), layer.KDABlock(mixers(142)[0], vec(), post=post()),
+              layer.KDABlock(mixers(143)[1], vec()), layer.KDABlock(fp8(144), vec(), post=post())]
+    embed, last, head = (torch.randn((V, WIDTH), generator=g) * 2).cuda(), vec(), w4(V, WIDTH, 145)[1]
+    sts = [states(B * W) for _ in blocks]
+    s = layer.BeamSearch(blocks, last, head, B, W, -1, [a for a, _ in sts], [c for _, c in sts])
+    first = [5 + b for b in range(B)]
+    paths = [[[first[b]] for _ in range(W)] for b in range(B)]
+    tokens = torch.tensor(first, device="cuda").repeat_interleave(W)
+    for step in range(4):
+        s.step(embed[tokens].clone())
+        torch.cuda.synchronize()
+        par, tok = s.parents.tolist(), s.tokens.tolist()
+        paths = [[paths[b][par[b][w]] + [tok[b][w]] for w in range(W)] for b in range(B)]
+        tokens = s.tokens.view(-1).long()
+    for b in range(B):
+        for w in range(W):
+            path, row = paths[b][w], b * W + w
+            logp, own = sequence_run(s, embed, path[:-1], B * W)
+            total = sum(logp[i][path[i + 1]] for i in range(len(path) - 1))
+            assert abs(float(s.scores[b, w]) - total) <= 4 * ((V / 64 + 330) * U + U * abs(total))
+            for (st, cv), mine, conv in zip(own, s.states, s.conv_states):
+                assert torch.equal(mine[row], st[row]) and torch.equal(conv[:, row], cv[:, row])
