@@ -754,8 +754,8 @@ def kda_gemm_epilogue(A, B, C, bias=None, activation="none", residual=None, stre
 def _sandwich_args(x, post_weight, residual, residual_out, norm_weight, gate, gate_activation, residual_scale,
                    branch_scale, post_eps, eps):
     shape = x.shape
-    if len(shape) != 2:
-        raise ValueError("x must be [M, K]")
+    if len(shape) != 2 or residual is None:
+        raise ValueError("x must be [M, K], and residual given")
     M, K = shape
     act, rd, wshape = ACTIVATIONS.get(gate_activation), residual.dtype, shape[1:]
     dense = (x.is_contiguous() and residual.is_contiguous() and residual.shape == shape and

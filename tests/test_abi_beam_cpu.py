@@ -238,3 +238,9 @@ def test_sizes_kept_of_past_calls_are_bounded():
     for B in range(1, 400):
         assert K._beam_bytes(B, 4, 1000 + B) == K.kda_beam_select_workspace_bytes(B, 4, 1000 + B)
     assert K._beam_bytes.cache_info().currsize <= 64
+
+
+def test_norms_around_a_block_need_a_residual():
+    x, w = torch.zeros((2, 64)), torch.zeros(64)
+    with pytest.raises(ValueError, match="residual"):
+        K.kda_sandwich_rmsnorm(x, w, None, None, w, torch.zeros((2, 64)))
