@@ -6,9 +6,9 @@
 // an ended one offers its end token alone, at S_w. The W best of the W V offers,
 // equal ones by lower beam, then lower token, are the new beams.
 //
-// Bound by HBM, one read of the logits: 64 x 8 beams over 131,072 float32 logits 58 us, 4.6
-// TB/s. Small calls by the chain of a step and a joining: 4 beams over 32,000 logits 3.4 and
-// 4.6 us in two launches, 7 us in one for 4 over 1000. A wavefront runs along a part of a row
+// Bound by HBM, one read of the logits of the beams that have not ended: 64 x 8 beams over 131,072
+// float32 logits 66 us, 4.1 TB/s. Small calls by the chain of a step and a joining: 4 beams
+// over 32,000 logits 4.5 and 4.9 us in two launches, 8 us in one for 4 over 1000. A wavefront runs along a part of a row
 // with the running maximum and sum of the softmax in each lane and the part's W best
 // values in order across its lanes (value and token, lane i the i-th): a step of
 // 1024 logits costs one comparison of the lanes' maxima with the W-th best, and only

@@ -22,7 +22,7 @@
 // own size: for uniform codes by 1.2e-7 (norm of all, 41,024 x 4096), for codes within 1 of the
 // zero point by 2e-7 to 6e-7, and codes at it throughout need not give exactly 0.
 //
-// Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 21 us, 4.3 TB/s. For
+// Bound by HBM (N K / 2 bytes of codes) for one row: 41,024 x 4096 in 20 us, 4.3 TB/s. For
 // more, by the instructions of a column tile, since those of the vector unit find little room
 // beside the matrix instruction's with two wavefronts a SIMD: 64 rows 30 to 36 us (30 with
 // part of the weights in the last-level cache), where each of a wavefront's turns takes 64
