@@ -241,3 +241,19 @@ def test_calls_repeat_themselves(M, N, k, G, zeros):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+def test_packed_expanded_and_used_on_another_stream():
+    """All three calls with stream=, none on the current one: the same bits."""
+    dev, _, _ = weight(500, 1024, 64, BF, True, 31)
+    x = torch.randn((20, 1024), generator=torch.Generator().manual_seed(32)).to(BF).cuda()
+    w = packed(dev)
+    want, wide = torch.empty((20, 500), device="cuda"), torch.empty((500, 1024), dtype=BF, device="cuda")
+    K.kda_gemm_w4(x, w, want), K.kda_w4_expand(w, wide)
+    y, other = torch.empty_like(want), torch.empty_like(wide)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    w2 = K.kda_w4_pack(*dev, stream=st)
+    K.kda_gemm_w4(x, w2, y, stream=st), K.kda_w4_expand(w2, other, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(w2.packed, w.packed) and torch.equal(y, want) and torch.equal(other, wide)
